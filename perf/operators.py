@@ -9,7 +9,7 @@
 
 The cache is [num_pages, Hkv, page, D]; position p of sequence b lies in page block_table[b, p // page] at row
 p % page.  An E4M3 cache holds code * 2^e with one e for each token and head (E8M0, [num_pages, Hkv, page]): the
-least e >= -120 with amax <= 448 * 2^e over the row's finite values.
+least e >= -120 with amax <= 448 * 2^e; a row that is not finite has the E8M0 NaN, and codes 0.
 """
 import math
 import random
@@ -135,14 +135,15 @@ def _pow2(e):
 
 def _quantise(x):
     """Rows of x (fp32, last axis) as (E4M3 codes, exponents): x ~ code * 2^e."""
-    finite = torch.isfinite(x)
-    amax = torch.where(finite, x.abs(), 0.0).amax(-1)
+    finite = torch.isfinite(x).all(-1)
+    x = torch.where(finite[..., None], x, 0.0)
+    amax = x.abs().amax(-1)
     m, k = torch.frexp(amax)  # amax = m 2^k, m in [1/2, 1): 448 = 7/8 2^9
     e = (k - 9 + (m > 0.875)).clamp(min=-120)
     e = torch.where(amax > 0, e, torch.full_like(e, -120))
     y = x * _pow2(-e)[..., None]
     top = torch.where(e >= 120, 240.0, 448.0)[..., None]  # 256 * 2^120 is infinite in bf16
-    return torch.maximum(torch.minimum(y, top), -top).to(_F8), e
+    return torch.maximum(torch.minimum(y, top), -top).to(_F8), torch.where(finite, e, torch.full_like(e, 128))
 
 
 def _e8(e):
