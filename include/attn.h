@@ -2,7 +2,10 @@
  * attn.h -- C ABI of the B200 (sm_100a) attention library: the forward pass in bf16
  * (attn_fwd, attn_fwd_ws, attn_fwd_noalloc; attn_fwd_from_host on host buffers) and E4M3
  * (attn_fwd_fp8), its gradients (attn_bwd), and rotary position embedding of Q and K
- * (attn_rope_tables, attn_rope_qk, attn_fwd_rope; their backward attn_rope_qk_inverse, attn_bwd_rope).
+ * (attn_rope_tables, attn_rope_qk, attn_fwd_rope; their backward attn_rope_qk_inverse, attn_bwd_rope);
+ * a paged key/value cache, bf16 or quantised (attn_cache_append, attn_cache_read), the attention of
+ * new tokens over it (attn_fwd_decode; behind a prefix that the batch shares,
+ * attn_fwd_shared_prefix), and attention to keys of another length (attn_fwd_cross).
  *
  * The operation is the tiled attention forward pass named by "HipKittens:
  * fast and furious AMD kernels" (section "Performance results": an attention
@@ -370,6 +373,120 @@ int attn_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* ls
                  int B, int Hq, int Hkv, int N, int D, int causal, float scale,
                  float q_descale, float k_descale, float v_descale,
                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Paged key/value cache.
+ *
+ * Layout (DEVICE memory, caller-owned), shared by the entry points below:
+ *   k_cache, v_cache  [num_pages, Hkv, page_size, D], contiguous, 16-byte aligned: bf16, or E4M3
+ *                     bytes when k_scale and v_scale are given.
+ *   k_scale, v_scale  E4M3 caches: E8M0 bytes [num_pages, Hkv, page_size], contiguous, 16-byte
+ *                     aligned; a stored value is code * 2^(byte - 127).  Null for a bf16 cache.
+ *   block_table       int32 [B, max_pages]: position p of sequence b is row p % page_size of page
+ *                     block_table[b][p / page_size].
+ *   lens              int32 [B]: positions of each sequence.  Values below 0 count as 0, values above
+ *                     max_pages * page_size as that.
+ *   D is 32, 64, 96 or 128, page_size a positive multiple of 16 (else ATTN_ERR_UNSUPPORTED),
+ *   num_pages >= 1, max_pages >= 0, num_pages * Hkv <= 2^31-1.
+ * Tables and lengths are read on the device when the kernels run, so captured calls see their
+ * values at replay.  A table entry outside [0, num_pages) is no page: nothing is written there, and
+ * it reads as zeros.  Host checks and errors as in attn_fwd: ATTN_ERR_INVALID_ARG (null pointers,
+ * negative sizes, one scale without the other), ATTN_ERR_MISALIGNED, ATTN_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------------------------ */
+
+/*
+ * attn_cache_append -- write new keys and values behind those a cache holds, quantising on the way.
+ *   k, v       bf16 [B, Hkv, T, D], contiguous, 16-byte aligned.                      read
+ *   lens       row t of sequence b goes to position lens[b] + t (lens itself stays as it is; a
+ *              position below 0 or past the table is not written).
+ *   new_lens   int32 [B] or null: only rows t < new_lens[b] are written; null: all T.
+ *   Limits: B * Hkv * T < 2^32.  B == 0 or T == 0: ATTN_OK, nothing is launched.
+ * Numerics, E4M3: per row, with amax its largest magnitude, e is the least integer >= -120 with
+ * amax <= 448 * 2^e and each code the E4M3 number nearest to x * 2^-e (ties to even; at most 240 in
+ * magnitude for e = 120, so that the value stays finite in bf16).  A row with an infinity or a NaN
+ * is stored as codes 0 with the E8M0 NaN (byte 255) and reads as NaN.
+ * Two rows of one call must not have the same place (the table's entries of positions being
+ * written are distinct); if they do, either may remain.
+ */
+int attn_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                      const int* block_table, const int* lens, const int* new_lens, int B, int Hkv, int T, int D,
+                      int num_pages, int page_size, int max_pages, void* stream);
+
+/*
+ * attn_cache_read -- positions [0, N) of every sequence, back as contiguous rows.
+ *   k, v       bf16 [B, Hkv, N, D], contiguous, 16-byte aligned.   written (every element: zeros at
+ *              positions >= lens[b], outside the table and where it names no page)
+ *   Limits: B * Hkv * N < 2^32.  E4M3 values are bf16 numbers exactly (of exponent bytes 7..247, as
+ *   attn_cache_append writes them): nothing is rounded.
+ */
+int attn_cache_read(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                    const int* block_table, const int* lens, void* k, void* v, int B, int Hkv, int N, int D,
+                    int num_pages, int page_size, int max_pages, void* stream);
+
+/*
+ * attn_fwd_decode -- attention of the last T tokens of each sequence over its cache.
+ *   q          bf16 [B, Hq, T, D], contiguous, 16-byte aligned.                        read
+ *   lens       positions of each sequence, the T tokens' own (already appended) among them: token t
+ *              stands at position lens[b] - T + t and sees the positions up to its own.
+ *   o, lse     bf16 [B, Hq, T, D] and fp32 [B, Hq, T], as attn_fwd; a row that sees no position has
+ *              o = 0 and lse = -infinity.                                  written (every element)
+ *   workspace  device pointer, 256-byte aligned, of at least attn_fwd_decode_workspace_bytes() bytes
+ *              (which may be 0); no initialisation; calls sharing it must be ordered.
+ * Any T >= 0 (T == 0 or B == 0: ATTN_OK, nothing launched), made for few rows: a KV head's keys are
+ * read once for each 64 of its T * Hq / Hkv rows.  Further limits (ATTN_ERR_UNSUPPORTED): fewer than
+ * 2^31 rows a KV head over the batch, and as many 16-row tiles.
+ * Numerics as attn_fwd (probabilities times the value's scale rounded to bf16).  E4M3 NaN codes,
+ * which attn_cache_append never writes, count as +-480.  Deterministic; the split of a sequence
+ * over the GPU, and with it the fp32 order of its sums, depends on all the batch's lengths.
+ */
+int attn_fwd_decode(const void* q, const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                    const int* block_table, const int* lens, void* o, float* lse, int B, int Hq, int Hkv, int T,
+                    int D, int num_pages, int page_size, int max_pages, float scale, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Workspace attn_fwd_decode needs on the current device; -1 on sizes it rejects or a CUDA error. */
+long long attn_fwd_decode_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int page_size, int max_pages);
+
+/*
+ * attn_fwd_shared_prefix -- attn_fwd_decode for a batch whose sequences start with one prefix.
+ *   prefix_table  int32 [ceil(prefix_len / page_size)]: the prefix's pages, held once.
+ *   prefix_len    positions of the prefix, >= 0; every row sees all of them.
+ *   block_table, lens   each sequence's own positions, behind the prefix; seen as in attn_fwd_decode.
+ * o and lse are those of the softmax over the prefix's and the row's own positions together.  The
+ * prefix is read once for up to 128 rows of a KV head (B * T * Hq / Hkv of them).  All other
+ * arguments, limits, errors and numerics as attn_fwd_decode; workspace of at least
+ * attn_fwd_shared_prefix_workspace_bytes() bytes.
+ */
+int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
+                           const void* v_scale, const int* prefix_table, int prefix_len, const int* block_table,
+                           const int* lens, void* o, float* lse, int B, int Hq, int Hkv, int T, int D, int num_pages,
+                           int page_size, int max_pages, float scale, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/* Workspace attn_fwd_shared_prefix needs on the current device; -1 on rejected sizes or a CUDA error. */
+long long attn_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int page_size, int max_pages,
+                                                 int prefix_len);
+
+/*
+ * attn_fwd_cross -- attention to keys of another length (a decoder's to an encoder's states).
+ *   q          bf16 [B, Hq,  Nq, D], contiguous, 16-byte aligned.                      read
+ *   k, v       bf16 [B, Hkv, Nk, D], contiguous, 16-byte aligned.                      read
+ *   k_lens     int32 [B] on the device, or null: the first k_lens[b] positions of batch row b are its
+ *              keys (clamped to [0, Nk]); what lies behind them is not used and may hold anything,
+ *              infinities and NaN included.  Null: all Nk.
+ *   o, lse     bf16 [B, Hq, Nq, D] and fp32 [B, Hq, Nq]; rows without a key have o = 0 and
+ *              lse = -infinity.                                          written (every element)
+ *   Nq, Nk >= 0; D is 32, 64, 96 or 128.  B == 0 or Nq == 0: ATTN_OK, nothing launched.  Limits
+ *   (ATTN_ERR_UNSUPPORTED): Nq * Hq / Hkv <= 2^30 and fewer than 2^31 16-row tiles.
+ *   workspace  device pointer, 256-byte aligned, of at least attn_fwd_cross_workspace_bytes() bytes.
+ * Errors and numerics as attn_fwd; deterministic.
+ */
+int attn_fwd_cross(const void* q, const void* k, const void* v, const int* k_lens, void* o, float* lse, int B, int Hq,
+                   int Hkv, int Nq, int Nk, int D, float scale, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/* Workspace attn_fwd_cross needs on the current device; -1 on rejected sizes or a CUDA error. */
+long long attn_fwd_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D);
 
 /* Human-readable name of an attn_status_t value (static string, never null). */
 const char* attn_status_string(int status);

@@ -18,3 +18,12 @@ from .attn_ref import (  # noqa: F401
     rope_rotate,
     rope_rotate_transpose,
 )
+from .kv_ref import (  # noqa: F401
+    attend,
+    cross_backward,
+    e8_value,
+    gather,
+    page_row,
+    quantise_row,
+    round_e4m3,
+)

@@ -30,6 +30,10 @@ __all__ = [
     "backward_from_host", "attn_rope_qk", "attn_fwd_rope", "attn_fwd_rope_workspace_bytes", "rope_tables",
     "rope", "forward_rope", "attn_fwd_fp8", "forward_fp8", "attn_rope_qk_inverse", "attn_bwd_rope",
     "attn_bwd_rope_workspace_bytes", "rope_inverse", "backward_rope",
+    "attn_cache_append", "attn_cache_read", "attn_fwd_decode", "attn_fwd_decode_workspace_bytes",
+    "attn_fwd_shared_prefix", "attn_fwd_shared_prefix_workspace_bytes", "attn_fwd_cross",
+    "attn_fwd_cross_workspace_bytes", "cache_append", "cache_read", "forward_decode", "forward_shared_prefix",
+    "forward_cross",
 ]
 
 ATTN_OK = 0
@@ -98,6 +102,22 @@ def _load() -> ctypes.CDLL:
     L.attn_rope_tables.restype = i
     L.attn_fwd_noalloc_scratch_bytes.argtypes = []
     L.attn_fwd_noalloc_scratch_bytes.restype = ctypes.c_size_t
+    L.attn_cache_append.argtypes = [vp] * 9 + [i] * 7 + [vp]
+    L.attn_cache_append.restype = i
+    L.attn_cache_read.argtypes = [vp] * 8 + [i] * 7 + [vp]
+    L.attn_cache_read.restype = i
+    L.attn_fwd_decode.argtypes = [vp] * 9 + [i] * 8 + [f, vp, ctypes.c_size_t, vp]
+    L.attn_fwd_decode.restype = i
+    L.attn_fwd_decode_workspace_bytes.argtypes = [i] * 7
+    L.attn_fwd_decode_workspace_bytes.restype = ctypes.c_longlong
+    L.attn_fwd_shared_prefix.argtypes = [vp] * 6 + [i] + [vp] * 4 + [i] * 8 + [f, vp, ctypes.c_size_t, vp]
+    L.attn_fwd_shared_prefix.restype = i
+    L.attn_fwd_shared_prefix_workspace_bytes.argtypes = [i] * 8
+    L.attn_fwd_shared_prefix_workspace_bytes.restype = ctypes.c_longlong
+    L.attn_fwd_cross.argtypes = [vp] * 6 + [i] * 6 + [f, vp, ctypes.c_size_t, vp]
+    L.attn_fwd_cross.restype = i
+    L.attn_fwd_cross_workspace_bytes.argtypes = [i] * 6
+    L.attn_fwd_cross_workspace_bytes.restype = ctypes.c_longlong
     L.attn_status_string.argtypes = [i]
     L.attn_status_string.restype = ctypes.c_char_p
     L.attn_last_cuda_error.argtypes = []
@@ -206,6 +226,55 @@ def attn_bwd_rope(q, k, v, cos_t, sin_t, o, lse, dout, dq, dk, dv, B, Hq, Hkv, N
 
 def attn_bwd_rope_workspace_bytes(B: int, Hq: int, Hkv: int, N: int, D: int) -> int:
     return lib.attn_bwd_rope_workspace_bytes(B, Hq, Hkv, N, D)
+
+
+def attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, lens, new_lens, B, Hkv, T, D, num_pages,
+                      page_size, max_pages, stream) -> int:
+    """Direct call of the cache append entry point (device pointers and stream as integers)."""
+    return lib.attn_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, lens, new_lens, B, Hkv, T, D,
+                                 num_pages, page_size, max_pages, stream)
+
+
+def attn_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, k, v, B, Hkv, N, D, num_pages, page_size,
+                    max_pages, stream) -> int:
+    """Direct call of the cache read entry point (device pointers and stream as integers)."""
+    return lib.attn_cache_read(k_cache, v_cache, k_scale, v_scale, block_table, lens, k, v, B, Hkv, N, D, num_pages,
+                               page_size, max_pages, stream)
+
+
+def attn_fwd_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o, lse, B, Hq, Hkv, T, D, num_pages,
+                    page_size, max_pages, scale, workspace, workspace_bytes, stream) -> int:
+    """Direct call of the decode entry point (pointers, sizes and stream as integers)."""
+    return lib.attn_fwd_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, o, lse, B, Hq, Hkv, T, D,
+                               num_pages, page_size, max_pages, float(scale), workspace, workspace_bytes, stream)
+
+
+def attn_fwd_decode_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, page_size: int, max_pages: int) -> int:
+    return lib.attn_fwd_decode_workspace_bytes(B, Hq, Hkv, T, D, page_size, max_pages)
+
+
+def attn_fwd_shared_prefix(q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_len, block_table, lens, o, lse,
+                           B, Hq, Hkv, T, D, num_pages, page_size, max_pages, scale, workspace, workspace_bytes,
+                           stream) -> int:
+    """Direct call of the shared-prefix entry point (pointers, sizes and stream as integers)."""
+    return lib.attn_fwd_shared_prefix(q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_len, block_table,
+                                      lens, o, lse, B, Hq, Hkv, T, D, num_pages, page_size, max_pages, float(scale),
+                                      workspace, workspace_bytes, stream)
+
+
+def attn_fwd_shared_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, page_size: int, max_pages: int,
+                                           prefix_len: int) -> int:
+    return lib.attn_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, T, D, page_size, max_pages, prefix_len)
+
+
+def attn_fwd_cross(q, k, v, k_lens, o, lse, B, Hq, Hkv, Nq, Nk, D, scale, workspace, workspace_bytes, stream) -> int:
+    """Direct call of the cross-attention entry point (pointers, sizes and stream as integers)."""
+    return lib.attn_fwd_cross(q, k, v, k_lens, o, lse, B, Hq, Hkv, Nq, Nk, D, float(scale), workspace,
+                              workspace_bytes, stream)
+
+
+def attn_fwd_cross_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, D: int) -> int:
+    return lib.attn_fwd_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, D)
 
 
 def attn_fwd_noalloc_scratch_bytes() -> int:
@@ -713,6 +782,235 @@ def forward_rope(q, k, v, cos_t, sin_t, causal: bool = False, scale: float | Non
                            ws.numel(), s.cuda_stream)
     if st != ATTN_OK:
         raise AttnError(st, "attn_fwd_rope")
+    return out, lse
+
+
+# ---------------------------------------------------------------- key/value cache, cross attention
+
+def _expect(t, name, dtype, shape, device):
+    """As _check, and the tensor must be on `device`."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or t.shape != shape \
+            or not t.is_contiguous():
+        _check(t, name, dtype, shape)
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _scratch(nbytes: int, device, stream):
+    """A workspace for one call, from torch's allocator on `stream` (None: the current one): freed on return, and its
+    memory handed on in that stream's order.  A captured call's lies in its graph's own pool, so graphs share none."""
+    import torch
+
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _on(device):
+    """Makes `device` current for the calls inside, where it is not already."""
+    import contextlib
+
+    import torch
+
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, device):
+    """Checks a paged cache's tensors; returns (B, Hkv, D, num_pages, page, max_pages)."""
+    import torch
+
+    if k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_cache must be 4-D [num_pages, Hkv, page, D] and block_table 2-D [B, max_pages]")
+    num_pages, Hkv, page, D = k_cache.shape
+    B, max_pages = block_table.shape
+    f8 = k_cache.dtype is torch.float8_e4m3fn
+    if not f8 and k_cache.dtype is not torch.bfloat16:
+        raise TypeError(f"k_cache must be torch.bfloat16 or torch.float8_e4m3fn, got {k_cache.dtype}")
+    if f8 != (k_scale is not None) or f8 != (v_scale is not None):
+        raise ValueError("k_scale and v_scale come with a float8_e4m3fn cache, and only with one")
+    if k_cache.device.type != "cuda":
+        raise ValueError("k_cache must be a CUDA tensor")
+    _expect(k_cache, "k_cache", k_cache.dtype, (num_pages, Hkv, page, D), device)
+    _expect(v_cache, "v_cache", k_cache.dtype, (num_pages, Hkv, page, D), device)
+    if f8:
+        _expect(k_scale, "k_scale", torch.float8_e8m0fnu, (num_pages, Hkv, page), device)
+        _expect(v_scale, "v_scale", torch.float8_e8m0fnu, (num_pages, Hkv, page), device)
+    _expect(block_table, "block_table", torch.int32, (B, max_pages), device)
+    _expect(lens, "lens", torch.int32, (B,), device)
+    return B, Hkv, D, num_pages, page, max_pages
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def cache_append(k, v, k_cache, v_cache, block_table, lens, new_lens=None, k_scale=None, v_scale=None, stream=None):
+    """Writes new keys and values k, v (bf16 [B, Hkv, T, D]) into a paged cache, behind the lens[b] positions that
+    each sequence holds: row t of sequence b goes to position lens[b] + t, for t < new_lens[b] (int32 [B]; None: all
+    T).  Returns None; ``lens`` is left as it is.
+
+    The cache is [num_pages, Hkv, page, D] (page a multiple of 16), position p of sequence b being row p % page of
+    page block_table[b, p // page] (int32 [B, max_pages]).  bfloat16, or float8_e4m3fn with k_scale and v_scale
+    (float8_e8m0fnu [num_pages, Hkv, page]): each row is then rounded to code * 2^e with its own exponent.  Positions
+    outside the table, and table entries that are no page, are not written.  No two rows of a call may have the same
+    place.
+    """
+    import torch
+
+    dev = k.device
+    B, Hkv, D, num_pages, page, max_pages = _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, dev)
+    T = k.shape[2] if k.dim() == 4 else -1
+    _expect(k, "k", torch.bfloat16, (B, Hkv, T, D), dev)
+    _expect(v, "v", torch.bfloat16, (B, Hkv, T, D), dev)
+    if new_lens is not None:
+        _expect(new_lens, "new_lens", torch.int32, (B,), dev)
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    with _on(dev):
+        st = lib.attn_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
+                                   _ptr(v_scale), block_table.data_ptr(), lens.data_ptr(), _ptr(new_lens), B, Hkv, T,
+                                   D, num_pages, page, max_pages, s.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_append")
+
+
+def cache_read(k_cache, v_cache, block_table, lens, N: int, k_scale=None, v_scale=None, k_out=None, v_out=None,
+               stream=None):
+    """Reads positions [0, N) of every sequence of a paged cache (see cache_append) back as contiguous bf16
+    [B, Hkv, N, D], the layout forward() takes; zeros at and past lens[b], and where the table names no page.
+    Returns (k, v).  E4M3 rows come back exactly: code * 2^e is a bf16 number."""
+    import torch
+
+    dev = k_cache.device
+    B, Hkv, D, num_pages, page, max_pages = _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, dev)
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    shape = (B, Hkv, N, D)
+    k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
+    v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v_out is None else v_out
+    _expect(k_out, "k_out", torch.bfloat16, shape, dev)
+    _expect(v_out, "v_out", torch.bfloat16, shape, dev)
+    with _on(dev):
+        st = lib.attn_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                                 block_table.data_ptr(), lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, Hkv,
+                                 N, D, num_pages, page, max_pages, s.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_cache_read")
+    return k_out, v_out
+
+
+def _decode_outputs(q, Hkv, B, D, out, lse):
+    import torch
+
+    if q.dim() != 4:
+        raise ValueError("q must be 4-D [B, Hq, T, D]")
+    Hq, T = q.shape[1], q.shape[2]
+    dev = q.device
+    _expect(q, "q", torch.bfloat16, (B, Hq, T, D), dev)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
+    _expect(out, "out", torch.bfloat16, (B, Hq, T, D), dev)
+    _expect(lse, "lse", torch.float32, (B, Hq, T), dev)
+    return Hq, T, out, lse
+
+
+def forward_decode(q, k_cache, v_cache, block_table, lens, k_scale=None, v_scale=None, scale: float | None = None,
+                   out=None, lse=None, stream=None):
+    """Attention of the last T tokens of each sequence (q bf16 [B, Hq, T, D]: T = 1, or a few drafted ones) over its
+    paged cache (see cache_append), which holds their keys and values already: lens[b] counts them, token t stands at
+    position lens[b] - T + t and sees the positions up to its own.  Returns (o bf16, lse fp32 [B, Hq, T]); a row that
+    sees nothing has o = 0 and lse = -inf.  Table entries that are no page read as zero keys and values.
+
+    Made for few rows: the cache is read once for each 64 rows (T times the query heads of a KV head)."""
+    import torch
+
+    dev = q.device
+    B, Hkv, D, num_pages, page, max_pages = _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, dev)
+    Hq, T, out, lse = _decode_outputs(q, Hkv, B, D, out, lse)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    with _on(dev):
+        nbytes = lib.attn_fwd_decode_workspace_bytes(B, Hq, Hkv, T, D, page, max_pages)
+        ws = _scratch(nbytes, dev, stream) if nbytes > 0 else None
+        st = lib.attn_fwd_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+                                 block_table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
+                                 T, D, num_pages, page, max_pages, scale, _ptr(ws), max(nbytes, 0), s.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_fwd_decode")
+    return out, lse
+
+
+def forward_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len: int, block_table, lens, k_scale=None,
+                          v_scale=None, scale: float | None = None, out=None, lse=None, stream=None):
+    """forward_decode for a batch whose sequences all start with one prefix of ``prefix_len`` tokens, held once in the
+    pages prefix_table (int32, at least ceil(prefix_len / page) entries): every query sees the whole prefix, and of its
+    own sequence's positions (block_table, lens: those behind the prefix) what forward_decode shows it.  The prefix is
+    read once for the batch and joined with each row's own keys by maximum and sum.  Returns (o, lse) of the softmax
+    over both."""
+    import torch
+
+    dev = q.device
+    B, Hkv, D, num_pages, page, max_pages = _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, dev)
+    Hq, T, out, lse = _decode_outputs(q, Hkv, B, D, out, lse)
+    _expect(prefix_table, "prefix_table", torch.int32, (prefix_table.numel(),), dev)
+    if prefix_len < 0 or prefix_len > prefix_table.numel() * page:
+        raise ValueError(f"prefix_len {prefix_len} does not fit prefix_table's {prefix_table.numel()} pages of {page}")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    with _on(dev):
+        nbytes = lib.attn_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, T, D, page, max_pages, prefix_len)
+        ws = _scratch(nbytes, dev, stream) if nbytes > 0 else None
+        st = lib.attn_fwd_shared_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
+                                        _ptr(v_scale), prefix_table.data_ptr(), prefix_len, block_table.data_ptr(),
+                                        lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, T, D, num_pages,
+                                        page, max_pages, scale, _ptr(ws), max(nbytes, 0), s.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_fwd_shared_prefix")
+    return out, lse
+
+
+def _cross_checks(q, k, v, k_lens):
+    import torch
+
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must be 4-D [B, H, N, D]")
+    B, Hq, Nq, D = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    dev = q.device
+    _expect(q, "q", torch.bfloat16, (B, Hq, Nq, D), dev)
+    _expect(k, "k", torch.bfloat16, (B, Hkv, Nk, D), dev)
+    _expect(v, "v", torch.bfloat16, (B, Hkv, Nk, D), dev)
+    if k_lens is not None:
+        _expect(k_lens, "k_lens", torch.int32, (B,), dev)
+    return B, Hq, Hkv, Nq, Nk, D, dev
+
+
+def forward_cross(q, k, v, k_lens=None, scale: float | None = None, out=None, lse=None, stream=None):
+    """Attention of q (bf16 [B, Hq, Nq, D]) to keys and values of another length (bf16 [B, Hkv, Nk, D]), as a
+    decoder's to an encoder's states.  ``k_lens`` (int32 [B], on the device) gives how many of the Nk positions each
+    batch row has; the padding behind them may hold anything.  Returns (o bf16, lse fp32 [B, Hq, Nq]); rows without
+    a key have o = 0 and lse = -inf."""
+    import torch
+
+    B, Hq, Hkv, Nq, Nk, D, dev = _cross_checks(q, k, v, k_lens)
+    out = torch.empty_like(q) if out is None else out
+    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if lse is None else lse
+    _expect(out, "out", torch.bfloat16, (B, Hq, Nq, D), dev)
+    _expect(lse, "lse", torch.float32, (B, Hq, Nq), dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    with _on(dev):
+        nbytes = lib.attn_fwd_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, D)
+        ws = _scratch(nbytes, dev, stream) if nbytes > 0 else None
+        st = lib.attn_fwd_cross(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_lens), out.data_ptr(),
+                                lse.data_ptr(), B, Hq, Hkv, Nq, Nk, D, scale, _ptr(ws), max(nbytes, 0),
+                                s.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_fwd_cross")
     return out, lse
 
 

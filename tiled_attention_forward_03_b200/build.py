@@ -22,7 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libattn_fwd.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["attn_api.cu"]
-HEADERS = ["attn_fwd_kernel.cuh", "attn_fwd_colsplit_kernel.cuh", "attn_fwd_wide_kernel.cuh", "attn_bwd_kernel.cuh", "attn_rope_kernel.cuh", "sm100_ptx.cuh"]
+HEADERS = ["attn_fwd_kernel.cuh", "attn_fwd_colsplit_kernel.cuh", "attn_fwd_wide_kernel.cuh", "attn_bwd_kernel.cuh", "attn_rope_kernel.cuh",
+           "attn_cache_kernel.cuh", "attn_decode_kernel.cuh", "attn_serve_api.cuh", "sm100_ptx.cuh"]
 EXPECTED_REGS = 168
 
 NVCC_FLAGS = [
@@ -30,7 +31,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-shared", "-Xcompiler", "-fPIC,-O2",
     "-Xptxas", "-v",
-    "--expt-relaxed-constexpr",
+    "--expt-relaxed-constexpr", "-split-compile=0",
 ]
 
 

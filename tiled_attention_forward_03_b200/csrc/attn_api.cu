@@ -1213,3 +1213,5 @@ int attn_fwd_from_host(const void* q_host, const void* k_host, const void* v_hos
 }
 
 }  // extern "C"
+
+#include "attn_serve_api.cuh"

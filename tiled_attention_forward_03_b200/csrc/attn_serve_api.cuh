@@ -1,0 +1,382 @@
+// attn_serve_api.cuh -- host side of the key/value cache and of attention over keys of another
+// length (include/attn.h): argument checks, schedules and launches.  Part of attn_api.cu's
+// translation unit: it uses that file's device set-up, error records and tensor-map encoders.
+#pragma once
+
+#include "attn_cache_kernel.cuh"
+#include "attn_decode_kernel.cuh"
+
+namespace {
+
+// ---------------------------------------------------------------- paged cache: shared checks
+
+struct CacheArgs {
+  const void *k, *v, *ks, *vs;
+  const int *table, *lens;
+  int B, Hkv, D, num_pages, page, max_pages;
+};
+
+// Sizes of a cache and of the call on it (no CUDA call, no pointer looked at).
+int cache_size_checks(const CacheArgs& a) {
+  if (a.B < 0 || a.Hkv < 1 || a.num_pages < 1 || a.page < 1 || a.max_pages < 0) return ATTN_ERR_INVALID_ARG;
+  if (!narrow_head_dim(a.D) || a.page % 16 != 0) return ATTN_ERR_UNSUPPORTED;
+  if ((long long)a.num_pages * a.Hkv > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+int cache_pointer_checks(const CacheArgs& a) {
+  if (!a.k || !a.v || !a.lens || (a.max_pages > 0 && !a.table)) return ATTN_ERR_INVALID_ARG;
+  if ((a.ks == nullptr) != (a.vs == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(a.k, 16) || !aligned(a.v, 16) || !aligned(a.table, 4) || !aligned(a.lens, 4) || !aligned(a.ks, 16) ||
+      !aligned(a.vs, 16))
+    return ATTN_ERR_MISALIGNED;
+  return ATTN_OK;
+}
+
+attn::CacheView cache_view(const CacheArgs& a) {
+  attn::CacheView c;
+  c.k = const_cast<void*>(a.k);
+  c.v = const_cast<void*>(a.v);
+  c.ks = static_cast<uint8_t*>(const_cast<void*>(a.ks));
+  c.vs = static_cast<uint8_t*>(const_cast<void*>(a.vs));
+  c.table = a.table;
+  c.lens = a.lens;
+  c.max_pages = a.max_pages;
+  c.num_pages = a.num_pages;
+  c.page = a.page;
+  c.Hkv = a.Hkv;
+  c.div_page = attn::make_fast_div((uint32_t)a.page);
+  return c;
+}
+
+int launch_status(const char* what) {
+  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) return ATTN_OK;
+  record_cuda_error(what, e);
+  return ATTN_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- decode schedule
+
+// Few rows over long keys: how attn_decode_kernel is launched, and its workspace.
+struct DecPlan {
+  int row_tiles, row_blocks, prefix_row_tiles = 1, prefix_row_blocks = 0;
+  int whole_units;
+  unsigned grid;
+  bool join;                 // the second kernel is needed
+  size_t slot_o, slot_ml;    // bytes
+  size_t area_o, area_ml;    // bytes of one area (shared prefix: two areas)
+  size_t bytes() const { return slot_o + slot_ml + 2 * (area_o + area_ml); }
+};
+
+constexpr int kDecMinShare = 2;     // blocks of 64 keys
+constexpr int kDecShortBlocks = 2;  // sequences of at most this many blocks are never split
+constexpr int kDecCtasPerSm = 3;    // resident CTAs (the kernel's launch bounds)
+
+// 16-row tiles per unit: 1, 2 or 4.
+int dec_row_tiles(long long rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+
+// `cap`: keys a sequence can have at most.  `shared`: a prefix of `prefix_len` keys comes first;
+// `prefix_here`: this kernel computes it too.
+DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms, bool shared, bool prefix_here,
+                 long long prefix_len) {
+  DecPlan pl;
+  const long long cap_blocks = cap > 0 ? (cap + attn::kDecBlock - 1) / attn::kDecBlock : 1;
+  const long long pre_blocks = (prefix_len + attn::kDecBlock - 1) / attn::kDecBlock;
+  pl.row_tiles = dec_row_tiles(GT);
+  pl.row_blocks = (int)((GT + 16 * pl.row_tiles - 1) / (16 * pl.row_tiles));
+  long long units = (long long)B * Hkv * pl.row_blocks;
+  double blocks = (double)units * (double)cap_blocks;
+  bool split = cap_blocks > kDecShortBlocks;
+  if (prefix_here) {
+    const long long rows = (long long)B * GT;
+    pl.prefix_row_tiles = dec_row_tiles(rows);
+    pl.prefix_row_blocks = (int)((rows + 16 * pl.prefix_row_tiles - 1) / (16 * pl.prefix_row_tiles));
+    blocks += (double)Hkv * pl.prefix_row_blocks * (double)pre_blocks;
+    units += (long long)Hkv * pl.prefix_row_blocks;
+    split = split || pre_blocks > kDecShortBlocks;
+  }
+  pl.whole_units = split ? 0 : 1;
+  const double most = split ? blocks / kDecMinShare + 1 : (double)units;
+  const long long ctas = (long long)kDecCtasPerSm * num_sms;
+  pl.grid = (unsigned)(most < (double)ctas ? (long long)most : ctas);
+  if (pl.grid < 1) pl.grid = 1;
+  pl.join = split || shared;
+  const int slot_rows = 16 * (pl.row_tiles > pl.prefix_row_tiles ? pl.row_tiles : pl.prefix_row_tiles);
+  const size_t slots = split ? 2 * (size_t)pl.grid * slot_rows : 0;
+  pl.slot_o = slots * D * sizeof(float);
+  pl.slot_ml = slots * sizeof(float2);
+  const size_t rows = shared ? ((size_t)B * Hkv * (size_t)GT + 63) / 64 * 64 : 0;
+  pl.area_o = rows * D * sizeof(float);
+  pl.area_ml = rows * sizeof(float2);
+  return pl;
+}
+
+template <int D>
+void launch_decode_dim(const attn::DecParams& p, const DecPlan& pl, bool f8, cudaStream_t s) {
+  if (f8)
+    attn::attn_decode_kernel<D, true><<<pl.grid, attn::kDecThreads, 0, s>>>(p);
+  else
+    attn::attn_decode_kernel<D, false><<<pl.grid, attn::kDecThreads, 0, s>>>(p);
+  if (pl.join)
+    attn::attn_decode_join_kernel<D>
+        <<<(unsigned)((long long)p.B * p.Hkv * p.row_blocks), attn::kDecThreads, 0, s>>>(p, pl.grid);
+}
+
+// Fills the schedule and workspace part of `p` and launches.
+int launch_decode(attn::DecParams& p, const DecPlan& pl, int D, bool shared, void* workspace, cudaStream_t s) {
+  p.row_tiles = pl.row_tiles;
+  p.row_blocks = pl.row_blocks;
+  p.prefix_row_tiles = pl.prefix_row_tiles;
+  p.prefix_row_blocks = pl.prefix_row_blocks;
+  p.whole_units = pl.whole_units;
+  p.min_share = pl.whole_units ? 1 : kDecMinShare;
+  p.slot_rows = 16 * (pl.row_tiles > pl.prefix_row_tiles ? pl.row_tiles : pl.prefix_row_tiles);
+  char* w = static_cast<char*>(workspace);
+  p.slot_o = reinterpret_cast<float*>(w);
+  p.slot_ml = reinterpret_cast<float2*>(w + pl.slot_o);
+  w += pl.slot_o + pl.slot_ml;
+  for (int i = 0; i < 2; ++i) {
+    p.area_o[i] = shared ? reinterpret_cast<float*>(w) : nullptr;
+    p.area_ml[i] = shared ? reinterpret_cast<float2*>(w + pl.area_o) : nullptr;
+    w += pl.area_o + pl.area_ml;
+  }
+  switch (D) {
+    case 32: launch_decode_dim<32>(p, pl, p.ks != nullptr, s); break;
+    case 64: launch_decode_dim<64>(p, pl, p.ks != nullptr, s); break;
+    case 96: launch_decode_dim<96>(p, pl, p.ks != nullptr, s); break;
+    default: launch_decode_dim<128>(p, pl, p.ks != nullptr, s); break;
+  }
+  return launch_status("decode kernel launch");
+}
+
+// Sizes common to decode and shared prefix; rows of a KV head in `GT`.
+int decode_size_checks(const CacheArgs& a, int Hq, int T, float scale, long long* GT) {
+  const int st = cache_size_checks(a);
+  if (st == ATTN_ERR_INVALID_ARG || Hq < 1 || T < 0 || Hq % a.Hkv != 0 || !std::isfinite(scale))
+    return ATTN_ERR_INVALID_ARG;
+  if (st != ATTN_OK) return st;
+  *GT = (long long)(Hq / a.Hkv) * T;
+  // rows and work units are indexed in 32 bits; a batch's rows of one KV head too (shared prefix)
+  if ((long long)a.B * a.Hkv > 0x7fffffffLL || *GT > (1LL << 30) || (double)a.B * (double)*GT > 2147483647.0 ||
+      (double)a.B * a.Hkv * ((double)*GT / 16 + 1) > 2147483647.0)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+int sm_count(int* num_sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(num_sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && *num_sms >= 1) return ATTN_OK;
+  record_cuda_error("cudaDeviceGetAttribute", e);
+  return ATTN_ERR_CUDA;
+}
+
+long long cache_cap(int page, int max_pages) {
+  const long long n = (long long)page * max_pages;
+  return n < 0x7fffffffLL ? n : 0x7fffffffLL;
+}
+
+void fill_decode(attn::DecParams& p, const CacheArgs& a, const void* q, void* o, float* lse, int T, long long GT,
+                 float scale, int causal) {
+  std::memset(&p, 0, sizeof(p));
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.k = a.k;
+  p.v = a.v;
+  p.ks = static_cast<const uint8_t*>(a.ks);
+  p.vs = static_cast<const uint8_t*>(a.vs);
+  p.table = a.table;
+  p.lens = a.lens;
+  p.cap = cache_cap(a.page, a.max_pages);
+  p.max_pages = a.max_pages;
+  p.num_pages = a.num_pages;
+  p.page = a.page;
+  p.Hkv = a.Hkv;
+  p.B = a.B;
+  p.div_page = attn::make_fast_div((uint32_t)a.page);
+  p.GT = (int)GT;
+  p.T = T;
+  p.causal = causal;
+  p.div_gt = attn::make_fast_div((uint32_t)GT);
+  p.c = scale * attn::kLog2e;
+  p.o = reinterpret_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, void* k_scale, void* v_scale,
+                      const int* block_table, const int* lens, const int* new_lens, int B, int Hkv, int T, int D,
+                      int num_pages, int page_size, int max_pages, void* stream) {
+  const CacheArgs a{k_cache, v_cache, k_scale, v_scale, block_table, lens, B, Hkv, D, num_pages, page_size, max_pages};
+  int st = cache_size_checks(a);
+  if (st != ATTN_OK) return st;
+  if (T < 0) return ATTN_ERR_INVALID_ARG;
+  // rows are indexed in 32 bits, 2^31 blocks of 8 rows
+  if ((double)B * Hkv * (double)T >= 4294967296.0) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return ATTN_OK;
+  if (!k || !v) return ATTN_ERR_INVALID_ARG;
+  if ((st = cache_pointer_checks(a)) != ATTN_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(new_lens, 4)) return ATTN_ERR_MISALIGNED;
+  const uint32_t rows = (uint32_t)((long long)B * Hkv * T);
+  const int lanes = D / 8 <= 4 ? 4 : D / 8 <= 8 ? 8 : 16;
+  const unsigned grid = (unsigned)(((unsigned long long)rows * lanes + 255) / 256);
+  const attn::CacheView c = cache_view(a);
+  const auto kb = reinterpret_cast<const __nv_bfloat16*>(k);
+  const auto vb = reinterpret_cast<const __nv_bfloat16*>(v);
+  const attn::FastDiv dt = attn::make_fast_div((uint32_t)T), dh = attn::make_fast_div((uint32_t)Hkv);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool f8 = k_scale != nullptr;
+  auto go = [&](auto kern) { kern<<<grid, 256, 0, s>>>(kb, vb, c, new_lens, T, dt, dh, rows); };
+  switch (D) {
+    case 32: f8 ? go(attn::attn_cache_append_kernel<32, true>) : go(attn::attn_cache_append_kernel<32, false>); break;
+    case 64: f8 ? go(attn::attn_cache_append_kernel<64, true>) : go(attn::attn_cache_append_kernel<64, false>); break;
+    case 96: f8 ? go(attn::attn_cache_append_kernel<96, true>) : go(attn::attn_cache_append_kernel<96, false>); break;
+    default: f8 ? go(attn::attn_cache_append_kernel<128, true>) : go(attn::attn_cache_append_kernel<128, false>); break;
+  }
+  return launch_status("cache append kernel launch");
+}
+
+int attn_cache_read(const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                    const int* block_table, const int* lens, void* k, void* v, int B, int Hkv, int N, int D,
+                    int num_pages, int page_size, int max_pages, void* stream) {
+  const CacheArgs a{k_cache, v_cache, k_scale, v_scale, block_table, lens, B, Hkv, D, num_pages, page_size, max_pages};
+  int st = cache_size_checks(a);
+  if (st != ATTN_OK) return st;
+  if (N < 0) return ATTN_ERR_INVALID_ARG;
+  if ((double)B * Hkv * (double)N >= 4294967296.0) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || N == 0) return ATTN_OK;
+  if (!k || !v) return ATTN_ERR_INVALID_ARG;
+  if ((st = cache_pointer_checks(a)) != ATTN_OK) return st;
+  if (!aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_MISALIGNED;
+  const unsigned long long items = (unsigned long long)B * Hkv * N * (D / 16);
+  const unsigned grid = (unsigned)((items + 255) / 256);
+  const attn::CacheView c = cache_view(a);
+  const auto kb = reinterpret_cast<__nv_bfloat16*>(k);
+  const auto vb = reinterpret_cast<__nv_bfloat16*>(v);
+  const attn::FastDiv dn = attn::make_fast_div((uint32_t)N), dh = attn::make_fast_div((uint32_t)Hkv);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool f8 = k_scale != nullptr;
+  auto go = [&](auto kern) { kern<<<grid, 256, 0, s>>>(c, kb, vb, N, dn, dh, items); };
+  switch (D) {
+    case 32: f8 ? go(attn::attn_cache_read_kernel<32, true>) : go(attn::attn_cache_read_kernel<32, false>); break;
+    case 64: f8 ? go(attn::attn_cache_read_kernel<64, true>) : go(attn::attn_cache_read_kernel<64, false>); break;
+    case 96: f8 ? go(attn::attn_cache_read_kernel<96, true>) : go(attn::attn_cache_read_kernel<96, false>); break;
+    default: f8 ? go(attn::attn_cache_read_kernel<128, true>) : go(attn::attn_cache_read_kernel<128, false>); break;
+  }
+  return launch_status("cache read kernel launch");
+}
+
+long long attn_fwd_decode_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int page_size, int max_pages) {
+  const CacheArgs a{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, B, Hkv, D, 1, page_size, max_pages};
+  long long GT = 0;
+  if (decode_size_checks(a, Hq, T, 1.f, &GT) != ATTN_OK) return -1;
+  if (B == 0 || T == 0) return 0;
+  int num_sms = 0;
+  if (sm_count(&num_sms) != ATTN_OK) return -1;
+  return (long long)dec_plan(B, Hkv, GT, D, cache_cap(page_size, max_pages), num_sms, false, false, 0).bytes();
+}
+
+int attn_fwd_decode(const void* q, const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
+                    const int* block_table, const int* lens, void* o, float* lse, int B, int Hq, int Hkv, int T,
+                    int D, int num_pages, int page_size, int max_pages, float scale, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  const CacheArgs a{k_cache, v_cache, k_scale, v_scale, block_table, lens, B, Hkv, D, num_pages, page_size, max_pages};
+  long long GT = 0;
+  int st = decode_size_checks(a, Hq, T, scale, &GT);
+  if (st != ATTN_OK) return st;
+  if (B == 0 || T == 0) return ATTN_OK;
+  if (!q || !o || !lse) return ATTN_ERR_INVALID_ARG;
+  if ((st = cache_pointer_checks(a)) != ATTN_OK) return st;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256)) return ATTN_ERR_MISALIGNED;
+  int num_sms = 0;
+  if ((st = sm_count(&num_sms)) != ATTN_OK) return st;
+  const DecPlan pl = dec_plan(B, Hkv, GT, D, cache_cap(page_size, max_pages), num_sms, false, false, 0);
+  if (pl.bytes() > workspace_bytes || (pl.bytes() > 0 && !workspace)) return ATTN_ERR_INVALID_ARG;
+  attn::DecParams p;
+  fill_decode(p, a, q, o, lse, T, GT, scale, 1);
+  return launch_decode(p, pl, D, false, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+long long attn_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int page_size, int max_pages,
+                                                 int prefix_len) {
+  const CacheArgs a{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, B, Hkv, D, 1, page_size, max_pages};
+  long long GT = 0;
+  if (prefix_len < 0 || decode_size_checks(a, Hq, T, 1.f, &GT) != ATTN_OK) return -1;
+  if (B == 0 || T == 0) return 0;
+  int num_sms = 0;
+  if (sm_count(&num_sms) != ATTN_OK) return -1;
+  return (long long)dec_plan(B, Hkv, GT, D, cache_cap(page_size, max_pages), num_sms, true, true, prefix_len).bytes();
+}
+
+int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
+                           const void* v_scale, const int* prefix_table, int prefix_len, const int* block_table,
+                           const int* lens, void* o, float* lse, int B, int Hq, int Hkv, int T, int D, int num_pages,
+                           int page_size, int max_pages, float scale, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  const CacheArgs a{k_cache, v_cache, k_scale, v_scale, block_table, lens, B, Hkv, D, num_pages, page_size, max_pages};
+  long long GT = 0;
+  int st = decode_size_checks(a, Hq, T, scale, &GT);
+  if (st != ATTN_OK) return st;
+  if (prefix_len < 0) return ATTN_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return ATTN_OK;
+  if (!q || !o || !lse || (prefix_len > 0 && !prefix_table)) return ATTN_ERR_INVALID_ARG;
+  if ((st = cache_pointer_checks(a)) != ATTN_OK) return st;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256) || !aligned(prefix_table, 4))
+    return ATTN_ERR_MISALIGNED;
+  int num_sms = 0;
+  if ((st = sm_count(&num_sms)) != ATTN_OK) return st;
+  const DecPlan pl =
+      dec_plan(B, Hkv, GT, D, cache_cap(page_size, max_pages), num_sms, true, prefix_len > 0, prefix_len);
+  if (pl.bytes() > workspace_bytes || (pl.bytes() > 0 && !workspace)) return ATTN_ERR_INVALID_ARG;
+  attn::DecParams p;
+  fill_decode(p, a, q, o, lse, T, GT, scale, 1);
+  p.prefix_table = prefix_table;
+  p.prefix_len = prefix_len;
+  p.prefix_pages = (prefix_len + page_size - 1) / page_size;
+  return launch_decode(p, pl, D, true, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------- cross attention
+
+long long attn_fwd_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D) {
+  if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Nq < 0 || Nk < 0 || !narrow_head_dim(D)) return -1;
+  const long long GT = (long long)(Hq / Hkv) * Nq;
+  if (B == 0 || Nq == 0) return 0;
+  int num_sms = 0;
+  if (sm_count(&num_sms) != ATTN_OK) return -1;
+  return (long long)dec_plan(B, Hkv, GT, D, Nk, num_sms, false, false, 0).bytes();
+}
+
+int attn_fwd_cross(const void* q, const void* k, const void* v, const int* k_lens, void* o, float* lse, int B, int Hq,
+                   int Hkv, int Nq, int Nk, int D, float scale, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  if (B < 0 || Nq < 0 || Nk < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !std::isfinite(scale))
+    return ATTN_ERR_INVALID_ARG;
+  if (!narrow_head_dim(D)) return ATTN_ERR_UNSUPPORTED;
+  const long long GT = (long long)(Hq / Hkv) * Nq;
+  if ((long long)B * Hkv > 0x7fffffffLL || GT > (1LL << 30) ||
+      (double)B * Hkv * ((double)GT / 16 + 1) > 2147483647.0)
+    return ATTN_ERR_UNSUPPORTED;
+  if (B == 0 || Nq == 0) return ATTN_OK;
+  if (!q || !o || !lse || (Nk > 0 && (!k || !v))) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
+      !aligned(k_lens, 4) || !aligned(workspace, 256))
+    return ATTN_ERR_MISALIGNED;
+  int st, num_sms = 0;
+  if ((st = sm_count(&num_sms)) != ATTN_OK) return st;
+  const DecPlan pl = dec_plan(B, Hkv, GT, D, Nk, num_sms, false, false, 0);
+  if (pl.bytes() > workspace_bytes || (pl.bytes() > 0 && !workspace)) return ATTN_ERR_INVALID_ARG;
+  // contiguous keys: sequence b is page b of Nk rows
+  const CacheArgs a{k, v, nullptr, nullptr, nullptr, k_lens, B, Hkv, D, B, Nk > 0 ? Nk : 1, 1};
+  attn::DecParams p;
+  fill_decode(p, a, q, o, lse, Nq, GT, scale, 0);
+  p.cap = Nk;
+  p.len_all = Nk;
+  return launch_decode(p, pl, D, false, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
