@@ -5,7 +5,7 @@
  * (attn_rope_tables, attn_rope_qk, attn_fwd_rope; their backward attn_rope_qk_inverse, attn_bwd_rope);
  * a paged key/value cache, bf16 or quantised (attn_cache_append, attn_cache_read), the attention of
  * new tokens over it (attn_fwd_decode; behind a prefix that the batch shares,
- * attn_fwd_shared_prefix), and attention to keys of another length (attn_fwd_cross).
+ * attn_fwd_shared_prefix), and attention to keys of another length (attn_fwd_cross, attn_bwd_cross).
  *
  * The operation is the tiled attention forward pass named by "HipKittens:
  * fast and furious AMD kernels" (section "Performance results": an attention
@@ -487,6 +487,25 @@ int attn_fwd_cross(const void* q, const void* k, const void* v, const int* k_len
 
 /* Workspace attn_fwd_cross needs on the current device; -1 on rejected sizes or a CUDA error. */
 long long attn_fwd_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D);
+
+/*
+ * attn_bwd_cross -- gradients of attn_fwd_cross (formulas as attn_bwd, the sums over the first
+ * k_lens[b] keys of each batch row).
+ *   q, k, v, k_lens, o, lse   the forward's inputs and outputs                        read
+ *   dout       bf16 [B, Hq, Nq, D]: dL/dO                                             read
+ *   dq         bf16 [B, Hq,  Nq, D]; zero in batch rows without a key      written (every element)
+ *   dk, dv     bf16 [B, Hkv, Nk, D]; zero at the padding                   written (every element)
+ *   workspace  device pointer, 256-byte aligned, of at least attn_bwd_cross_workspace_bytes() bytes.
+ * Sizes, limits and errors as attn_fwd_cross; additionally B * Hkv * ceil(Nk / 128) <= 2^30.  With
+ * Nq == 0 dk and dv are zero-filled, with Nk == 0 dq is.  The padding's keys and values are not used.  Numerics and
+ * determinism as attn_bwd.
+ */
+int attn_bwd_cross(const void* q, const void* k, const void* v, const int* k_lens, const void* o, const float* lse,
+                   const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Nq, int Nk, int D,
+                   float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace attn_bwd_cross needs; host only, -1 on rejected sizes. */
+long long attn_bwd_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq);
 
 /* Human-readable name of an attn_status_t value (static string, never null). */
 const char* attn_status_string(int status);

@@ -33,7 +33,7 @@ __all__ = [
     "attn_cache_append", "attn_cache_read", "attn_fwd_decode", "attn_fwd_decode_workspace_bytes",
     "attn_fwd_shared_prefix", "attn_fwd_shared_prefix_workspace_bytes", "attn_fwd_cross",
     "attn_fwd_cross_workspace_bytes", "cache_append", "cache_read", "forward_decode", "forward_shared_prefix",
-    "forward_cross",
+    "forward_cross", "attn_bwd_cross", "attn_bwd_cross_workspace_bytes", "backward_cross",
 ]
 
 ATTN_OK = 0
@@ -118,6 +118,10 @@ def _load() -> ctypes.CDLL:
     L.attn_fwd_cross.restype = i
     L.attn_fwd_cross_workspace_bytes.argtypes = [i] * 6
     L.attn_fwd_cross_workspace_bytes.restype = ctypes.c_longlong
+    L.attn_bwd_cross.argtypes = [vp] * 10 + [i] * 6 + [f, vp, ctypes.c_size_t, vp]
+    L.attn_bwd_cross.restype = i
+    L.attn_bwd_cross_workspace_bytes.argtypes = [i] * 4
+    L.attn_bwd_cross_workspace_bytes.restype = ctypes.c_longlong
     L.attn_status_string.argtypes = [i]
     L.attn_status_string.restype = ctypes.c_char_p
     L.attn_last_cuda_error.argtypes = []
@@ -275,6 +279,17 @@ def attn_fwd_cross(q, k, v, k_lens, o, lse, B, Hq, Hkv, Nq, Nk, D, scale, worksp
 
 def attn_fwd_cross_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, D: int) -> int:
     return lib.attn_fwd_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, D)
+
+
+def attn_bwd_cross(q, k, v, k_lens, o, lse, dout, dq, dk, dv, B, Hq, Hkv, Nq, Nk, D, scale, workspace,
+                   workspace_bytes, stream) -> int:
+    """Direct call of the cross-attention backward entry point (pointers, sizes and stream as integers)."""
+    return lib.attn_bwd_cross(q, k, v, k_lens, o, lse, dout, dq, dk, dv, B, Hq, Hkv, Nq, Nk, D, float(scale),
+                              workspace, workspace_bytes, stream)
+
+
+def attn_bwd_cross_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int) -> int:
+    return lib.attn_bwd_cross_workspace_bytes(B, Hq, Hkv, Nq)
 
 
 def attn_fwd_noalloc_scratch_bytes() -> int:
@@ -1012,6 +1027,38 @@ def forward_cross(q, k, v, k_lens=None, scale: float | None = None, out=None, ls
     if st != ATTN_OK:
         raise AttnError(st, "attn_fwd_cross")
     return out, lse
+
+
+def backward_cross(q, k, v, o, lse, dout, k_lens=None, scale: float | None = None, dq=None, dk=None, dv=None,
+                   stream=None):
+    """Gradients of forward_cross: returns (dq, dk, dv), bf16, shaped like q, k, v, given its o and lse for the same
+    q, k, v, k_lens and scale, and dout = dL/do (bf16).  dk and dv are zero at the padding, dq where a batch row has no
+    key."""
+    import torch
+
+    B, Hq, Hkv, Nq, Nk, D, dev = _cross_checks(q, k, v, k_lens)
+    q_shape, k_shape = (B, Hq, Nq, D), (B, Hkv, Nk, D)
+    _expect(o, "o", torch.bfloat16, q_shape, dev)
+    _expect(lse, "lse", torch.float32, (B, Hq, Nq), dev)
+    _expect(dout, "dout", torch.bfloat16, q_shape, dev)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    _expect(dq, "dq", torch.bfloat16, q_shape, dev)
+    _expect(dk, "dk", torch.bfloat16, k_shape, dev)
+    _expect(dv, "dv", torch.bfloat16, k_shape, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    with _on(dev):
+        nbytes = lib.attn_bwd_cross_workspace_bytes(B, Hq, Hkv, Nq)
+        ws = _scratch(nbytes, dev, stream) if nbytes > 0 else None
+        st = lib.attn_bwd_cross(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_lens), o.data_ptr(), lse.data_ptr(),
+                                dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Nq, Nk, D,
+                                scale, _ptr(ws), max(nbytes, 0), s.cuda_stream)
+    if st != ATTN_OK:
+        raise AttnError(st, "attn_bwd_cross")
+    return dq, dk, dv
 
 
 def device_status(stream=None):

@@ -65,6 +65,15 @@
 // (D = 128: 2 + 2 stages in the KV pass, 3 + 2 in the Q pass; 4 + 4 at D <= 64).
 //
 // Every wait is bounded, as in the forward kernel.
+//
+// kX: cross attention (keys of another length, each batch row's own count of them).  The query rows
+// of a KV head's group are contiguous in memory and all see the same keys, so a KV head has one
+// "query head" of group * Nq rows and there is no group sum.  Row and column tiles have counts of
+// their own; a unit whose key block (KV pass) or whose batch row (Q pass) has no key streams nothing
+// and its gradients are stored as zeros.  Padding keys may hold anything, NaN included: their columns
+// of P and dP are replaced by zeros in registers, and the MMA warp overwrites their rows of the K tile with
+// zeros before dS K reads it (0 * NaN would not vanish in the sum); as rows of the KV pass's own tile they reach
+// only their own lanes of tensor memory, which are stored as zeros.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -153,6 +162,10 @@ struct BwdParams {
   uint32_t idesc_acc;   // 128 x D x 128, A from TMEM, B MN-major
   int pair;             // causal: an item is a row head's heaviest and lightest remaining row blocks
   int num_items;        // items of the pass being launched
+  // kX: N, num_blocks count the pass's row tiles; group is 1
+  const int* k_lens;    // [B], or null: every batch row has Nk keys
+  int Nk;
+  int col_blocks;       // KV pass: column (query) tiles
 };
 
 // -delta_i = -sum_d dO_id O_id (fp32 sums of the bf16 products) and -lse2_i = -LSE_i log2(e)
@@ -216,15 +229,25 @@ struct BwdUnit {
   int n;          // column tiles
   int cpb;        // column tiles per query head (KV pass)
   int c0;         // first column block
+  int len;        // kX: the batch row's keys
 };
 
 // Unit `which` (0 or 1) of work item `item`; false if the item has no such unit.  Items are
 // numbered row head by row head; a causal item pairs the heaviest and the lightest remaining
 // row blocks of a head (equal items) when p.pair is set, else an item is one row block,
 // heaviest first.
-template <bool kKV>
+template <bool kKV, bool kX = false>
 __device__ __forceinline__ bool bwd_unit(const BwdParams& p, int item, int which, BwdUnit& w) {
   const int nb = p.num_blocks;
+  if constexpr (kX) {
+    if (which) return false;
+    w.row_head = item / nb;
+    w.rb = item - w.row_head * nb;
+    w.c0 = 0;
+    w.len = p.k_lens != nullptr ? max(0, min(__ldg(p.k_lens + w.row_head / p.Hkv), p.Nk)) : p.Nk;
+    w.n = w.cpb = kKV ? (w.rb * kBlockM < w.len ? p.col_blocks : 0) : (int)(((long long)w.len + kBlockN - 1) / kBlockN);
+    return true;
+  }
   int k;
   if (p.pair) {
     const int sph = (nb + 1) >> 1;
@@ -266,7 +289,7 @@ __device__ __forceinline__ void bwd_col(const BwdParams& p, const BwdUnit& w, in
   }
 }
 
-template <int D, bool kKV>
+template <int D, bool kKV, bool kX = false>
 __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     attn_bwd_sm100(const __grid_constant__ CUtensorMap tmap_r0, const __grid_constant__ CUtensorMap tmap_r1,
                    const __grid_constant__ CUtensorMap tmap_c0, const __grid_constant__ CUtensorMap tmap_c1,
@@ -377,7 +400,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
       for (int item = blockIdx.x; item < p.num_items && ok; item += gridDim.x)
       for (int which = 0; which < 2 && ok; ++which) {
       BwdUnit w;
-      if (!bwd_unit<kKV>(p, item, which, w)) continue;
+      if (!bwd_unit<kKV, kX>(p, item, which, w)) continue;
+      if (kX && w.n == 0) continue;
       // the row tiles once the previous unit's last S and dP have read them
       if (units > 0u && !(ok = wait_phase(r_empty, (units - 1u) & 1u, abort_flag, kSiteBwdProducer))) break;
       mbar_arrive_expect_tx(r_full, 2 * Plan::kTileBytes);
@@ -473,11 +497,25 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     for (int item = blockIdx.x; item < p.num_items && ok; item += gridDim.x)
     for (int which = 0; which < 2 && ok; ++which) {
     BwdUnit w;
-    if (!bwd_unit<kKV>(p, item, which, w)) continue;
+    if (!bwd_unit<kKV, kX>(p, item, which, w)) continue;
+    if (kX && w.n == 0) continue;
+    // Padding keys' rows of the last K tile become zeros (see the head of the file).
+    auto clear_padding = [&](uint32_t st, int it) {
+      if (!kX || kKV) return;
+      const int first = w.len - it * kBlockN;   // rows of the tile that hold keys
+      if (first >= kBlockN || w.len == p.Nk) return;   // (rows past Nk are zero-filled by TMA)
+      for (int i = first * 8 + lane; i < kBlockN * 8; i += 32)
+#pragma unroll
+        for (int ch = 0; ch < Plan::kChunks; ++ch)
+          st_shared_v4(smem_u32(sC0) + st_bytes(st) + ch * Plan::kChunkBytes + i * 16, 0u, 0u, 0u, 0u);
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
     if (!(ok = wait_all(r_full, units & 1u, kSiteBwdMmaRow))) break;
     // First tile's S and dP.  S's columns were read by the softmax (s_free of the previous unit's
     // last tile was waited for); dP's buffer was last read by MMAs issued before these.
     if (!(ok = wait_all(&c0_full[r0.stage], r0.phase, kSiteBwdMmaCol))) break;
+    clear_padding(r0.stage, 0);
     tc_fence_after();
     issue_rc(0, desc_r0, adv(desc_c0_k, st_bytes(r0.stage)));
     commit(s_full);
@@ -497,6 +535,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
       if (!(ok = wait_all(s_free, par, kSiteBwdMmaP))) break;
       if (has_next) {
         if (!(ok = wait_all(&c0_full[n0.stage], n0.phase, kSiteBwdMmaCol))) break;
+        clear_padding(n0.stage, it + 1);
         tc_fence_after();
         issue_rc(0, desc_r0, adv(desc_c0_k, st_bytes(n0.stage)));
         commit(s_full);
@@ -564,8 +603,29 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     const int item = (int)blockIdx.x + (q >> 1) * (int)gridDim.x;
     if (item >= p.num_items) break;
     BwdUnit w;
-    if (!bwd_unit<kKV>(p, item, q & 1, w)) continue;
+    if (!bwd_unit<kKV, kX>(p, item, q & 1, w)) continue;
     const int row = w.rb * kBlockM + r;         // global index of this thread's tile row
+    if constexpr (kX) {
+      if (w.n == 0) {   // no keys: zero gradients (the two warpgroups take alternate 32-column chunks)
+        if (row < p.N) {
+          for (int ch = h; ch < D / 32; ch += 2) {
+            const size_t at = ((size_t)w.row_head * p.N + row) * D + 32 * ch;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+              if (kKV) {
+                reinterpret_cast<uint4*>(p.dk + at)[i] = zero;
+                reinterpret_cast<uint4*>(p.dv + at)[i] = zero;
+              } else {
+                reinterpret_cast<uint4*>(p.dq + at)[i] = zero;
+              }
+            }
+          }
+        }
+        continue;
+      }
+    }
+    const int keys = kX ? w.len : p.N;          // positions that are keys
     // Q pass: the row's -lse2 and -delta are fixed for the whole unit.
     float row_nlse2 = 0.f, row_ndelta = 0.f;
     if (!kKV) {
@@ -633,7 +693,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
       {
         const int col0 = cb * kBlockN + 64 * h;   // global index of column 0 of this half
         if (kKV) {
-          const bool row_dead = row >= p.N;
+          const bool row_dead = row >= keys;
           const bool diag = p.causal && cb == w.rb;
           if (row_dead || diag) {
 #pragma unroll
@@ -641,7 +701,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
               if (row_dead || col0 + i < row) pv[i] = 0.f;
           }
         } else {
-          const int lim = p.causal ? min(row, p.N - 1) : p.N - 1;  // last allowed key
+          const int lim = p.causal ? min(row, keys - 1) : keys - 1;  // last allowed key
           if (col0 + 63 > lim) {
 #pragma unroll
             for (int i = 0; i < 64; ++i)
@@ -661,6 +721,16 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
         tmem_ld_wait();
         reg_fence32(d0);
         reg_fence32(d1);
+        if constexpr (kX && !kKV) {
+          const int live = keys - cb * kBlockN - 64 * h;   // columns of this half that are keys
+          if (live < 64) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (i >= live) d0[i] = 0u;
+              if (32 + i >= live) d1[i] = 0u;
+            }
+          }
+        }
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
           uint32_t pk[16];
@@ -701,7 +771,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
         mbar_arrive(p_ready_bar(it));
       }
       ring.advance<S0>();
-      if (++cb == p.num_blocks) cb = w.c0;     // the next query head of the group (KV pass)
+      if (++cb == (kX ? w.n : p.num_blocks)) cb = w.c0;     // the next query head of the group (KV pass)
     }
 
     if (!ok) break;
@@ -711,6 +781,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     {
       tc_fence_after();
       const bool row_ok = row < p.N;
+      const bool row_zero = kX && kKV && row >= keys;   // a padding key of a block that has keys
       auto store_acc = [&](uint32_t col, float mul, __nv_bfloat16* out) {
         for (int ch = h; ch < D / 32; ch += 2) {
           uint32_t av[32];
@@ -720,7 +791,7 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            pk[i] = pack_bf16x2(__uint_as_float(av[2 * i]) * mul, __uint_as_float(av[2 * i + 1]) * mul);
+            pk[i] = row_zero ? 0u : pack_bf16x2(__uint_as_float(av[2 * i]) * mul, __uint_as_float(av[2 * i + 1]) * mul);
           if (row_ok) {
             uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)w.row_head * p.N + row) * D + 32 * ch);
 #pragma unroll

@@ -380,3 +380,167 @@ int attn_fwd_cross(const void* q, const void* k, const void* v, const int* k_len
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- cross attention, backward
+
+namespace {
+
+struct CrossBwdDeviceInfo {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+CrossBwdDeviceInfo g_cross_bwd_dev[kMaxDevices];
+
+template <int D>
+cudaError_t cross_bwd_setup_dim() {
+  cudaError_t e = cudaSuccess;
+  auto setup = [&](const void* fn, int smem) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaFuncAttributes fa{};
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, fn);
+    // the register split (setmaxnreg) needs exactly the launch allocation it was sized for
+    if (e == cudaSuccess && attn::BwdCfg<D>::kSplit && fa.numRegs != attn::kRegsAtLaunch)
+      e = cudaErrorInvalidDeviceFunction;
+  };
+  setup(reinterpret_cast<const void*>(attn::attn_bwd_sm100<D, true, true>), attn::BwdPlan<D, true>::kAlloc);
+  setup(reinterpret_cast<const void*>(attn::attn_bwd_sm100<D, false, true>), attn::BwdPlan<D, false>::kAlloc);
+  return e;
+}
+
+bool cross_bwd_device_setup(int dev) {
+  if (dev < 0 || dev >= kMaxDevices) return false;
+  CrossBwdDeviceInfo& d = g_cross_bwd_dev[dev];
+  std::call_once(d.once, [&d] {
+    cudaError_t e = cross_bwd_setup_dim<32>();
+    if (e == cudaSuccess) e = cross_bwd_setup_dim<64>();
+    if (e == cudaSuccess) e = cross_bwd_setup_dim<96>();
+    if (e == cudaSuccess) e = cross_bwd_setup_dim<128>();
+    d.err = e;
+  });
+  if (d.err == cudaSuccess) return true;
+  record_cuda_error("cross-attention backward device setup", d.err);
+  return false;
+}
+
+template <int D>
+void launch_cross_bwd_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
+                          const attn::BwdParams& pkv, const attn::BwdParams& pq, int num_sms, cudaStream_t s) {
+  auto grid = [&](int items) { return (unsigned)(items > num_sms ? num_sms : items); };
+  if (pkv.num_items > 0)
+    attn::attn_bwd_sm100<D, true, true>
+        <<<grid(pkv.num_items), attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, true>::kAlloc, s>>>(mk, mv, mq, mdo, pkv);
+  attn::attn_bwd_sm100<D, false, true>
+      <<<grid(pq.num_items), attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, false>::kAlloc, s>>>(mq, mdo, mk, mv, pq);
+}
+
+// Sizes of a cross-attention problem; query rows of a KV head in `GT`.
+int cross_size_checks(int B, int Hq, int Hkv, int Nq, int Nk, int D, float scale, long long* GT) {
+  if (B < 0 || Nq < 0 || Nk < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !std::isfinite(scale))
+    return ATTN_ERR_INVALID_ARG;
+  if (!narrow_head_dim(D)) return ATTN_ERR_UNSUPPORTED;
+  *GT = (long long)(Hq / Hkv) * Nq;
+  if ((long long)B * Hkv > 0x7fffffffLL || *GT > (1LL << 30) ||
+      (double)B * Hkv * ((double)*GT / 16 + 1) > 2147483647.0 ||
+      (double)B * Hkv * ((double)Nk / 128 + 1) > 1073741824.0)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+long long attn_bwd_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq) {
+  long long GT = 0;
+  if (cross_size_checks(B, Hq, Hkv, Nq, 0, 32, 1.f, &GT) != ATTN_OK) return -1;
+  return attn_bwd_workspace_bytes(B, Hkv, (int)GT);
+}
+
+int attn_bwd_cross(const void* q, const void* k, const void* v, const int* k_lens, const void* o, const float* lse,
+                   const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Nq, int Nk, int D,
+                   float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  // ---- host-side validation (no CUDA call before this block passes)
+  long long GT = 0;
+  int st = cross_size_checks(B, Hq, Hkv, Nq, Nk, D, scale, &GT);
+  if (st != ATTN_OK) return st;
+  if (B == 0 || (Nq == 0 && Nk == 0)) return ATTN_OK;
+  if (Nq > 0 && (!q || !o || !lse || !dout || !dq || !workspace)) return ATTN_ERR_INVALID_ARG;
+  if (Nk > 0 && (!k || !v || !dk || !dv)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(dout, 16) ||
+      !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(lse, 4) || !aligned(k_lens, 4) ||
+      !aligned(workspace, 256))
+    return ATTN_ERR_MISALIGNED;
+  const size_t part = bwd_part_bytes(B, Hkv, (int)GT);
+  if (workspace_bytes < 2 * part) return ATTN_ERR_INVALID_ARG;
+  int dev = 0, num_sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) {
+    record_cuda_error("cudaGetDevice", e);
+    return ATTN_ERR_CUDA;
+  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // one side empty: the other's gradients are zero
+  const size_t q_bytes = (size_t)B * Hkv * (size_t)GT * D * 2, k_bytes = (size_t)B * Hkv * (size_t)Nk * D * 2;
+  if (Nq == 0 || Nk == 0) {
+    if (q_bytes) e = cudaMemsetAsync(dq, 0, q_bytes, s);
+    if (k_bytes) e = cudaMemsetAsync(dk, 0, k_bytes, s);
+    if (k_bytes && e == cudaSuccess) e = cudaMemsetAsync(dv, 0, k_bytes, s);
+    if (e == cudaSuccess) return ATTN_OK;
+    record_cuda_error("cudaMemsetAsync", e);
+    return ATTN_ERR_CUDA;
+  }
+  if ((st = sm_count(&num_sms)) != ATTN_OK) return st;
+  if (!cross_bwd_device_setup(dev)) return ATTN_ERR_CUDA;
+
+  CUtensorMap mq, mk, mv, mdo;
+  const long long heads = (long long)B * Hkv;
+  if ((st = encode_map(&mq, q, heads, (int)GT, D)) != ATTN_OK) return st;
+  if ((st = encode_map(&mk, k, heads, Nk, D)) != ATTN_OK) return st;
+  if ((st = encode_map(&mv, v, heads, Nk, D)) != ATTN_OK) return st;
+  if ((st = encode_map(&mdo, dout, heads, (int)GT, D)) != ATTN_OK) return st;
+
+  const int nq = (int)((GT + attn::kBlockM - 1) / attn::kBlockM);
+  const int nk = (int)(((long long)Nk + attn::kBlockN - 1) / attn::kBlockN);
+  attn::BwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.dq = reinterpret_cast<__nv_bfloat16*>(dq);
+  p.dk = reinterpret_cast<__nv_bfloat16*>(dk);
+  p.dv = reinterpret_cast<__nv_bfloat16*>(dv);
+  float* nlse2 = reinterpret_cast<float*>(workspace);
+  float* ndelta = reinterpret_cast<float*>(static_cast<char*>(workspace) + part);
+  p.nlse2 = nlse2;
+  p.ndelta = ndelta;
+  p.Hq = Hkv;
+  p.Hkv = Hkv;
+  p.Npad = nq * attn::kBlockN;
+  p.group = 1;
+  p.c = scale * attn::kLog2e;
+  p.scale = scale;
+  p.idesc_s = attn::idesc_bf16_f32(attn::kBlockM, attn::kBlockN, false, false, false);
+  p.idesc_acc = attn::idesc_bf16_f32(attn::kBlockM, D, false, true, false);
+  p.k_lens = k_lens;
+  p.Nk = Nk;
+  p.col_blocks = nq;
+  attn::BwdParams pkv = p, pq = p;
+  pkv.N = Nk;
+  pkv.num_blocks = nk;
+  pkv.num_items = (int)(heads * nk);
+  pq.N = (int)GT;
+  pq.num_blocks = nq;
+  pq.num_items = (int)(heads * nq);
+
+  const long long rows = heads * p.Npad;
+  const long long rows_per_block = 256 / 16 * attn::kPrepRows;
+  attn::attn_bwd_prep<<<(unsigned)((rows + rows_per_block - 1) / rows_per_block), 256, 0, s>>>(
+      reinterpret_cast<const __nv_bfloat16*>(o), reinterpret_cast<const __nv_bfloat16*>(dout), lse, nlse2, ndelta,
+      rows, (int)GT, p.Npad, D);
+  switch (D) {
+    case 32: launch_cross_bwd_dim<32>(mq, mk, mv, mdo, pkv, pq, num_sms, s); break;
+    case 64: launch_cross_bwd_dim<64>(mq, mk, mv, mdo, pkv, pq, num_sms, s); break;
+    case 96: launch_cross_bwd_dim<96>(mq, mk, mv, mdo, pkv, pq, num_sms, s); break;
+    default: launch_cross_bwd_dim<128>(mq, mk, mv, mdo, pkv, pq, num_sms, s); break;
+  }
+  return launch_status("cross-attention backward kernel launch");
+}
+
+}  // extern "C"
