@@ -190,4 +190,25 @@ __global__ void __launch_bounds__(256) attn_cache_read_kernel(CacheView c, __nv_
   vo[1] = o[1][1];
 }
 
+// Two E4M3 codes in the high bytes of r's halves -> a bf16 pair (their low bytes are ignored).
+__device__ __forceinline__ uint32_t e4m3_hi2_to_bf16(uint32_t r) {
+  const uint32_t x = ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u);   // value * 2^-120
+  uint32_t y;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7b807b80u));  // 2^120
+  return y;
+}
+
+// An E8M0 factor as a bf16 pair, and four E4M3 codes times such a pair -> two bf16 pairs, exactly.
+__device__ __forceinline__ uint32_t e8_bf16x2(int e8) {
+  const uint32_t b = e8 == kE8Nan ? 0x7fc0u : e8 == 0 ? 0x0040u : (uint32_t)e8 << 7;
+  return b | (b << 16);
+}
+
+__device__ __forceinline__ uint2 e4m3x4_times(uint32_t w, uint32_t f) {
+  uint2 r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(e4m3_hi2_to_bf16(__byte_perm(w, 0u, 0x1000))), "r"(f));
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(e4m3_hi2_to_bf16(__byte_perm(w, 0u, 0x3020))), "r"(f));
+  return r;
+}
+
 }  // namespace attn

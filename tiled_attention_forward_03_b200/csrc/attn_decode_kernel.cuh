@@ -163,14 +163,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two E4M3 codes in the high bytes of r's halves -> a bf16 pair (their low bytes are ignored).
-__device__ __forceinline__ uint32_t e4m3_hi2_to_bf16(uint32_t r) {
-  const uint32_t x = ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u);   // value * 2^-120
-  uint32_t y;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7b807b80u));  // 2^120
-  return y;
-}
-
 template <int D, bool kF8>
 struct DecCfg {
   static constexpr int kElem = kF8 ? 1 : 2;
@@ -575,6 +567,7 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](const float* po, const float2* pml, long long at) {
       const float2 ml = pml[at];
+      if (ml.x == -INFINITY && ml.y == 0.f) return;   // no keys: nothing to add
       const float4 v = *reinterpret_cast<const float4*>(po + at * D + d);
       const float mn = fmaxf(m, ml.x);
       const float a = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_approx(m - mn);

@@ -5,6 +5,7 @@
 
 #include "attn_cache_kernel.cuh"
 #include "attn_decode_kernel.cuh"
+#include "attn_fwd_rows_kernel.cuh"
 
 namespace {
 
@@ -204,6 +205,230 @@ void fill_decode(attn::DecParams& p, const CacheArgs& a, const void* q, void* o,
   p.lse = lse;
 }
 
+// ---------------------------------------------------------------- many rows: the tensor-core kernel
+
+struct RowsDeviceInfo {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+RowsDeviceInfo g_rows_dev[kMaxDevices];
+
+template <int D>
+cudaError_t rows_setup_dim() {
+  cudaError_t e = cudaSuccess;
+  auto setup = [&](const void* fn, int regs) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, attn::CsPlan<D>::kAlloc);
+    cudaFuncAttributes fa{};
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, fn);
+    // the register split (setmaxnreg) needs exactly the launch allocation it was sized for
+    if (e == cudaSuccess && fa.numRegs != regs) e = cudaErrorInvalidDeviceFunction;
+  };
+  setup(reinterpret_cast<const void*>(attn::attn_fwd_rows_sm100<D, false, false>), attn::RowsCfg<false>::kRegsLaunch);
+  setup(reinterpret_cast<const void*>(attn::attn_fwd_rows_sm100<D, true, false>), attn::RowsCfg<false>::kRegsLaunch);
+  setup(reinterpret_cast<const void*>(attn::attn_fwd_rows_sm100<D, true, true>), attn::RowsCfg<true>::kRegsLaunch);
+  return e;
+}
+
+bool rows_device_setup() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevices)) e = cudaErrorInvalidDevice;
+  if (e != cudaSuccess) {
+    record_cuda_error("cudaGetDevice", e);
+    return false;
+  }
+  RowsDeviceInfo& d = g_rows_dev[dev];
+  std::call_once(d.once, [&d] {
+    cudaError_t x = rows_setup_dim<32>();
+    if (x == cudaSuccess) x = rows_setup_dim<64>();
+    if (x == cudaSuccess) x = rows_setup_dim<96>();
+    if (x == cudaSuccess) x = rows_setup_dim<128>();
+    d.err = x;
+  });
+  if (d.err == cudaSuccess) return true;
+  record_cuda_error("many-row kernel device setup", d.err);
+  return false;
+}
+
+// A bf16 tensor as TMA loads it: `rank` dimensions, D fastest, boxes of 64 columns and the given
+// extents with 128-byte swizzle; elements outside read as zero.
+int encode_rows_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint32_t* box) {
+  auto enc = tensor_map_encoder();
+  if (!enc) {
+    std::snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "cuTensorMapEncodeTiled entry point unavailable");
+    return ATTN_ERR_CUDA;
+  }
+  cuuint64_t strides[3];
+  cuuint64_t bytes = 2;
+  for (int i = 0; i + 1 < rank; ++i) strides[i] = bytes *= dims[i];
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r == CUDA_SUCCESS) return ATTN_OK;
+  record_driver_error("cuTensorMapEncodeTiled", (int)r);
+  return ATTN_ERR_CUDA;
+}
+
+// How many parts the keys of each tile are cut into, so that `units` tiles fill the GPU: the number
+// with the least estimated time, counted in 128-key blocks (about 1 us each): waves of units, each
+// its blocks and two more for its start and end, and four for the joining kernel where it is not
+// needed anyway.
+int rows_parts(long long units, long long blocks, int num_sms, bool parted) {
+  int best = 1;
+  double least = 0;
+  const long long most = blocks / 2 < 64 ? (blocks / 2 < 1 ? 1 : blocks / 2) : 64;
+  for (int n = 1; n <= most; ++n) {
+    const double waves = (double)((units * n + num_sms - 1) / num_sms);
+    const double cost = waves * ((double)((blocks + n - 1) / n) + 2) + (n > 1 && !parted ? 4 : 0);
+    if (n == 1 || cost < least) {
+      best = n;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+template <int D>
+void launch_rows_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
+                     const attn::RowsParams& p, bool part, bool f8, unsigned grid, cudaStream_t s) {
+  constexpr int smem = attn::CsPlan<D>::kAlloc;
+  if (f8)
+    attn::attn_fwd_rows_sm100<D, true, true><<<grid, attn::RowsCfg<true>::kThreads, smem, s>>>(mq, mk, mv, mo, p);
+  else if (part)
+    attn::attn_fwd_rows_sm100<D, true, false><<<grid, attn::RowsCfg<false>::kThreads, smem, s>>>(mq, mk, mv, mo, p);
+  else
+    attn::attn_fwd_rows_sm100<D, false, false><<<grid, attn::RowsCfg<false>::kThreads, smem, s>>>(mq, mk, mv, mo, p);
+}
+
+template <int D>
+void launch_rows_join_dim(const float* part_o, const float2* part_ml, int parts, long long rows, void* o, float* lse,
+                          cudaStream_t s) {
+  attn::attn_rows_join_kernel<D><<<(unsigned)((rows * (D / 4) + 255) / 256), 256, 0, s>>>(
+      part_o, part_ml, parts, rows, reinterpret_cast<__nv_bfloat16*>(o), lse);
+}
+
+// The tiles of a problem.
+struct RowsPlan {
+  int tiles, seqs = 1, seq_tiles = 1, parts = 1;
+  long long units = 0;             // without the parts
+  size_t part_o = 0, part_ml = 0;  // bytes
+  size_t bytes() const { return part_o + part_ml; }
+};
+
+RowsPlan rows_plan(int B, int Hkv, long long GT, int D, long long max_len, int num_sms, bool prefix) {
+  RowsPlan pl;
+  const long long blocks = (max_len + attn::kBlockN - 1) / attn::kBlockN;
+  const long long per_seq = (GT + attn::kBlockM - 1) / attn::kBlockM;
+  if (!prefix) {
+    pl.tiles = (int)per_seq;
+  } else if (GT <= attn::kBlockM) {
+    pl.seqs = (int)(attn::kBlockM / GT);
+    pl.tiles = (B + pl.seqs - 1) / pl.seqs;
+  } else {
+    pl.seq_tiles = (int)per_seq;
+    pl.tiles = (int)(B * per_seq);
+  }
+  pl.units = (long long)(prefix ? Hkv : (long long)B * Hkv) * pl.tiles;
+  pl.parts = rows_parts(pl.units, blocks, num_sms, prefix);
+  if (prefix || pl.parts > 1) {
+    const size_t rows = ((size_t)B * Hkv * (size_t)GT * pl.parts + 63) / 64 * 64;
+    pl.part_o = rows * D * sizeof(float);
+    pl.part_ml = rows * sizeof(float2);
+  }
+  return pl;
+}
+
+// Fills the sizes and launches; p's key, output and length fields are the caller's.
+int launch_rows(attn::RowsParams& p, const RowsPlan& pl, const void* q, const void* k, const void* v, void* o, int D,
+                bool prefix, bool f8, float scale, void* workspace, int num_sms, cudaStream_t s) {
+  if (!rows_device_setup()) return ATTN_ERR_CUDA;
+  p.tiles = pl.tiles;
+  p.parts = pl.parts;
+  p.seqs = pl.seqs;
+  p.seq_tiles = pl.seq_tiles;
+  p.prefix = prefix ? 1 : 0;
+  p.num_units = (int)(pl.units * pl.parts);
+  p.part_o = reinterpret_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + pl.part_o);
+  p.o = reinterpret_cast<__nv_bfloat16*>(o);
+  const bool many = prefix && pl.seq_tiles == 1;   // a tile holds whole sequences
+  p.q_box_rows = many ? p.GT * pl.seqs : attn::kBlockM;
+  // c > 0 always: masked scores are -inf and must stay so (scale == 0: every 2^(s c) is 1)
+  p.c = std::fmax(std::fabs(scale) * 1.44269504088896340736f, 1e-30f);
+  p.idesc_s = attn::idesc_bf16_f32(attn::kBlockM, attn::kBlockN, false, false, scale < 0.f);
+  p.idesc_pv = attn::idesc_bf16_f32(attn::kBlockM, D, false, true, false);
+  CUtensorMap mq, mk, mv, mo;
+  std::memset(&mk, 0, sizeof(mk));
+  std::memset(&mv, 0, sizeof(mv));
+  std::memset(&mo, 0, sizeof(mo));
+  int st;
+  const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)p.GT, (cuuint64_t)p.Hkv, (cuuint64_t)p.B};
+  const cuuint32_t qb[4] = {64, (cuuint32_t)(many ? p.GT : attn::kBlockM), 1, (cuuint32_t)pl.seqs};
+  if ((st = encode_rows_map(&mq, q, 4, qd, qb)) != ATTN_OK) return st;
+  p.box = attn::kBlockN;
+  if (p.table != nullptr)
+    while (p.page % p.box != 0) p.box /= 2;
+  if (!f8) {
+    const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)p.page, (cuuint64_t)p.num_pages * (cuuint64_t)p.Hkv};
+    const cuuint32_t kb[3] = {64, (cuuint32_t)p.box, 1};
+    if ((st = encode_rows_map(&mk, k, 3, kd, kb)) != ATTN_OK) return st;
+    if ((st = encode_rows_map(&mv, v, 3, kd, kb)) != ATTN_OK) return st;
+  }
+  const bool part = pl.part_o > 0;
+  if (!part && (st = encode_map_o(&mo, o, (long long)p.B * p.Hkv, p.GT, D)) != ATTN_OK) return st;
+  const unsigned grid = (unsigned)(p.num_units < num_sms ? p.num_units : num_sms);
+  switch (D) {
+    case 32: launch_rows_dim<32>(mq, mk, mv, mo, p, part, f8, grid, s); break;
+    case 64: launch_rows_dim<64>(mq, mk, mv, mo, p, part, f8, grid, s); break;
+    case 96: launch_rows_dim<96>(mq, mk, mv, mo, p, part, f8, grid, s); break;
+    default: launch_rows_dim<128>(mq, mk, mv, mo, p, part, f8, grid, s); break;
+  }
+  if ((st = launch_status("many-row kernel launch")) != ATTN_OK || prefix || !part) return st;
+  const long long rows = (long long)p.B * p.Hkv * p.GT;
+  switch (D) {
+    case 32: launch_rows_join_dim<32>(p.part_o, p.part_ml, pl.parts, rows, o, p.lse, s); break;
+    case 64: launch_rows_join_dim<64>(p.part_o, p.part_ml, pl.parts, rows, o, p.lse, s); break;
+    case 96: launch_rows_join_dim<96>(p.part_o, p.part_ml, pl.parts, rows, o, p.lse, s); break;
+    default: launch_rows_join_dim<128>(p.part_o, p.part_ml, pl.parts, rows, o, p.lse, s); break;
+  }
+  return launch_status("join kernel launch");
+}
+
+// At most this many rows go through the decode kernel; more, through the tensor-core kernel.
+constexpr int kFewRows = 32;
+
+// Shared prefix: the plans of its two kernels, and the workspace's layout (decode's part first).
+struct PrefixPlan {
+  bool here;        // the decode kernel computes the prefix too
+  DecPlan dec;
+  RowsPlan rows;
+  size_t bytes() const { return dec.bytes() + rows.bytes(); }
+};
+
+PrefixPlan prefix_plan(int B, int Hkv, long long GT, int D, int page, int max_pages, long long prefix_len,
+                       int num_sms) {
+  PrefixPlan pl;
+  pl.here = prefix_len > 0 && (long long)B * GT <= kFewRows;
+  pl.dec = dec_plan(B, Hkv, GT, D, cache_cap(page, max_pages), num_sms, true, pl.here, prefix_len);
+  if (prefix_len > 0 && !pl.here) pl.rows = rows_plan(B, Hkv, GT, D, prefix_len, num_sms, true);
+  return pl;
+}
+
+// Sizes of a cross-attention problem; query rows of a KV head in `GT`.
+int cross_size_checks(int B, int Hq, int Hkv, int Nq, int Nk, int D, float scale, long long* GT) {
+  if (B < 0 || Nq < 0 || Nk < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !std::isfinite(scale))
+    return ATTN_ERR_INVALID_ARG;
+  if (!narrow_head_dim(D)) return ATTN_ERR_UNSUPPORTED;
+  *GT = (long long)(Hq / Hkv) * Nq;
+  if ((long long)B * Hkv > 0x7fffffffLL || *GT > (1LL << 30) ||
+      (double)B * Hkv * ((double)*GT / 16 + 1) > 2147483647.0 ||
+      (double)B * Hkv * ((double)Nk / 128 + 1) > 1073741824.0)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -309,7 +534,7 @@ long long attn_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int T, 
   if (B == 0 || T == 0) return 0;
   int num_sms = 0;
   if (sm_count(&num_sms) != ATTN_OK) return -1;
-  return (long long)dec_plan(B, Hkv, GT, D, cache_cap(page_size, max_pages), num_sms, true, true, prefix_len).bytes();
+  return (long long)prefix_plan(B, Hkv, GT, D, page_size, max_pages, prefix_len, num_sms).bytes();
 }
 
 int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
@@ -329,54 +554,90 @@ int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cac
     return ATTN_ERR_MISALIGNED;
   int num_sms = 0;
   if ((st = sm_count(&num_sms)) != ATTN_OK) return st;
-  const DecPlan pl =
-      dec_plan(B, Hkv, GT, D, cache_cap(page_size, max_pages), num_sms, true, prefix_len > 0, prefix_len);
+  const PrefixPlan pl = prefix_plan(B, Hkv, GT, D, page_size, max_pages, prefix_len, num_sms);
   if (pl.bytes() > workspace_bytes || (pl.bytes() > 0 && !workspace)) return ATTN_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   attn::DecParams p;
   fill_decode(p, a, q, o, lse, T, GT, scale, 1);
-  p.prefix_table = prefix_table;
-  p.prefix_len = prefix_len;
-  p.prefix_pages = (prefix_len + page_size - 1) / page_size;
-  return launch_decode(p, pl, D, true, workspace, reinterpret_cast<cudaStream_t>(stream));
+  if (pl.here) {
+    p.prefix_table = prefix_table;
+    p.prefix_len = prefix_len;
+    p.prefix_pages = (prefix_len + page_size - 1) / page_size;
+  } else if (prefix_len > 0) {
+    // many rows: the prefix on the tensor-core kernel, its parts joined by the decode's second kernel
+    attn::RowsParams r;
+    std::memset(&r, 0, sizeof(r));
+    r.B = B;
+    r.Hkv = Hkv;
+    r.GT = (int)GT;
+    r.len_all = r.max_len = prefix_len;
+    r.table = prefix_table;
+    r.page = page_size;
+    r.num_pages = num_pages;
+    r.k = k_cache;
+    r.v = v_cache;
+    r.ks = p.ks;
+    r.vs = p.vs;
+    char* w = static_cast<char*>(workspace) + pl.dec.bytes();
+    if ((st = launch_rows(r, pl.rows, q, k_cache, v_cache, o, D, true, p.ks != nullptr, scale, w, num_sms, s)) !=
+        ATTN_OK)
+      return st;
+    p.prefix_splits = pl.rows.parts;
+    p.split_o = r.part_o;
+    p.split_ml = r.part_ml;
+  }
+  return launch_decode(p, pl.dec, D, true, workspace, s);
 }
 
 // ---------------------------------------------------------------- cross attention
 
 long long attn_fwd_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int D) {
-  if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Nq < 0 || Nk < 0 || !narrow_head_dim(D)) return -1;
-  const long long GT = (long long)(Hq / Hkv) * Nq;
+  long long GT = 0;
+  if (cross_size_checks(B, Hq, Hkv, Nq, Nk, D, 1.f, &GT) != ATTN_OK) return -1;
   if (B == 0 || Nq == 0) return 0;
   int num_sms = 0;
   if (sm_count(&num_sms) != ATTN_OK) return -1;
-  return (long long)dec_plan(B, Hkv, GT, D, Nk, num_sms, false, false, 0).bytes();
+  return (long long)(GT <= kFewRows || Nk == 0 ? dec_plan(B, Hkv, GT, D, Nk, num_sms, false, false, 0).bytes()
+                                               : rows_plan(B, Hkv, GT, D, Nk, num_sms, false).bytes());
 }
 
 int attn_fwd_cross(const void* q, const void* k, const void* v, const int* k_lens, void* o, float* lse, int B, int Hq,
                    int Hkv, int Nq, int Nk, int D, float scale, void* workspace, size_t workspace_bytes,
                    void* stream) {
-  if (B < 0 || Nq < 0 || Nk < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !std::isfinite(scale))
-    return ATTN_ERR_INVALID_ARG;
-  if (!narrow_head_dim(D)) return ATTN_ERR_UNSUPPORTED;
-  const long long GT = (long long)(Hq / Hkv) * Nq;
-  if ((long long)B * Hkv > 0x7fffffffLL || GT > (1LL << 30) ||
-      (double)B * Hkv * ((double)GT / 16 + 1) > 2147483647.0)
-    return ATTN_ERR_UNSUPPORTED;
+  long long GT = 0;
+  int st = cross_size_checks(B, Hq, Hkv, Nq, Nk, D, scale, &GT);
+  if (st != ATTN_OK) return st;
   if (B == 0 || Nq == 0) return ATTN_OK;
   if (!q || !o || !lse || (Nk > 0 && (!k || !v))) return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lse, 4) ||
       !aligned(k_lens, 4) || !aligned(workspace, 256))
     return ATTN_ERR_MISALIGNED;
-  int st, num_sms = 0;
+  int num_sms = 0;
   if ((st = sm_count(&num_sms)) != ATTN_OK) return st;
-  const DecPlan pl = dec_plan(B, Hkv, GT, D, Nk, num_sms, false, false, 0);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (GT <= kFewRows || Nk == 0) {
+    const DecPlan pl = dec_plan(B, Hkv, GT, D, Nk, num_sms, false, false, 0);
+    if (pl.bytes() > workspace_bytes || (pl.bytes() > 0 && !workspace)) return ATTN_ERR_INVALID_ARG;
+    // contiguous keys: sequence b is page b of Nk rows
+    const CacheArgs a{k, v, nullptr, nullptr, nullptr, k_lens, B, Hkv, D, B, Nk > 0 ? Nk : 1, 1};
+    attn::DecParams p;
+    fill_decode(p, a, q, o, lse, Nq, GT, scale, 0);
+    p.cap = p.len_all = Nk;
+    return launch_decode(p, pl, D, false, workspace, s);
+  }
+  const RowsPlan pl = rows_plan(B, Hkv, GT, D, Nk, num_sms, false);
   if (pl.bytes() > workspace_bytes || (pl.bytes() > 0 && !workspace)) return ATTN_ERR_INVALID_ARG;
-  // contiguous keys: sequence b is page b of Nk rows
-  const CacheArgs a{k, v, nullptr, nullptr, nullptr, k_lens, B, Hkv, D, B, Nk > 0 ? Nk : 1, 1};
-  attn::DecParams p;
-  fill_decode(p, a, q, o, lse, Nq, GT, scale, 0);
-  p.cap = Nk;
-  p.len_all = Nk;
-  return launch_decode(p, pl, D, false, workspace, reinterpret_cast<cudaStream_t>(stream));
+  attn::RowsParams r;
+  std::memset(&r, 0, sizeof(r));
+  r.lse = lse;
+  r.B = B;
+  r.Hkv = Hkv;
+  r.GT = (int)GT;
+  r.k_lens = k_lens;
+  r.len_all = r.max_len = Nk;
+  r.page = Nk;
+  r.num_pages = B;
+  return launch_rows(r, pl, q, k, v, o, D, false, false, scale, workspace, num_sms, s);
 }
 
 }  // extern "C"
@@ -431,19 +692,6 @@ void launch_cross_bwd_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CU
         <<<grid(pkv.num_items), attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, true>::kAlloc, s>>>(mk, mv, mq, mdo, pkv);
   attn::attn_bwd_sm100<D, false, true>
       <<<grid(pq.num_items), attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, false>::kAlloc, s>>>(mq, mdo, mk, mv, pq);
-}
-
-// Sizes of a cross-attention problem; query rows of a KV head in `GT`.
-int cross_size_checks(int B, int Hq, int Hkv, int Nq, int Nk, int D, float scale, long long* GT) {
-  if (B < 0 || Nq < 0 || Nk < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !std::isfinite(scale))
-    return ATTN_ERR_INVALID_ARG;
-  if (!narrow_head_dim(D)) return ATTN_ERR_UNSUPPORTED;
-  *GT = (long long)(Hq / Hkv) * Nq;
-  if ((long long)B * Hkv > 0x7fffffffLL || *GT > (1LL << 30) ||
-      (double)B * Hkv * ((double)*GT / 16 + 1) > 2147483647.0 ||
-      (double)B * Hkv * ((double)Nk / 128 + 1) > 1073741824.0)
-    return ATTN_ERR_UNSUPPORTED;
-  return ATTN_OK;
 }
 
 }  // namespace
