@@ -10,13 +10,16 @@
 // (E4M3): the kernel is bound by HBM, and is built to keep loads in flight and to touch each byte
 // once:
 //
-//  * Keys and values go from global memory straight into the registers that the tensor-core
-//    instruction (m16n8k16, 16 query rows) takes them from: no shared memory, no barriers, no
-//    transposition.  The K = 16 index of Q K^T may be any permutation of D as long as Q uses the same
-//    one, so a lane loads 16 contiguous bytes of its key's row and calls them its share of several K
-//    steps; likewise the N = 8 index of P V is any permutation of the output columns, so a lane
-//    loads 8 (bf16) or 16 (E4M3) contiguous columns of the four value rows that it holds as K index, and pairs two rows
-//    with one byte permutation per operand register.
+//  * Keys and values reach shared memory by TMA (128-byte swizzled rows) through rings of 8 KB
+//    stages, eight stages a CTA and three CTAs an SM: about 100 KB in flight while as much is
+//    computed on.  (Loads straight into registers, a first version, held 340 us for the 550 MB of
+//    B64 Hq32 Hkv8 N<=8192 D128 E4M3, the warps waiting for memory 70 % of the time.)
+//  * A lane reads its operands of the tensor-core instruction (m16n8k16, 16 query rows) as they lie:
+//    the K = 16 index of Q K^T may be any permutation of D as long as Q uses the same one, so a lane
+//    takes 16 contiguous bytes of its key's row for several K steps (pieces 2t, 2t+1 of a swizzled
+//    row: no bank conflicts); likewise the N = 8 index of P V is any permutation of the output
+//    columns, so a lane takes 16 bytes of the four value rows that it holds as K index, and pairs two
+//    rows with one byte permutation per operand register.  Nothing is transposed.
 //  * E4M3 codes become bf16 by moving their bits (sign, then exponent and mantissa 4 bits down: the
 //    value times 2^-120, exact for subnormal codes too) and one exact multiplication by 2^120.  A
 //    token's K exponent multiplies its scores in fp32, its V exponent its probability before that is
@@ -33,7 +36,8 @@
 // workspace: results depend on the inputs alone.
 //
 // A CTA's four warps take `row_tiles` tiles of 16 rows (1, 2 or 4) and share the keys 4 / row_tiles
-// ways; warps with the same keys meet in L1.  Their results are joined in shared memory.
+// ways; the warps of one way share its ring (a stage is refilled once all of them have left it).
+// Their results are joined in shared memory, in the ring's place.  Every wait is bounded.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -44,13 +48,17 @@ namespace attn {
 
 constexpr int kDecThreads = 128;
 constexpr int kDecBlock = 64;       // keys per block of the schedule
-constexpr int kDecMaxRows = 64;     // rows per row block: 4 tiles of 16
+constexpr int kDecStages = 8;       // of all the CTA's rings together
+constexpr int kDecStageBytes = 8192;
+
+enum : unsigned {
+  kSiteDecodeFull = 51,
+  kSiteDecodeEmpty = 52,
+};
 
 struct DecParams {
   const __nv_bfloat16* q;    // [B][Hkv][GT][D]
-  const void* k;             // [num_pages][Hkv][page][D]
-  const void* v;
-  const uint8_t* ks;
+  const uint8_t* ks;         // E4M3: exponents [num_pages][Hkv][page]
   const uint8_t* vs;
   const int* table;          // [B][max_pages], or null: sequence b is page b
   const int* lens;           // [B], or null: len_all
@@ -60,10 +68,12 @@ struct DecParams {
   int GT, T;                 // rows of a sequence and KV head; tokens (row i is token i % T)
   int causal;                // token t sees keys up to len - T + t
   FastDiv div_gt;
-  int row_tiles, row_blocks;            // per unit of a sequence
+  int row_tiles;                        // of a CTA
+  int row_blocks;                       // of a sequence
+  int box;                              // key rows of a TMA box: the step, or 16
   // shared prefix handled here (prefix_len > 0): an extra first sequence with all rows of the batch
   const int* prefix_table;
-  int prefix_len, prefix_pages, prefix_row_tiles, prefix_row_blocks;
+  int prefix_len, prefix_row_blocks;
   int whole_units;           // 1: CTAs take whole units only (every sequence is short)
   int min_share;             // blocks a CTA takes at least
   float c;                   // scale * log2(e)
@@ -166,13 +176,33 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
 template <int D, bool kF8>
 struct DecCfg {
   static constexpr int kElem = kF8 ? 1 : 2;
-  static constexpr int kGroups = (kF8 || D <= 64) ? 2 : 1;   // 16-key groups per warp step
+  static constexpr int kChunks = (D * kElem + 127) / 128;   // 128-byte pieces of a row
+  static constexpr int kGroups = 2 / kChunks;               // 16-key groups per step
   static constexpr int kStep = 16 * kGroups;
-  static constexpr int kKWords = D * kElem / 16;             // 32-bit words of a key a lane holds (1/4 of it)
-  static constexpr int kVWords = D * kElem / 32;             // of a value row (1/8 of it)
-  static constexpr bool kWideK = !kF8 || D % 64 == 0;        // 16-byte key pieces, else 8
-  static constexpr int kRowStride = D + 4;                   // floats, of a row staged in shared memory
+  static constexpr int kChunkBytes = kStep * 128;
+  static constexpr int kVOff = kChunks * kChunkBytes;       // V behind K in a stage
+  static_assert(2 * kVOff == kDecStageBytes, "a stage holds one step");
+  static constexpr int kKWords = D * kElem / 16;            // 32-bit words of a key a lane holds (1/4 of it)
+  static constexpr int kVWords = D * kElem / 32;            // of a value row (1/8 of it)
+  static constexpr int kRowStride = D + 4;                  // floats, of a row of the join
+  static constexpr int kJoinBytes = 4 * 16 * kRowStride * 4;
+  static_assert(kJoinBytes <= kDecStages * kDecStageBytes, "the join takes the rings' place");
 };
+constexpr int kDecSmem = kDecStages * kDecStageBytes + 1024;   // slack for 1024-byte alignment
+
+// Byte `b` of row `r` in a tile of 128-byte rows as TMA swizzles it.
+__device__ __forceinline__ uint32_t dec_sw(uint32_t r, uint32_t b) { return r * 128 + (b ^ ((r & 7) << 4)); }
+
+// First element of K step s's four in D that lane t holds: 16-byte pieces 2t, 2t+1 of a full
+// 128-byte row piece, piece t of half of one, 8-byte pieces where E4M3 rows are neither.
+template <int D, bool kF8>
+__device__ __forceinline__ constexpr int dec_koff(int s, int t) {
+  if (kF8 && D == 128) return 16 * (2 * t + s / 4) + 4 * (s % 4);
+  if (kF8 && D == 64) return 16 * t + 4 * s;
+  if (kF8) return 32 * (s / 2) + 8 * t + 4 * (s % 2);
+  const int i = s / 2, c = i / 2;   // 16-byte pieces of 8 elements, two to a lane and 64-element chunk
+  return (64 * c + 64 <= D) ? 64 * c + 8 * (2 * t + i % 2) + 4 * (s % 2) : 64 * c + 8 * t + 4 * (s % 2);
+}
 
 // Output column of operand register `ct` of P V (0 <= ct < D/8) for N index n (0..7): the columns a
 // lane loads contiguously.
@@ -182,56 +212,98 @@ __device__ __forceinline__ constexpr int dec_col(int ct, int n) {
   return ct < 8 * (D / 64) ? 64 * (ct / 8) + 8 * n + ct % 8 : 64 * (D / 64) + 4 * n + (ct - 8 * (D / 64));
 }
 
-// This lane's words of one value row (`row` points at its first byte; g = lane / 4).
+__device__ __forceinline__ void lds16(uint32_t* w, uint32_t addr) {
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+}
+__device__ __forceinline__ void lds8(uint32_t* w, uint32_t addr) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+__device__ __forceinline__ void lds4(uint32_t* w, uint32_t addr) {
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+}
+
+// Lane t's words of key row r in the K tile at `tile`: word order as dec_koff's steps.
 template <int D, bool kF8>
-__device__ __forceinline__ void dec_load_v(uint32_t (&w)[DecCfg<D, kF8>::kVWords], const uint8_t* row, int g) {
-  constexpr int kE = DecCfg<D, kF8>::kElem;
+__device__ __forceinline__ void dec_load_k(uint32_t (&w)[DecCfg<D, kF8>::kKWords], uint32_t tile, uint32_t r, uint32_t t) {
+  constexpr int kChunkBytes = DecCfg<D, kF8>::kChunkBytes;
+  if constexpr (kF8 && D % 64 != 0) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) lds8(w + 2 * i, tile + dec_sw(r, 32 * i + 8 * t));
+  } else {
+    constexpr int kRowBytes = D * DecCfg<D, kF8>::kElem;
+#pragma unroll
+    for (int c = 0; c < kRowBytes / 128; ++c) {
+      lds16(w + 8 * c, tile + c * kChunkBytes + dec_sw(r, 32 * t));
+      lds16(w + 8 * c + 4, tile + c * kChunkBytes + dec_sw(r, 32 * t + 16));
+    }
+    if constexpr (kRowBytes % 128 != 0)
+      lds16(w + 8 * (kRowBytes / 128), tile + (kRowBytes / 128) * kChunkBytes + dec_sw(r, 16 * t));
+  }
+}
+
+// Lane group g's words of value row r in the V tile at `tile`.
+template <int D, bool kF8>
+__device__ __forceinline__ void dec_load_v(uint32_t (&w)[DecCfg<D, kF8>::kVWords], uint32_t tile, uint32_t r, uint32_t g) {
+  constexpr int kChunkBytes = DecCfg<D, kF8>::kChunkBytes;
   if constexpr (kF8 && D == 128) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + 16 * g));
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    lds16(w, tile + dec_sw(r, 16 * g));
+  } else if constexpr (kF8) {
+    if constexpr (D >= 64) lds8(w, tile + dec_sw(r, 8 * g));
+    if constexpr (D % 64 != 0) lds4(w + 2 * (D / 64), tile + dec_sw(r, 64 * (D / 64) + 4 * g));
   } else {
 #pragma unroll
-    for (int c = 0; c < D / 64; ++c) {
-      if constexpr (kF8) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(row + 64 * c + 8 * g));
-        w[2 * c] = x.x, w[2 * c + 1] = x.y;
-      } else {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + 128 * c + 16 * g));
-        w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
-      }
-    }
-    if constexpr (D % 64 != 0) {
-      constexpr int c = D / 64;
-      if constexpr (kF8) {
-        w[2 * c] = __ldg(reinterpret_cast<const uint32_t*>(row + 64 * c + 4 * g));
-      } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(row + kE * 64 * c + 8 * g));
-        w[4 * c] = x.x, w[4 * c + 1] = x.y;
-      }
-    }
+    for (int c = 0; c < D / 64; ++c) lds16(w + 4 * c, tile + c * kChunkBytes + dec_sw(r, 16 * g));
+    if constexpr (D % 64 != 0) lds8(w + 4 * (D / 64), tile + (D / 64) * kChunkBytes + dec_sw(r, 8 * g));
   }
 }
 
 template <int D, bool kF8>
-__global__ void __launch_bounds__(kDecThreads, 3) attn_decode_kernel(const DecParams p) {
+__global__ void __launch_bounds__(kDecThreads, 3)
+    attn_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                       const DecParams p) {
   using Cfg = DecCfg<D, kF8>;
-  constexpr int G = Cfg::kGroups, KW = Cfg::kKWords, VW = Cfg::kVWords, kE = Cfg::kElem;
-  __shared__ __align__(16) float so[4][16][Cfg::kRowStride];
+  constexpr int G = Cfg::kGroups, KW = Cfg::kKWords, VW = Cfg::kVWords;
+  extern __shared__ uint8_t smem_raw[];
   __shared__ float2 sml[4][16];
   __shared__ long long scratch[16];
+  __shared__ uint64_t full[kDecStages], empty[kDecStages];
+  __shared__ uint32_t abort_word;
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  auto so = reinterpret_cast<float(*)[16][Cfg::kRowStride]>(smem);
+  volatile uint32_t* abort_flag = &abort_word;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int row_tiles = p.row_tiles;
+  const int kg = warp / row_tiles, rt = warp - kg * row_tiles, ways = 4 / row_tiles;
+  const int stages = kDecStages / ways;                 // of this way's ring
+  const uint32_t ring = smem_u32(smem) + kg * stages * kDecStageBytes;
+  uint64_t* ring_full = full + kg * stages;
+  uint64_t* ring_empty = empty + kg * stages;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kDecStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], row_tiles);
+    }
+    *abort_flag = 0u;
+    fence_mbar_init();
+    if (p.cap > 0 || p.prefix_len > 0) {   // (without any key there are no tensor maps)
+      tma_prefetch_desc(&tmap_k);
+      tma_prefetch_desc(&tmap_v);
+    }
+  }
 
   int seq;
   long long first;
-  const DecLine ln = dec_locate(p, gridDim.x, blockIdx.x, -1, scratch, seq, first);
+  const DecLine ln = dec_locate(p, gridDim.x, blockIdx.x, -1, scratch, seq, first);   // (its barriers order the above)
   const long long begin = (long long)blockIdx.x * ln.share, end = min(ln.total, begin + ln.share);
+  // ring positions: steps issued (the way's first warp) and left behind, over all units
+  uint32_t issued = 0u, done = 0u;
+  bool ok = true;
 
   for (long long x = begin; x < end;) {
     // ---- the unit at line position x, and the part of it in this CTA's range
     const bool prefix = seq < 0;
     const int len = prefix ? p.prefix_len : dec_len(p, seq);
     const int nblk = prefix ? (p.whole_units ? 1 : (len + kDecBlock - 1) / kDecBlock) : dec_blocks(p, len);
-    const int row_tiles = prefix ? p.prefix_row_tiles : p.row_tiles;
     const int row_blocks = prefix ? p.prefix_row_blocks : p.row_blocks;
     const int rows = prefix ? p.B * p.GT : p.GT;
     const int unit = (int)((x - first) / nblk);
@@ -239,8 +311,8 @@ __global__ void __launch_bounds__(kDecThreads, 3) attn_decode_kernel(const DecPa
     const int blk1 = (int)min((long long)nblk, blk0 + (end - x));
     const int h = unit / row_blocks, rb = unit - h * row_blocks;
     const int* table = prefix ? p.prefix_table : (p.table ? p.table + (size_t)seq * p.max_pages : nullptr);
-    const int kg = warp / row_tiles, ways = 4 / row_tiles;
-    const int i0 = rb * 16 * row_tiles + (warp - kg * row_tiles) * 16;   // first row of this warp's tile
+    const int i0 = rb * 16 * row_tiles + rt * 16;   // first row of this warp's tile
+    const int key_begin = p.whole_units ? 0 : blk0 * kDecBlock;
     const int key_end = p.whole_units ? len : (int)min((long long)len, (long long)blk1 * kDecBlock);
 
     // row i of the unit -> its index in q, o, lse
@@ -249,152 +321,161 @@ __global__ void __launch_bounds__(kDecThreads, 3) attn_decode_kernel(const DecPa
       const uint32_t b = fast_div((uint32_t)i, p.div_gt);
       return ((long long)b * p.Hkv + h) * p.GT + (i - (int)b * p.GT);
     };
+    // this way's steps: keys key_begin + (kg + ways * n) * kStep
+    const int stride = ways * Cfg::kStep;
+    const int k_first = key_begin + kg * Cfg::kStep;
+    const int steps = k_first < key_end ? (key_end - k_first + stride - 1) / stride : 0;
+    // key position k -> (page's plane in the tensor maps, row in the page); no page: plane past the end
+    auto place = [&](int k, int& plane, int& row) {
+      const uint32_t pg = fast_div((uint32_t)k, p.div_page);
+      const int id = table ? __ldg(table + pg) : seq;
+      row = k - (int)(pg * (uint32_t)p.page);
+      plane = (unsigned)id < (unsigned)p.num_pages ? id * p.Hkv + h : p.num_pages * p.Hkv;
+    };
+    // Loads of step n (one lane): boxes with a key only.
+    auto issue = [&](int n) {
+      const uint32_t st = issued % (uint32_t)stages;
+      const int k = k_first + n * stride;
+      const int boxes = min(Cfg::kStep / p.box, (key_end - k + p.box - 1) / p.box);
+      mbar_arrive_expect_tx(&ring_full[st], (uint32_t)(2 * Cfg::kChunks * boxes * p.box * 128));
+      for (int i = 0; i < boxes; ++i) {
+        int plane, row;
+        place(k + i * p.box, plane, row);
+#pragma unroll
+        for (int c = 0; c < Cfg::kChunks; ++c) {
+          uint8_t* dst = smem + (kg * stages + st) * kDecStageBytes + c * Cfg::kChunkBytes + i * p.box * 128;
+          tma_load_3d(dst, &tmap_k, &ring_full[st], c * (128 / Cfg::kElem), row, plane, l2_policy_evict_first());
+          tma_load_3d(dst + Cfg::kVOff, &tmap_v, &ring_full[st], c * (128 / Cfg::kElem), row, plane,
+                      l2_policy_evict_first());
+        }
+      }
+    };
+    const bool issuer = rt == 0 && lane == 0;
+    if (issuer && ok)
+      for (int n = 0; n < min(stages - 1, steps) && ok; ++n) {
+        if (issued >= (uint32_t)stages)
+          ok = wait_phase(&ring_empty[issued % (uint32_t)stages], (issued / (uint32_t)stages - 1u) & 1u, abort_flag,
+                          kSiteDecodeEmpty);
+        if (!ok) break;
+        issue(n);
+        ++issued;
+      }
+    ok = __all_sync(0xffffffffu, ok);
+
     float o[D / 8][4];
 #pragma unroll
     for (int ct = 0; ct < D / 8; ++ct)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[ct][e] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    const bool active = i0 < rows;   // (a tile past the rows only keeps the ring going)
 
-    if (i0 < rows) {
-      // Q as the A operand of Q K^T: words 2s, 2s+1 of a row are K step s
-      uint32_t q0[2 * (D / 16)], q1[2 * (D / 16)];
+    // Q as the A operand of Q K^T: words 2s, 2s+1 of a row are K step s
+    uint32_t q0[2 * (D / 16)], q1[2 * (D / 16)];
+    {
       const bool r0 = i0 + g < rows, r1 = i0 + g + 8 < rows;
       const __nv_bfloat16* qa = p.q + (r0 ? row_index(i0 + g) : 0) * D;
       const __nv_bfloat16* qb = p.q + (r1 ? row_index(i0 + g + 8) : 0) * D;
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
-        const int off = (kF8 && Cfg::kWideK) ? 64 * (s / 4) + 16 * t4 + 4 * (s % 4) : 32 * (s / 2) + 8 * t4 + 4 * (s % 2);
+        const int off = dec_koff<D, kF8>(s, t4);
         const uint2 a = r0 ? __ldg(reinterpret_cast<const uint2*>(qa + off)) : make_uint2(0u, 0u);
         const uint2 b = r1 ? __ldg(reinterpret_cast<const uint2*>(qb + off)) : make_uint2(0u, 0u);
         q0[2 * s] = a.x, q0[2 * s + 1] = a.y;
         q1[2 * s] = b.x, q1[2 * s + 1] = b.y;
       }
-      // keys below the limits are seen by rows g and g + 8 of the tile
-      int lim0 = len, lim1 = len, lim_min = len;
-      if (p.causal && !prefix) {
-        lim0 = len - p.T + 1 + (i0 + g) % p.T;
-        lim1 = len - p.T + 1 + (i0 + g + 8) % p.T;
-        lim_min = len - p.T + 1;
-      }
-
-      // 16-key group at key k: its first row in the cache (elements / D), or -1 where there is none
-      auto group_row = [&](int k) -> long long {
-        if (k >= key_end) return -1;
-        const uint32_t pg = fast_div((uint32_t)k, p.div_page);
-        const int id = table ? __ldg(table + pg) : seq;
-        if ((unsigned)id >= (unsigned)p.num_pages) return -1;
-        return ((long long)id * p.Hkv + h) * p.page + (k - (int)(pg * (uint32_t)p.page));
-      };
-      uint32_t kr[G][2][KW], vr[G][4][VW];
-      uint32_t sk[G][2], sv[G][2];    // E4M3: exponent bytes of keys 2t, 2t+1 of each half group
-      auto load_k = [&](int k, const long long (&base)[G]) {
+    }
+    // keys below the limits are seen by rows g and g + 8 of the tile
+    int lim0 = len, lim1 = len, lim_min = len;
+    if (p.causal && !prefix) {
+      lim0 = len - p.T + 1 + (i0 + g) % p.T;
+      lim1 = len - p.T + 1 + (i0 + g + 8) % p.T;
+      lim_min = len - p.T + 1;
+    }
+    // E4M3: exponent bytes of keys 2t, 2t+1 of each half group of a step (1 for no page: zero rows)
+    uint32_t sk[G][2], sv[G][2];
+    auto load_scales = [&](int n) {
+      if constexpr (kF8) {
+        const int k = k_first + n * stride;
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) sk[gr][j] = sv[gr][j] = 0x7f7fu;
+          if (n >= steps || k + 16 * gr >= key_end) continue;
+          int plane, row;
+          place(k + 16 * gr, plane, row);
+          if (plane >= p.num_pages * p.Hkv) continue;
+          const long long e = (long long)plane * p.page + row + 2 * t4;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int w = 0; w < KW; ++w) kr[gr][j][w] = 0u;
-            sk[gr][j] = sv[gr][j] = 0u;
-            if (base[gr] < 0) continue;
-            // a key past the end reads the last one's row: it is masked, and its memory is not ours
-            const int last = len - 1 - (k + 16 * gr);
-            const uint8_t* row = static_cast<const uint8_t*>(p.k) + (base[gr] + min(8 * j + g, last)) * (D * kE);
-            if constexpr (Cfg::kWideK) {
-#pragma unroll
-              for (int i = 0; i < KW / 4; ++i) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + 64 * i + 16 * t4));
-                kr[gr][j][4 * i] = w.x, kr[gr][j][4 * i + 1] = w.y, kr[gr][j][4 * i + 2] = w.z, kr[gr][j][4 * i + 3] = w.w;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < KW / 2; ++i) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + 32 * i + 8 * t4));
-                kr[gr][j][2 * i] = w.x, kr[gr][j][2 * i + 1] = w.y;
-              }
-            }
-            if constexpr (kF8) {
-              const long long e = base[gr] + 8 * j + 2 * t4;
-              sk[gr][j] = __ldg(reinterpret_cast<const uint16_t*>(p.ks + e));
-              sv[gr][j] = __ldg(reinterpret_cast<const uint16_t*>(p.vs + e));
-            }
+            sk[gr][j] = __ldg(reinterpret_cast<const uint16_t*>(p.ks + e + 8 * j));
+            sv[gr][j] = __ldg(reinterpret_cast<const uint16_t*>(p.vs + e + 8 * j));
           }
         }
-      };
-      auto load_v = [&](int k, const long long (&base)[G]) {
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-#pragma unroll
-            for (int w = 0; w < VW; ++w) vr[gr][e][w] = 0u;
-            if (base[gr] < 0) continue;
-            const int last = len - 1 - (k + 16 * gr);
-            const int j = 2 * t4 + (e & 1) + 8 * (e >> 1);
-            dec_load_v<D, kF8>(vr[gr][e], static_cast<const uint8_t*>(p.v) + (base[gr] + min(j, last)) * (D * kE), g);
-          }
-        }
-      };
+      }
+    };
+    load_scales(0);
 
-      const int stride = ways * Cfg::kStep;
-      int k = (p.whole_units ? 0 : blk0 * kDecBlock) + kg * Cfg::kStep;
-      long long base[G], next[G];
-#pragma unroll
-      for (int gr = 0; gr < G; ++gr) base[gr] = group_row(k + 16 * gr);
-      if (k < key_end) load_k(k, base);
-      for (; k < key_end; k += stride) {
-        load_v(k, base);
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) next[gr] = k < 0x7fffffff - stride - 64 ? group_row(k + stride + 16 * gr) : -1;
+    for (int n = 0; n < steps && ok; ++n, ++done) {
+      const int k = k_first + n * stride;
+      if (issuer && n + stages - 1 < steps) {
+        // the stage of the step before last is free once the way's warps have left it
+        if (issued >= (uint32_t)stages)
+          ok = wait_phase(&ring_empty[issued % (uint32_t)stages], (issued / (uint32_t)stages - 1u) & 1u, abort_flag,
+                          kSiteDecodeEmpty);
+        if (ok) {
+          issue(n + stages - 1);
+          ++issued;
+        }
+      }
+      const uint32_t st = done % (uint32_t)stages;
+      ok = wait_phase(&ring_full[st], (done / (uint32_t)stages) & 1u, abort_flag, kSiteDecodeFull) && ok;
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (active) {
+        const uint32_t tile_k = ring + st * kDecStageBytes, tile_v = tile_k + Cfg::kVOff;
         // S = Q K^T
         float s[G][2][4];
-        uint32_t se[G][2], ve[G][2];
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
+            uint32_t kw[KW];
+            dec_load_k<D, kF8>(kw, tile_k, 16 * gr + 8 * j + g, t4);
             s[gr][j][0] = s[gr][j][1] = s[gr][j][2] = s[gr][j][3] = 0.f;
-            se[gr][j] = sk[gr][j];
-            ve[gr][j] = sv[gr][j];
 #pragma unroll
-            for (int st = 0; st < D / 16; ++st) {
-              const uint32_t a[4] = {q0[2 * st], q1[2 * st], q0[2 * st + 1], q1[2 * st + 1]};
+            for (int q = 0; q < D / 16; ++q) {
+              const uint32_t a[4] = {q0[2 * q], q1[2 * q], q0[2 * q + 1], q1[2 * q + 1]};
               if constexpr (kF8) {
-                const uint32_t w = kr[gr][j][st];
-                mma_16816(s[gr][j], a, e4m3_hi2_to_bf16(__byte_perm(w, 0u, 0x1000)),
-                          e4m3_hi2_to_bf16(__byte_perm(w, 0u, 0x3020)));
+                mma_16816(s[gr][j], a, e4m3_hi2_to_bf16(__byte_perm(kw[q], 0u, 0x1000)),
+                          e4m3_hi2_to_bf16(__byte_perm(kw[q], 0u, 0x3020)));
               } else {
-                mma_16816(s[gr][j], a, kr[gr][j][2 * st], kr[gr][j][2 * st + 1]);
+                mma_16816(s[gr][j], a, kw[2 * q], kw[2 * q + 1]);
               }
             }
           }
         }
-        // the keys' registers are free: the next step's loads go out before this one's softmax
-        if (k < key_end - stride) load_k(k + stride, next);
         float f[G][4];   // E4M3: factor of P for keys 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if constexpr (kF8) {
-              const float c0 = p.c * e8_scale((int)(se[gr][j] & 255u)), c1 = p.c * e8_scale((int)(se[gr][j] >> 8));
+              const float c0 = p.c * e8_scale((int)(sk[gr][j] & 255u)), c1 = p.c * e8_scale((int)(sk[gr][j] >> 8));
               s[gr][j][0] *= c0;
               s[gr][j][1] *= c1;
               s[gr][j][2] *= c0;
               s[gr][j][3] *= c1;
-              f[gr][2 * j] = e8_scale((int)(ve[gr][j] & 255u));
-              f[gr][2 * j + 1] = e8_scale((int)(ve[gr][j] >> 8));
-              if (base[gr] < 0) {   // no page: zero keys and values, whatever the exponents
-                s[gr][j][0] = s[gr][j][1] = s[gr][j][2] = s[gr][j][3] = 0.f;
-                f[gr][2 * j] = f[gr][2 * j + 1] = 0.f;
-              }
+              f[gr][2 * j] = e8_scale((int)(sv[gr][j] & 255u));
+              f[gr][2 * j + 1] = e8_scale((int)(sv[gr][j] >> 8));
             } else {
 #pragma unroll
               for (int e = 0; e < 4; ++e) s[gr][j][e] *= p.c;
             }
           }
         }
-        if (k + Cfg::kStep > lim_min || k + Cfg::kStep > key_end) {
+        load_scales(n + 1);
+        const bool tail = k + Cfg::kStep > key_end;
+        if (tail || k + Cfg::kStep > lim_min) {
 #pragma unroll
           for (int gr = 0; gr < G; ++gr)
 #pragma unroll
@@ -452,29 +533,44 @@ __global__ void __launch_bounds__(kDecThreads, 3) attn_decode_kernel(const DecPa
             }
           }
           // O += P V
+          uint32_t vr[4][VW];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 16 * gr + 2 * t4 + (e & 1) + 8 * (e >> 1);
+            dec_load_v<D, kF8>(vr[e], tile_v, j, g);
+            if (tail && k + j >= key_end) {   // not a key: its row may hold anything, and 0 * NaN would stay
+#pragma unroll
+              for (int w = 0; w < VW; ++w) vr[e][w] = 0u;
+            }
+          }
 #pragma unroll
           for (int ct = 0; ct < D / 8; ++ct) {
             uint32_t b0, b1;
             if constexpr (kF8) {
               const int w = ct / 4;
               const uint32_t sel = ((uint32_t)(4 + ct % 4) << 12) | ((uint32_t)(ct % 4) << 4);
-              b0 = e4m3_hi2_to_bf16(__byte_perm(vr[gr][0][w], vr[gr][1][w], sel));
-              b1 = e4m3_hi2_to_bf16(__byte_perm(vr[gr][2][w], vr[gr][3][w], sel));
+              b0 = e4m3_hi2_to_bf16(__byte_perm(vr[0][w], vr[1][w], sel));
+              b1 = e4m3_hi2_to_bf16(__byte_perm(vr[2][w], vr[3][w], sel));
             } else {
               const uint32_t sel = (ct & 1) ? 0x7632u : 0x5410u;
-              b0 = __byte_perm(vr[gr][0][ct / 2], vr[gr][1][ct / 2], sel);
-              b1 = __byte_perm(vr[gr][2][ct / 2], vr[gr][3][ct / 2], sel);
+              b0 = __byte_perm(vr[0][ct / 2], vr[1][ct / 2], sel);
+              b1 = __byte_perm(vr[2][ct / 2], vr[3][ct / 2], sel);
             }
             mma_16816(o[ct], a, b0, b1);
           }
         }
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) base[gr] = next[gr];
       }
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-      l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring_empty[st]);   // this warp has left the stage
+    }
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    // all rings are empty: the join may take their place, unless a wait gave up
+    if (__syncthreads_or(!ok)) {
+      ok = false;
+      break;
     }
 
     // ---- join the warps' results, and write the unit out or its part to a slot
@@ -524,6 +620,7 @@ __global__ void __launch_bounds__(kDecThreads, 3) attn_decode_kernel(const DecPa
         if (d == 0) (whole ? p.area_ml[prefix] : p.slot_ml)[at] = make_float2(mt, lt);
       }
     }
+    fence_proxy_async_smem();   // the next unit's copies follow these accesses
     __syncthreads();
 
     // ---- the next unit
@@ -534,6 +631,10 @@ __global__ void __launch_bounds__(kDecThreads, 3) attn_decode_kernel(const DecPa
       ++seq;
     }
   }
+  // Drain after a wait gave up: every issued copy lands before the CTA exits.
+  if (!ok && rt == 0 && lane == 0)
+    for (uint32_t i = issued > (uint32_t)stages ? issued - (uint32_t)stages : 0u; i < issued; ++i)
+      drain_phase(&ring_full[i % (uint32_t)stages], (i / (uint32_t)stages) & 1u, abort_flag);
 }
 
 // Joins the parts of every split unit in key order, and, behind a shared prefix (area_o set), the
@@ -590,7 +691,7 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
         add(p.slot_o, p.slot_ml, (2 * c + ((c == f && a0 != c * ln.share) ? 1 : 0)) * p.slot_rows + slot_row);
     };
     if (p.prefix_len > 0) {
-      const int pr = b * p.GT + i, per = 16 * p.prefix_row_tiles;
+      const int pr = b * p.GT + i, per = 16 * p.row_tiles;
       const long long a0 = ((long long)h * p.prefix_row_blocks + pr / per) * pre_nblk;
       add_unit(a0, a0 + pre_nblk, 1, pr % per);
     }

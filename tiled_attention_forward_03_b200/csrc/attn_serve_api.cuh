@@ -57,11 +57,37 @@ int launch_status(const char* what) {
   return ATTN_ERR_CUDA;
 }
 
+// A tensor of bf16 (elem_bytes 2) or E4M3 bytes (1) as TMA loads it: `rank` dimensions, D fastest,
+// boxes of 128 bytes of D and the given extents with 128-byte swizzle; elements outside read as zero.
+int encode_rows_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint32_t* box,
+                    int elem_bytes = 2) {
+  auto enc = tensor_map_encoder();
+  if (!enc) {
+    std::snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "cuTensorMapEncodeTiled entry point unavailable");
+    return ATTN_ERR_CUDA;
+  }
+  cuuint64_t strides[3];
+  cuuint64_t bytes = (cuuint64_t)elem_bytes;
+  for (int i = 0; i + 1 < rank; ++i) strides[i] = bytes *= dims[i];
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(map, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r == CUDA_SUCCESS) return ATTN_OK;
+  record_driver_error("cuTensorMapEncodeTiled", (int)r);
+  return ATTN_ERR_CUDA;
+}
+
 // ---------------------------------------------------------------- decode schedule
 
 // Few rows over long keys: how attn_decode_kernel is launched, and its workspace.
+struct DecodeDeviceInfo {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+};
+
 struct DecPlan {
-  int row_tiles, row_blocks, prefix_row_tiles = 1, prefix_row_blocks = 0;
+  int row_tiles, row_blocks, prefix_row_blocks = 0;
   int whole_units;
   unsigned grid;
   bool join;                 // the second kernel is needed
@@ -84,15 +110,14 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   DecPlan pl;
   const long long cap_blocks = cap > 0 ? (cap + attn::kDecBlock - 1) / attn::kDecBlock : 1;
   const long long pre_blocks = (prefix_len + attn::kDecBlock - 1) / attn::kDecBlock;
-  pl.row_tiles = dec_row_tiles(GT);
+  pl.row_tiles = dec_row_tiles(prefix_here ? (long long)B * GT : GT);
   pl.row_blocks = (int)((GT + 16 * pl.row_tiles - 1) / (16 * pl.row_tiles));
   long long units = (long long)B * Hkv * pl.row_blocks;
   double blocks = (double)units * (double)cap_blocks;
   bool split = cap_blocks > kDecShortBlocks;
   if (prefix_here) {
     const long long rows = (long long)B * GT;
-    pl.prefix_row_tiles = dec_row_tiles(rows);
-    pl.prefix_row_blocks = (int)((rows + 16 * pl.prefix_row_tiles - 1) / (16 * pl.prefix_row_tiles));
+    pl.prefix_row_blocks = (int)((rows + 16 * pl.row_tiles - 1) / (16 * pl.row_tiles));
     blocks += (double)Hkv * pl.prefix_row_blocks * (double)pre_blocks;
     units += (long long)Hkv * pl.prefix_row_blocks;
     split = split || pre_blocks > kDecShortBlocks;
@@ -103,7 +128,7 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   pl.grid = (unsigned)(most < (double)ctas ? (long long)most : ctas);
   if (pl.grid < 1) pl.grid = 1;
   pl.join = split || shared;
-  const int slot_rows = 16 * (pl.row_tiles > pl.prefix_row_tiles ? pl.row_tiles : pl.prefix_row_tiles);
+  const int slot_rows = 16 * pl.row_tiles;
   const size_t slots = split ? 2 * (size_t)pl.grid * slot_rows : 0;
   pl.slot_o = slots * D * sizeof(float);
   pl.slot_ml = slots * sizeof(float2);
@@ -113,26 +138,53 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   return pl;
 }
 
-template <int D>
-void launch_decode_dim(const attn::DecParams& p, const DecPlan& pl, bool f8, cudaStream_t s) {
-  if (f8)
-    attn::attn_decode_kernel<D, true><<<pl.grid, attn::kDecThreads, 0, s>>>(p);
-  else
-    attn::attn_decode_kernel<D, false><<<pl.grid, attn::kDecThreads, 0, s>>>(p);
+template <int D, bool kF8>
+int launch_decode_dim(attn::DecParams& p, const DecPlan& pl, const void* k, const void* v, cudaStream_t s) {
+  using Cfg = attn::DecCfg<D, kF8>;
+  static DecodeDeviceInfo info[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevices)) e = cudaErrorInvalidDevice;
+  if (e == cudaSuccess) {
+    std::call_once(info[dev].once, [&] {
+      info[dev].err = cudaFuncSetAttribute(reinterpret_cast<const void*>(attn::attn_decode_kernel<D, kF8>),
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, attn::kDecSmem);
+    });
+    e = info[dev].err;
+  }
+  if (e != cudaSuccess) {
+    record_cuda_error("decode device setup", e);
+    return ATTN_ERR_CUDA;
+  }
+  // boxes of a whole step where pages hold whole steps (contiguous keys are one page), else of 16 keys
+  p.box = (p.table == nullptr || p.page % Cfg::kStep == 0) ? Cfg::kStep : 16;
+  CUtensorMap mk, mv;
+  int st;
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.page, (cuuint64_t)p.num_pages * (cuuint64_t)p.Hkv};
+  const cuuint32_t box[3] = {(cuuint32_t)(128 / Cfg::kElem), (cuuint32_t)p.box, 1};
+  if (p.cap > 0 || p.prefix_len > 0) {
+    if ((st = encode_rows_map(&mk, k, 3, dims, box, Cfg::kElem)) != ATTN_OK) return st;
+    if ((st = encode_rows_map(&mv, v, 3, dims, box, Cfg::kElem)) != ATTN_OK) return st;
+  } else {   // no keys at all: nothing is loaded
+    std::memset(&mk, 0, sizeof(mk));
+    std::memset(&mv, 0, sizeof(mv));
+  }
+  attn::attn_decode_kernel<D, kF8><<<pl.grid, attn::kDecThreads, attn::kDecSmem, s>>>(mk, mv, p);
   if (pl.join)
     attn::attn_decode_join_kernel<D>
         <<<(unsigned)((long long)p.B * p.Hkv * p.row_blocks), attn::kDecThreads, 0, s>>>(p, pl.grid);
+  return launch_status("decode kernel launch");
 }
 
 // Fills the schedule and workspace part of `p` and launches.
-int launch_decode(attn::DecParams& p, const DecPlan& pl, int D, bool shared, void* workspace, cudaStream_t s) {
+int launch_decode(attn::DecParams& p, const DecPlan& pl, const void* k, const void* v, int D, bool shared,
+                  void* workspace, cudaStream_t s) {
   p.row_tiles = pl.row_tiles;
   p.row_blocks = pl.row_blocks;
-  p.prefix_row_tiles = pl.prefix_row_tiles;
   p.prefix_row_blocks = pl.prefix_row_blocks;
   p.whole_units = pl.whole_units;
   p.min_share = pl.whole_units ? 1 : kDecMinShare;
-  p.slot_rows = 16 * (pl.row_tiles > pl.prefix_row_tiles ? pl.row_tiles : pl.prefix_row_tiles);
+  p.slot_rows = 16 * pl.row_tiles;
   char* w = static_cast<char*>(workspace);
   p.slot_o = reinterpret_cast<float*>(w);
   p.slot_ml = reinterpret_cast<float2*>(w + pl.slot_o);
@@ -142,13 +194,13 @@ int launch_decode(attn::DecParams& p, const DecPlan& pl, int D, bool shared, voi
     p.area_ml[i] = shared ? reinterpret_cast<float2*>(w + pl.area_o) : nullptr;
     w += pl.area_o + pl.area_ml;
   }
+  const bool f8 = p.ks != nullptr;
   switch (D) {
-    case 32: launch_decode_dim<32>(p, pl, p.ks != nullptr, s); break;
-    case 64: launch_decode_dim<64>(p, pl, p.ks != nullptr, s); break;
-    case 96: launch_decode_dim<96>(p, pl, p.ks != nullptr, s); break;
-    default: launch_decode_dim<128>(p, pl, p.ks != nullptr, s); break;
+    case 32: return f8 ? launch_decode_dim<32, true>(p, pl, k, v, s) : launch_decode_dim<32, false>(p, pl, k, v, s);
+    case 64: return f8 ? launch_decode_dim<64, true>(p, pl, k, v, s) : launch_decode_dim<64, false>(p, pl, k, v, s);
+    case 96: return f8 ? launch_decode_dim<96, true>(p, pl, k, v, s) : launch_decode_dim<96, false>(p, pl, k, v, s);
+    default: return f8 ? launch_decode_dim<128, true>(p, pl, k, v, s) : launch_decode_dim<128, false>(p, pl, k, v, s);
   }
-  return launch_status("decode kernel launch");
 }
 
 // Sizes common to decode and shared prefix; rows of a KV head in `GT`.
@@ -183,8 +235,6 @@ void fill_decode(attn::DecParams& p, const CacheArgs& a, const void* q, void* o,
                  float scale, int causal) {
   std::memset(&p, 0, sizeof(p));
   p.q = reinterpret_cast<const __nv_bfloat16*>(q);
-  p.k = a.k;
-  p.v = a.v;
   p.ks = static_cast<const uint8_t*>(a.ks);
   p.vs = static_cast<const uint8_t*>(a.vs);
   p.table = a.table;
@@ -249,26 +299,6 @@ bool rows_device_setup() {
   if (d.err == cudaSuccess) return true;
   record_cuda_error("many-row kernel device setup", d.err);
   return false;
-}
-
-// A bf16 tensor as TMA loads it: `rank` dimensions, D fastest, boxes of 64 columns and the given
-// extents with 128-byte swizzle; elements outside read as zero.
-int encode_rows_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint32_t* box) {
-  auto enc = tensor_map_encoder();
-  if (!enc) {
-    std::snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "cuTensorMapEncodeTiled entry point unavailable");
-    return ATTN_ERR_CUDA;
-  }
-  cuuint64_t strides[3];
-  cuuint64_t bytes = 2;
-  for (int i = 0; i + 1 < rank; ++i) strides[i] = bytes *= dims[i];
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r == CUDA_SUCCESS) return ATTN_OK;
-  record_driver_error("cuTensorMapEncodeTiled", (int)r);
-  return ATTN_ERR_CUDA;
 }
 
 // How many parts the keys of each tile are cut into, so that `units` tiles fill the GPU: the number
@@ -523,7 +553,7 @@ int attn_fwd_decode(const void* q, const void* k_cache, const void* v_cache, con
   if (pl.bytes() > workspace_bytes || (pl.bytes() > 0 && !workspace)) return ATTN_ERR_INVALID_ARG;
   attn::DecParams p;
   fill_decode(p, a, q, o, lse, T, GT, scale, 1);
-  return launch_decode(p, pl, D, false, workspace, reinterpret_cast<cudaStream_t>(stream));
+  return launch_decode(p, pl, k_cache, v_cache, D, false, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 long long attn_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int page_size, int max_pages,
@@ -562,7 +592,6 @@ int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cac
   if (pl.here) {
     p.prefix_table = prefix_table;
     p.prefix_len = prefix_len;
-    p.prefix_pages = (prefix_len + page_size - 1) / page_size;
   } else if (prefix_len > 0) {
     // many rows: the prefix on the tensor-core kernel, its parts joined by the decode's second kernel
     attn::RowsParams r;
@@ -586,7 +615,7 @@ int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cac
     p.split_o = r.part_o;
     p.split_ml = r.part_ml;
   }
-  return launch_decode(p, pl.dec, D, true, workspace, s);
+  return launch_decode(p, pl.dec, k_cache, v_cache, D, true, workspace, s);
 }
 
 // ---------------------------------------------------------------- cross attention
@@ -623,7 +652,7 @@ int attn_fwd_cross(const void* q, const void* k, const void* v, const int* k_len
     attn::DecParams p;
     fill_decode(p, a, q, o, lse, Nq, GT, scale, 0);
     p.cap = p.len_all = Nk;
-    return launch_decode(p, pl, D, false, workspace, s);
+    return launch_decode(p, pl, k, v, D, false, workspace, s);
   }
   const RowsPlan pl = rows_plan(B, Hkv, GT, D, Nk, num_sms, false);
   if (pl.bytes() > workspace_bytes || (pl.bytes() > 0 && !workspace)) return ATTN_ERR_INVALID_ARG;
