@@ -238,6 +238,51 @@ def test_decode_large_scores_move_the_maximum(attn):
     check_decode(attn, c, 4, 2)
 
 
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("lo,hi", [(127, 127), (100, 150), (20, 230), (60, 71), (60, 72)])
+def test_decode_value_scales_far_apart(attn, d, lo, hi):
+    """V exponents that do not fit one pass of the kernel's probabilities, and K exponents against them."""
+    c = Cache(43, [333, 70, 1], 2, d, 16, True)
+    r = np.random.RandomState(lo + hi)
+    vs = c.vs.view(torch.uint8)
+    new = torch.tensor(r.randint(lo, hi + 1, tuple(vs.shape)), dtype=torch.uint8)
+    new[:, :, ::3] = lo
+    new[:, :, 5] = hi
+    vs[vs != 255] = new[vs != 255]
+    check_decode(attn, c, 4, 3)
+
+
+def test_decode_weights_spread_over_many_small_ones(attn):
+    """One key far above the rest, whose weights sum to as much: small probabilities must not vanish."""
+    for f8 in (False, True):
+        c = Cache(44, [6000], 1, 64, 64, f8)
+        if f8:
+            c.ks.view(torch.uint8)[c.ks.view(torch.uint8) != 255] = 127
+        q = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16)
+        q[0, 0, 0, 0] = 1.0
+        for p in range(6000):
+            i, row = page_row(c.table[0].tolist(), 64, c.k.shape[0], p)
+            c.k[i, 0, row, 0] = torch.tensor(9.0 if p == 777 else 0.0).to(c.k.dtype)
+        o, lse = run_decode(attn, c, q, 1.0)
+        check(f64(o[0]), f64(lse[0]), decode_want(c, f64(q[0]), 0, 1.0), 64, 1.0, 6000)
+
+
+@pytest.mark.parametrize("power", [-120, -60, 60, 110])
+def test_decode_queries_of_any_size(attn, power):
+    """Query rows far from 1, each with elements far apart."""
+    for f8 in (False, True):
+        c = Cache(45, [200, 31], 2, 64, 16, f8)
+        q = bf16(gen(4), 2, 4, 2, 64)
+        q[..., ::2] *= 2.0 ** -9
+        q = (q.double() * 2.0 ** power).to(torch.bfloat16)
+        scale = 2.0 ** -power / 8
+        k, v, table, lens, sc = c.on_gpu()
+        o, lse = attn.forward_decode(q.cuda(), k, v, table, lens, scale=scale, **sc)
+        settled(attn)
+        for b in range(2):
+            check(f64(o[b]), f64(lse[b]), decode_want(c, f64(q[b]), b, scale), 64, scale, c.lens[b])
+
+
 def test_decode_is_deterministic(attn):
     c = Cache(28, [2000, 77, 0, 513], 2, 128, 64, True)
     q = bf16(gen(9), 4, 8, 1, 128)

@@ -14,17 +14,26 @@
 //    stages, eight stages a CTA and three CTAs an SM: about 100 KB in flight while as much is
 //    computed on.  (Loads straight into registers, a first version, held 340 us for the 550 MB of
 //    B64 Hq32 Hkv8 N<=8192 D128 E4M3, the warps waiting for memory 70 % of the time.)
-//  * A lane reads its operands of the tensor-core instruction (m16n8k16, 16 query rows) as they lie:
-//    the K = 16 index of Q K^T may be any permutation of D as long as Q uses the same one, so a lane
-//    takes 16 contiguous bytes of its key's row for several K steps (pieces 2t, 2t+1 of a swizzled
-//    row: no bank conflicts); likewise the N = 8 index of P V is any permutation of the output
-//    columns, so a lane takes 16 bytes of the four value rows that it holds as K index, and pairs two
-//    rows with one byte permutation per operand register.  Nothing is transposed.
-//  * E4M3 codes become bf16 by moving their bits (sign, then exponent and mantissa 4 bits down: the
-//    value times 2^-120, exact for subnormal codes too) and one exact multiplication by 2^120.  A
-//    token's K exponent multiplies its scores in fp32, its V exponent its probability before that is
-//    rounded to bf16: both are powers of two and round nothing.
-//  * The running maximum moves only when some row of the warp grew by more than 8 (2^8 in P), so the
+//  * The products are transposed, S^T = K Q^T and O^T = V^T P^T, so that the rows are the N = 8 index of
+//    the tensor-core instruction (m16n8k16): few rows are few columns, and none of the work is for
+//    rows that are not there (with rows as M = 16, half of it was at the usual 8 rows or fewer).  P
+//    goes from the first product's layout to the second's by a register transposition of each 8 x 8.
+//  * A lane reads its operands as they lie: the K = 16 index of K Q^T may be any permutation of D as
+//    long as Q uses the same one, so a lane takes 16 contiguous bytes of its key's row for several K
+//    steps (pieces 2t, 2t+1 of a swizzled row: no bank conflicts); likewise the M = 16 index of V^T P^T
+//    is any permutation of the output columns, so a lane takes 16 bytes of the four value rows that it
+//    holds as K index, and pairs two rows with one byte permutation per operand register.
+//  * E4M3 codes are converted two at a time to f16, exactly (moving the bits to bf16 by integer
+//    instructions took twice the arithmetic pipe's time, which then bounded the kernel).  The f16
+//    operands on the other side keep the products exact enough:
+//      Q    each row is multiplied by the power of two that brings its largest magnitude to 2^13, so
+//           that a bf16 number keeps all its bits down to 2^-27 of the row's largest, and loses at
+//           most 2^-38 of that below; the power is taken back from the scores in fp32.
+//      P    a token's V exponent multiplies its probability: P' = p 2^13 2^(ev - E) with E the
+//           largest exponent that the warp has met, 11 bits down to 2^-27 of the largest (2^-17 at
+//           ev = E - 10).  When E grows, O is scaled by a power of two; tokens more than 10 below E
+//           get passes of their own.
+//  * The running maximum moves only when some row of the warp grew by more than 8 (E4M3: 2), so the
 //    usual step needs one vote and no shuffle, and O is rarely rescaled.
 //
 // Schedule.  The work is counted in blocks of 64 keys of one (sequence, KV head, row block) unit,
@@ -35,7 +44,7 @@
 // second kernel joins the parts of each split unit in key order.  No atomics, no state in the
 // workspace: results depend on the inputs alone.
 //
-// A CTA's four warps take `row_tiles` tiles of 16 rows (1, 2 or 4) and share the keys 4 / row_tiles
+// A CTA's four warps take `row_tiles` tiles of 16 rows (1, 2 or 4; or one of 8) and share the keys 4 / row_tiles
 // ways; the warps of one way share its ring (a stage is refilled once all of them have left it).
 // Their results are joined in shared memory, in the ring's place.  Every wait is bounded.
 #pragma once
@@ -68,7 +77,7 @@ struct DecParams {
   int GT, T;                 // rows of a sequence and KV head; tokens (row i is token i % T)
   int causal;                // token t sees keys up to len - T + t
   FastDiv div_gt;
-  int row_tiles;                        // of a CTA
+  int row_tiles, unit_rows;             // of a CTA: tiles of rows, and their rows together
   int row_blocks;                       // of a sequence
   int box;                              // key rows of a TMA box: the step, or 16
   // shared prefix handled here (prefix_len > 0): an extra first sequence with all rows of the batch
@@ -80,9 +89,8 @@ struct DecParams {
   __nv_bfloat16* o;          // [B][Hkv][GT][D]
   float* lse;                // [B][Hkv][GT]
   // workspace
-  float* slot_o;             // [2 * grid][slot_rows][D]
-  float2* slot_ml;           // [2 * grid][slot_rows]
-  int slot_rows;
+  float* slot_o;             // [2 * grid][unit_rows][D]
+  float2* slot_ml;           // [2 * grid][unit_rows]
   // shared prefix: whole units go here instead of o, lse, indexed like o: [0] own keys, [1] prefix
   float* area_o[2];
   float2* area_ml[2];
@@ -164,7 +172,7 @@ __device__ __forceinline__ DecLine dec_locate(const DecParams& p, unsigned ctas,
   return ln;
 }
 
-// D += A B, m16n8k16, bf16 operands and fp32 accumulators in registers.
+// D += A B, m16n8k16, bf16 (f16) operands and fp32 accumulators in registers.
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -172,6 +180,36 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+__device__ __forceinline__ void mma_16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two E4M3 codes (the low or the high half of w) -> an f16 pair, exactly.
+__device__ __forceinline__ uint32_t e4m3_lo_to_f16(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi_to_f16(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// Two floats -> packed f16x2 (nearest even); `lo` in bits 0-15.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A power of two from its exponent field (0 < e < 255: 2^(e - 127); 255: infinity; 0: 0).
+__device__ __forceinline__ float pow2_field(int e) { return __uint_as_float((uint32_t)e << 23); }
 
 template <int D, bool kF8>
 struct DecCfg {
@@ -182,6 +220,9 @@ struct DecCfg {
   static constexpr int kChunkBytes = kStep * 128;
   static constexpr int kVOff = kChunks * kChunkBytes;       // V behind K in a stage
   static_assert(2 * kVOff == kDecStageBytes, "a stage holds one step");
+  static constexpr float kLazy = kF8 ? 2.f : kRescaleLog2;  // growth of a row's maximum that is let go
+  static constexpr float kLift = kF8 ? 13.f : 0.f;          // P is 2^kLift times the probability
+  static constexpr int kWindow = 10;                        // V exponents of one pass
   static constexpr int kKWords = D * kElem / 16;            // 32-bit words of a key a lane holds (1/4 of it)
   static constexpr int kVWords = D * kElem / 32;            // of a value row (1/8 of it)
   static constexpr int kRowStride = D + 4;                  // floats, of a row of the join
@@ -204,8 +245,8 @@ __device__ __forceinline__ constexpr int dec_koff(int s, int t) {
   return (64 * c + 64 <= D) ? 64 * c + 8 * (2 * t + i % 2) + 4 * (s % 2) : 64 * c + 8 * t + 4 * (s % 2);
 }
 
-// Output column of operand register `ct` of P V (0 <= ct < D/8) for N index n (0..7): the columns a
-// lane loads contiguously.
+// Output column number `ct` (0 <= ct < D/8) of lane group n (0..7): the columns a lane loads
+// contiguously.  Two of them are M indices g and g + 8 of one product.
 template <int D, bool kF8>
 __device__ __forceinline__ constexpr int dec_col(int ct, int n) {
   if (kF8 && D == 128) return 16 * n + ct;
@@ -257,12 +298,34 @@ __device__ __forceinline__ void dec_load_v(uint32_t (&w)[DecCfg<D, kF8>::kVWords
   }
 }
 
-template <int D, bool kF8>
+// An 8 x 8 matrix of 16-bit values, transposed across the warp: lane (g, t) gives row g, columns 2t and
+// 2t + 1, and gets row g of the transpose.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// Column ct (of a lane's contiguous ones) of two value rows as a pair, an A operand of V^T P^T: bf16 as
+// they are, E4M3 as f16 (the byte permutation serves two columns).
+template <bool kF8>
+__device__ __forceinline__ uint32_t dec_pair(const uint32_t* r0, const uint32_t* r1, int ct) {
+  if constexpr (kF8) {
+    const uint32_t x = __byte_perm(r0[ct / 4], r1[ct / 4], (ct & 2) ? 0x7362u : 0x5140u);
+    return (ct & 1) ? e4m3_hi_to_f16(x) : e4m3_lo_to_f16(x);
+  } else {
+    return __byte_perm(r0[ct / 2], r1[ct / 2], (ct & 1) ? 0x7632u : 0x5410u);
+  }
+}
+
+// kN: tiles of 8 rows a warp takes (1: units of at most 8 rows; else 2).
+template <int D, bool kF8, int kN>
 __global__ void __launch_bounds__(kDecThreads, 3)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const DecParams p) {
   using Cfg = DecCfg<D, kF8>;
   constexpr int G = Cfg::kGroups, KW = Cfg::kKWords, VW = Cfg::kVWords;
+  constexpr int kTile = 8 * kN;   // rows of a warp
   extern __shared__ uint8_t smem_raw[];
   __shared__ float2 sml[4][16];
   __shared__ long long scratch[16];
@@ -295,8 +358,11 @@ __global__ void __launch_bounds__(kDecThreads, 3)
   long long first;
   const DecLine ln = dec_locate(p, gridDim.x, blockIdx.x, -1, scratch, seq, first);   // (its barriers order the above)
   const long long begin = (long long)blockIdx.x * ln.share, end = min(ln.total, begin + ln.share);
-  // ring positions: steps issued (the way's first warp) and left behind, over all units
-  uint32_t issued = 0u, done = 0u;
+  // ring positions (stage, parity of its use) of the next issue (the way's first warp) and of the
+  // next step, over all units; uses of the ring before its first refill need no wait
+  uint32_t i_stage = 0u, i_phase = 0u, i_count = 0u, stage = 0u, phase = 0u;
+  const uint64_t policy = l2_policy_evict_first();   // each key and value is read once
+  const int no_plane = p.num_pages * p.Hkv;          // outside the tensor maps: zeros
   bool ok = true;
 
   for (long long x = begin; x < end;) {
@@ -311,7 +377,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
     const int blk1 = (int)min((long long)nblk, blk0 + (end - x));
     const int h = unit / row_blocks, rb = unit - h * row_blocks;
     const int* table = prefix ? p.prefix_table : (p.table ? p.table + (size_t)seq * p.max_pages : nullptr);
-    const int i0 = rb * 16 * row_tiles + rt * 16;   // first row of this warp's tile
+    const int i0 = (rb * row_tiles + rt) * kTile;   // first row of this warp's tile
     const int key_begin = p.whole_units ? 0 : blk0 * kDecBlock;
     const int key_end = p.whole_units ? len : (int)min((long long)len, (long long)blk1 * kDecBlock);
 
@@ -325,153 +391,191 @@ __global__ void __launch_bounds__(kDecThreads, 3)
     const int stride = ways * Cfg::kStep;
     const int k_first = key_begin + kg * Cfg::kStep;
     const int steps = k_first < key_end ? (key_end - k_first + stride - 1) / stride : 0;
-    // key position k -> (page's plane in the tensor maps, row in the page); no page: plane past the end
-    auto place = [&](int k, int& plane, int& row) {
-      const uint32_t pg = fast_div((uint32_t)k, p.div_page);
+    // page pg of the unit -> its plane in the tensor maps
+    auto plane_of = [&](int pg) -> int {
       const int id = table ? __ldg(table + pg) : seq;
-      row = k - (int)(pg * (uint32_t)p.page);
-      plane = (unsigned)id < (unsigned)p.num_pages ? id * p.Hkv + h : p.num_pages * p.Hkv;
+      return (unsigned)id < (unsigned)p.num_pages ? id * p.Hkv + h : no_plane;
     };
-    // Loads of step n (one lane): boxes with a key only.
-    auto issue = [&](int n) {
-      const uint32_t st = issued % (uint32_t)stages;
-      const int k = k_first + n * stride;
-      const int boxes = min(Cfg::kStep / p.box, (key_end - k + p.box - 1) / p.box);
-      mbar_arrive_expect_tx(&ring_full[st], (uint32_t)(2 * Cfg::kChunks * boxes * p.box * 128));
-      for (int i = 0; i < boxes; ++i) {
-        int plane, row;
-        place(k + i * p.box, plane, row);
+    // A position walking along the steps: page and row in it.
+    struct Walk {
+      int pg, row;
+    };
+    auto walk_at = [&](int k) -> Walk {
+      const int pg = (int)fast_div((uint32_t)k, p.div_page);
+      return Walk{pg, k - pg * p.page};
+    };
+    auto walk_on = [&](Walk& w, int by) {
+      for (w.row += by; w.row >= p.page; w.row -= p.page) ++w.pg;
+    };
+    // The loads of a step: boxes with a key only.  The planes were looked up a step before.
+    constexpr int kMaxBoxes = G;
+    const int boxes_per_step = Cfg::kStep / p.box;
+    Walk iw[kMaxBoxes];
+    int iplane[kMaxBoxes];
+    auto look_up = [&](int n) {   // planes of step n's boxes (where it has keys), iw standing at that step
+#pragma unroll
+      for (int i = 0; i < kMaxBoxes; ++i)
+        iplane[i] = (i < boxes_per_step && n < steps && k_first + n * stride + i * p.box < key_end) ? plane_of(iw[i].pg) : -1;
+    };
+    auto issue = [&](int n) -> bool {   // one lane; moves iw and the planes on to step n + 1
+      if (i_count >= (uint32_t)stages &&
+          !wait_phase(&ring_empty[i_stage], i_phase ^ 1u, abort_flag, kSiteDecodeEmpty))
+        return false;
+      int boxes = 0;
+#pragma unroll
+      for (int i = 0; i < kMaxBoxes; ++i) boxes += iplane[i] >= 0 ? 1 : 0;
+      mbar_arrive_expect_tx(&ring_full[i_stage], (uint32_t)(2 * Cfg::kChunks * boxes * p.box * 128));
+#pragma unroll
+      for (int i = 0; i < kMaxBoxes; ++i) {
+        if (iplane[i] < 0) continue;
 #pragma unroll
         for (int c = 0; c < Cfg::kChunks; ++c) {
-          uint8_t* dst = smem + (kg * stages + st) * kDecStageBytes + c * Cfg::kChunkBytes + i * p.box * 128;
-          tma_load_3d(dst, &tmap_k, &ring_full[st], c * (128 / Cfg::kElem), row, plane, l2_policy_evict_first());
-          tma_load_3d(dst + Cfg::kVOff, &tmap_v, &ring_full[st], c * (128 / Cfg::kElem), row, plane,
-                      l2_policy_evict_first());
+          uint8_t* dst = smem + (kg * stages + i_stage) * kDecStageBytes + c * Cfg::kChunkBytes + i * p.box * 128;
+          tma_load_3d(dst, &tmap_k, &ring_full[i_stage], c * (128 / Cfg::kElem), iw[i].row, iplane[i], policy);
+          tma_load_3d(dst + Cfg::kVOff, &tmap_v, &ring_full[i_stage], c * (128 / Cfg::kElem), iw[i].row, iplane[i],
+                      policy);
         }
       }
+      ++i_count;
+      if (++i_stage == (uint32_t)stages) {
+        i_stage = 0u;
+        i_phase ^= 1u;
+      }
+#pragma unroll
+      for (int i = 0; i < kMaxBoxes; ++i) walk_on(iw[i], stride);
+      look_up(n + 1);
+      return true;
     };
     const bool issuer = rt == 0 && lane == 0;
-    if (issuer && ok)
-      for (int n = 0; n < min(stages - 1, steps) && ok; ++n) {
-        if (issued >= (uint32_t)stages)
-          ok = wait_phase(&ring_empty[issued % (uint32_t)stages], (issued / (uint32_t)stages - 1u) & 1u, abort_flag,
-                          kSiteDecodeEmpty);
-        if (!ok) break;
-        issue(n);
-        ++issued;
-      }
+    if (issuer) {
+#pragma unroll
+      for (int i = 0; i < kMaxBoxes; ++i) iw[i] = walk_at(k_first + i * p.box);
+      look_up(0);
+      for (int n = 0; n < min(stages - 1, steps) && ok; ++n) ok = issue(n);
+    }
     ok = __all_sync(0xffffffffu, ok);
 
-    float o[D / 8][4];
+    // O^T: [row tile][pair of columns 2c, 2c+1]: rows 2t, 2t+1 of column 2c, then of 2c+1
+    float o[kN][D / 16][4];
 #pragma unroll
-    for (int ct = 0; ct < D / 8; ++ct)
+    for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[ct][e] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+      for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[nt][c][e] = 0.f;
+    // per row 8 nt + 2t + e of the tile: running maximum, this lane's part of the sum, the factor of
+    // its scores, and the first key that it does not see
+    float m[kN][2], l[kN][2], cf[kN][2];
+    int lim[kN][2], lim_min = len;
     const bool active = i0 < rows;   // (a tile past the rows only keeps the ring going)
 
-    // Q as the A operand of Q K^T: words 2s, 2s+1 of a row are K step s
-    uint32_t q0[2 * (D / 16)], q1[2 * (D / 16)];
-    {
-      const bool r0 = i0 + g < rows, r1 = i0 + g + 8 < rows;
-      const __nv_bfloat16* qa = p.q + (r0 ? row_index(i0 + g) : 0) * D;
-      const __nv_bfloat16* qb = p.q + (r1 ? row_index(i0 + g + 8) : 0) * D;
+    // Q as the B operand of K Q^T: words 2s, 2s+1 of row 8 nt + g are K step s
+    uint32_t qw[kN][2 * (D / 16)];
+#pragma unroll
+    for (int nt = 0; nt < kN; ++nt) {
+      const int i = i0 + 8 * nt + g;
+      const __nv_bfloat16* qr = p.q + (i < rows ? row_index(i) : 0) * D;
 #pragma unroll
       for (int s = 0; s < D / 16; ++s) {
-        const int off = dec_koff<D, kF8>(s, t4);
-        const uint2 a = r0 ? __ldg(reinterpret_cast<const uint2*>(qa + off)) : make_uint2(0u, 0u);
-        const uint2 b = r1 ? __ldg(reinterpret_cast<const uint2*>(qb + off)) : make_uint2(0u, 0u);
-        q0[2 * s] = a.x, q0[2 * s + 1] = a.y;
-        q1[2 * s] = b.x, q1[2 * s + 1] = b.y;
+        const uint2 a = i < rows ? __ldg(reinterpret_cast<const uint2*>(qr + dec_koff<D, kF8>(s, t4))) : make_uint2(0u, 0u);
+        qw[nt][2 * s] = a.x, qw[nt][2 * s + 1] = a.y;
+      }
+      float back = 1.f;
+      if constexpr (kF8) {
+        // bf16 -> f16 times 2^sh, which brings the row's largest magnitude to [2^13, 2^14)
+        uint32_t top = 0u;
+#pragma unroll
+        for (int w = 0; w < 2 * (D / 16); ++w) top = max(top, max(qw[nt][w] & 0x7fffu, (qw[nt][w] >> 16) & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int sh = min(126, 140 - (int)(top >> 7));
+        const float mul = pow2_field(127 + sh);
+        back = pow2_field(127 - sh);
+#pragma unroll
+        for (int w = 0; w < 2 * (D / 16); ++w)
+          qw[nt][w] = pack_f16x2(__uint_as_float(qw[nt][w] << 16) * mul, __uint_as_float(qw[nt][w] & 0xffff0000u) * mul);
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+        cf[nt][e] = p.c * __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));   // from the lane of that row
+        lim[nt][e] = (p.causal && !prefix) ? len - p.T + 1 + (i0 + 8 * nt + 2 * t4 + e) % p.T : len;
       }
     }
-    // keys below the limits are seen by rows g and g + 8 of the tile
-    int lim0 = len, lim1 = len, lim_min = len;
-    if (p.causal && !prefix) {
-      lim0 = len - p.T + 1 + (i0 + g) % p.T;
-      lim1 = len - p.T + 1 + (i0 + g + 8) % p.T;
-      lim_min = len - p.T + 1;
-    }
-    // E4M3: exponent bytes of keys 2t, 2t+1 of each half group of a step (1 for no page: zero rows)
+    if (p.causal && !prefix) lim_min = len - p.T + 1;
+    // E4M3: exponent bytes of keys g and g + 8 of each group of the next step (for no page: 1, of
+    // zero rows), and the largest V exponent so far (0: none yet)
     uint32_t sk[G][2], sv[G][2];
-    auto load_scales = [&](int n) {
+    int top_e = 0;
+    Walk sw[G];
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) sw[gr] = walk_at(k_first + 16 * gr);
+    auto load_scales = [&](int n) {   // of step n, where sw stands; moves sw on
       if constexpr (kF8) {
-        const int k = k_first + n * stride;
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) sk[gr][j] = sv[gr][j] = 0x7f7fu;
-          if (n >= steps || k + 16 * gr >= key_end) continue;
-          int plane, row;
-          place(k + 16 * gr, plane, row);
-          if (plane >= p.num_pages * p.Hkv) continue;
-          const long long e = (long long)plane * p.page + row + 2 * t4;
+          for (int j = 0; j < 2; ++j) sk[gr][j] = sv[gr][j] = 127u;
+          const int plane = (n < steps && k_first + n * stride + 16 * gr < key_end) ? plane_of(sw[gr].pg) : no_plane;
+          if (plane != no_plane) {
+            const long long e = (long long)plane * p.page + sw[gr].row + g;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            sk[gr][j] = __ldg(reinterpret_cast<const uint16_t*>(p.ks + e + 8 * j));
-            sv[gr][j] = __ldg(reinterpret_cast<const uint16_t*>(p.vs + e + 8 * j));
+            for (int j = 0; j < 2; ++j) {
+              sk[gr][j] = __ldg(p.ks + e + 8 * j);
+              sv[gr][j] = __ldg(p.vs + e + 8 * j);
+            }
           }
+          walk_on(sw[gr], stride);
         }
       }
     };
     load_scales(0);
 
-    for (int n = 0; n < steps && ok; ++n, ++done) {
+    for (int n = 0; n < steps && ok; ++n) {
       const int k = k_first + n * stride;
-      if (issuer && n + stages - 1 < steps) {
-        // the stage of the step before last is free once the way's warps have left it
-        if (issued >= (uint32_t)stages)
-          ok = wait_phase(&ring_empty[issued % (uint32_t)stages], (issued / (uint32_t)stages - 1u) & 1u, abort_flag,
-                          kSiteDecodeEmpty);
-        if (ok) {
-          issue(n + stages - 1);
-          ++issued;
-        }
-      }
-      const uint32_t st = done % (uint32_t)stages;
-      ok = wait_phase(&ring_full[st], (done / (uint32_t)stages) & 1u, abort_flag, kSiteDecodeFull) && ok;
+      // the stage of the step before last is free once the way's warps have left it
+      if (issuer && n + stages - 1 < steps) ok = issue(n + stages - 1);
+      ok = wait_phase(&ring_full[stage], phase, abort_flag, kSiteDecodeFull) && ok;
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       if (active) {
-        const uint32_t tile_k = ring + st * kDecStageBytes, tile_v = tile_k + Cfg::kVOff;
-        // S = Q K^T
-        float s[G][2][4];
+        const uint32_t tile_k = ring + stage * kDecStageBytes, tile_v = tile_k + Cfg::kVOff;
+        // S^T = K Q^T: keys g and g + 8 of each group, rows 2t and 2t + 1 of each tile
+        float s[G][kN][4];
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
+          uint32_t ka[KW], kb[KW];
+          dec_load_k<D, kF8>(ka, tile_k, 16 * gr + g, t4);
+          dec_load_k<D, kF8>(kb, tile_k, 16 * gr + 8 + g, t4);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t kw[KW];
-            dec_load_k<D, kF8>(kw, tile_k, 16 * gr + 8 * j + g, t4);
-            s[gr][j][0] = s[gr][j][1] = s[gr][j][2] = s[gr][j][3] = 0.f;
+          for (int nt = 0; nt < kN; ++nt) s[gr][nt][0] = s[gr][nt][1] = s[gr][nt][2] = s[gr][nt][3] = 0.f;
 #pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
-              const uint32_t a[4] = {q0[2 * q], q1[2 * q], q0[2 * q + 1], q1[2 * q + 1]};
-              if constexpr (kF8) {
-                mma_16816(s[gr][j], a, e4m3_hi2_to_bf16(__byte_perm(kw[q], 0u, 0x1000)),
-                          e4m3_hi2_to_bf16(__byte_perm(kw[q], 0u, 0x3020)));
-              } else {
-                mma_16816(s[gr][j], a, kw[2 * q], kw[2 * q + 1]);
-              }
+          for (int q = 0; q < D / 16; ++q) {
+            if constexpr (kF8) {
+              const uint32_t a[4] = {e4m3_lo_to_f16(ka[q]), e4m3_lo_to_f16(kb[q]), e4m3_hi_to_f16(ka[q]),
+                                     e4m3_hi_to_f16(kb[q])};
+#pragma unroll
+              for (int nt = 0; nt < kN; ++nt) mma_16816_f16(s[gr][nt], a, qw[nt][2 * q], qw[nt][2 * q + 1]);
+            } else {
+              const uint32_t a[4] = {ka[2 * q], kb[2 * q], ka[2 * q + 1], kb[2 * q + 1]};
+#pragma unroll
+              for (int nt = 0; nt < kN; ++nt) mma_16816(s[gr][nt], a, qw[nt][2 * q], qw[nt][2 * q + 1]);
             }
           }
         }
-        float f[G][4];   // E4M3: factor of P for keys 2t, 2t+1, 2t+8, 2t+9
+        int ev[G][2];   // E4M3: V exponents of keys g, g + 8
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if constexpr (kF8) {
-              const float c0 = p.c * e8_scale((int)(sk[gr][j] & 255u)), c1 = p.c * e8_scale((int)(sk[gr][j] >> 8));
-              s[gr][j][0] *= c0;
-              s[gr][j][1] *= c1;
-              s[gr][j][2] *= c0;
-              s[gr][j][3] *= c1;
-              f[gr][2 * j] = e8_scale((int)(sv[gr][j] & 255u));
-              f[gr][2 * j + 1] = e8_scale((int)(sv[gr][j] >> 8));
-            } else {
+          for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) s[gr][j][e] *= p.c;
+            for (int e = 0; e < 4; ++e) {
+              s[gr][nt][e] *= cf[nt][e & 1];
+              // (a marked row has codes 0: 0 * infinity is the NaN it stands for)
+              if constexpr (kF8) s[gr][nt][e] *= pow2_field((int)sk[gr][e >> 1]);
             }
-          }
+          ev[gr][0] = (int)sv[gr][0];
+          ev[gr][1] = (int)sv[gr][1];
         }
         load_scales(n + 1);
         const bool tail = k + Cfg::kStep > key_end;
@@ -479,61 +583,69 @@ __global__ void __launch_bounds__(kDecThreads, 3)
 #pragma unroll
           for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j) {
+              const int key = k + 16 * gr + 8 * j + g;
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int key = k + 16 * gr + 8 * j + 2 * t4 + e;
-                if (key >= min(lim0, key_end)) s[gr][j][e] = -INFINITY;
-                if (key >= min(lim1, key_end)) s[gr][j][2 + e] = -INFINITY;
-                if (kF8 && key >= key_end) f[gr][2 * j + e] = 0.f;
-              }
-        }
-        float mx0 = -INFINITY, mx1 = -INFINITY;
+              for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            mx0 = fmaxf(mx0, fmaxf(s[gr][j][0], s[gr][j][1]));
-            mx1 = fmaxf(mx1, fmaxf(s[gr][j][2], s[gr][j][3]));
-          }
-        if (__any_sync(0xffffffffu, mx0 > m0 + kRescaleLog2 || mx1 > m1 + kRescaleLog2)) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-          mx0 = fmaxf(m0, fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2)));
-          mx1 = fmaxf(m1, fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2)));
-          const float a0 = mx0 == m0 ? 1.f : ex2_approx(m0 - mx0), a1 = mx1 == m1 ? 1.f : ex2_approx(m1 - mx1);
-          m0 = mx0;
-          m1 = mx1;
-          l0 *= a0;
-          l1 *= a1;
-#pragma unroll
-          for (int ct = 0; ct < D / 8; ++ct) {
-            o[ct][0] *= a0;
-            o[ct][1] *= a0;
-            o[ct][2] *= a1;
-            o[ct][3] *= a1;
-          }
-        }
-        const float n0 = m0 == -INFINITY ? 0.f : m0, n1 = m1 == -INFINITY ? 0.f : m1;
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          uint32_t a[4];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float p0 = ex2_approx(s[gr][j][0] - n0), p1 = ex2_approx(s[gr][j][1] - n0);
-            const float p2 = ex2_approx(s[gr][j][2] - n1), p3 = ex2_approx(s[gr][j][3] - n1);
-            l0 += p0 + p1;
-            l1 += p2 + p3;
-            if constexpr (kF8) {
-              a[2 * j] = pack_bf16x2(p0 * f[gr][2 * j], p1 * f[gr][2 * j + 1]);
-              a[2 * j + 1] = pack_bf16x2(p2 * f[gr][2 * j], p3 * f[gr][2 * j + 1]);
-            } else {
-              a[2 * j] = pack_bf16x2(p0, p1);
-              a[2 * j + 1] = pack_bf16x2(p2, p3);
+                for (int e = 0; e < 2; ++e)
+                  if (key >= min(lim[nt][e], key_end)) s[gr][nt][2 * j + e] = -INFINITY;
+              if (kF8 && key >= key_end) ev[gr][j] = top_e;   // not a key: any exponent does
             }
+        }
+        auto scale_o = [&](int nt, float a0, float a1) {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            o[nt][c][0] *= a0;
+            o[nt][c][1] *= a1;
+            o[nt][c][2] *= a0;
+            o[nt][c][3] *= a1;
           }
-          // O += P V
-          uint32_t vr[4][VW];
+        };
+        float mx[kN][2];
+        bool grew = false;
+#pragma unroll
+        for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mx[nt][e] = fmaxf(s[0][nt][e], s[0][nt][2 + e]);
+#pragma unroll
+            for (int gr = 1; gr < G; ++gr) mx[nt][e] = fmaxf(mx[nt][e], fmaxf(s[gr][nt][e], s[gr][nt][2 + e]));
+            grew = grew || mx[nt][e] > m[nt][e] + Cfg::kLazy;
+          }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+          for (int nt = 0; nt < kN; ++nt) {
+            float a[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = mx[nt][e];
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+              x = fmaxf(x, m[nt][e]);
+              a[e] = x == m[nt][e] ? 1.f : ex2_approx(m[nt][e] - x);
+              m[nt][e] = x;
+              l[nt][e] *= a[e];
+            }
+            scale_o(nt, a[0], a[1]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float ref = (m[nt][e] == -INFINITY ? 0.f : m[nt][e]) - Cfg::kLift;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float& x = s[gr][nt][2 * j + e];
+                x = ex2_approx(x - ref);
+                l[nt][e] += x;
+              }
+          }
+        // The four value rows of group gr that this lane holds as K index.
+        auto load_v = [&](uint32_t (&vr)[4][VW], int gr) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = 16 * gr + 2 * t4 + (e & 1) + 8 * (e >> 1);
@@ -543,30 +655,142 @@ __global__ void __launch_bounds__(kDecThreads, 3)
               for (int w = 0; w < VW; ++w) vr[e][w] = 0u;
             }
           }
+        };
+        // P of group gr and row tile nt as the B operand, its keys' factors f0 (key g) and f1 (key g + 8)
+        auto operand_p = [&](int gr, int nt, float f0, float f1, uint32_t& b0, uint32_t& b1) {
+          const float(&x)[4] = s[gr][nt];
+          if constexpr (kF8) {
+            b0 = transpose8x8(pack_f16x2(x[0] * f0, x[1] * f0));
+            b1 = transpose8x8(pack_f16x2(x[2] * f1, x[3] * f1));
+          } else {
+            b0 = transpose8x8(pack_bf16x2(x[0], x[1]));
+            b1 = transpose8x8(pack_bf16x2(x[2], x[3]));
+          }
+        };
+        bool wide = false;
+        if constexpr (kF8) {
+          // are all of the step's V exponents in [top_e - kWindow, top_e]?
+          auto outside = [&]() -> bool {
+            uint32_t far = 0u;
 #pragma unroll
-          for (int ct = 0; ct < D / 8; ++ct) {
-            uint32_t b0, b1;
-            if constexpr (kF8) {
-              const int w = ct / 4;
-              const uint32_t sel = ((uint32_t)(4 + ct % 4) << 12) | ((uint32_t)(ct % 4) << 4);
-              b0 = e4m3_hi2_to_bf16(__byte_perm(vr[0][w], vr[1][w], sel));
-              b1 = e4m3_hi2_to_bf16(__byte_perm(vr[2][w], vr[3][w], sel));
-            } else {
-              const uint32_t sel = (ct & 1) ? 0x7632u : 0x5410u;
-              b0 = __byte_perm(vr[0][ct / 2], vr[1][ct / 2], sel);
-              b1 = __byte_perm(vr[2][ct / 2], vr[3][ct / 2], sel);
+            for (int gr = 0; gr < G; ++gr) far = max(far, max((uint32_t)(top_e - ev[gr][0]), (uint32_t)(top_e - ev[gr][1])));
+            return __any_sync(0xffffffffu, far > (uint32_t)Cfg::kWindow);
+          };
+          if (outside()) {
+            int top = top_e;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if (ev[gr][j] != kE8Nan) top = max(top, ev[gr][j]);
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (top > top_e && top_e > 0) {
+              const float a = pow2_field(max(0, 127 - (top - top_e)));
+#pragma unroll
+              for (int nt = 0; nt < kN; ++nt) scale_o(nt, a, a);
             }
-            mma_16816(o[ct], a, b0, b1);
+            top_e = top;
+            if (tail) {
+#pragma unroll
+              for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  if (k + 16 * gr + 8 * j + g >= key_end) ev[gr][j] = top_e;
+            }
+            wide = outside();
+          }
+        }
+        if (!wide) {
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr) {
+            uint32_t b0[kN], b1[kN], vr[4][VW];
+#pragma unroll
+            for (int nt = 0; nt < kN; ++nt)
+              operand_p(gr, nt, kF8 ? pow2_field(127 + ev[gr][0] - top_e) : 1.f,
+                        kF8 ? pow2_field(127 + ev[gr][1] - top_e) : 1.f, b0[nt], b1[nt]);
+            load_v(vr, gr);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              const uint32_t a[4] = {dec_pair<kF8>(vr[0], vr[1], 2 * c), dec_pair<kF8>(vr[0], vr[1], 2 * c + 1),
+                                     dec_pair<kF8>(vr[2], vr[3], 2 * c), dec_pair<kF8>(vr[2], vr[3], 2 * c + 1)};
+#pragma unroll
+              for (int nt = 0; nt < kN; ++nt) {
+                if constexpr (kF8)
+                  mma_16816_f16(o[nt][c], a, b0[nt], b1[nt]);
+                else
+                  mma_16816(o[nt][c], a, b0[nt], b1[nt]);
+              }
+            }
+          }
+        } else if constexpr (kF8) {
+          // Exponents too far apart for one pass: the largest of those left, and what is within the
+          // window below it, pass by pass (a marked row's factor is NaN, in the first).
+          uint32_t left = (1u << (2 * G)) - 1u;   // this lane's keys not yet added
+          for (bool first_pass = true; __any_sync(0xffffffffu, left != 0u); first_pass = false) {
+            int top = 0;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if ((left >> (2 * gr + j) & 1u) && ev[gr][j] != kE8Nan) top = max(top, ev[gr][j]);
+            top = __reduce_max_sync(0xffffffffu, top);
+            const float back = pow2_field(max(0, 127 - (top_e - top)));
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+              float f[2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const bool marked = ev[gr][j] == kE8Nan;
+                const bool now = (left >> (2 * gr + j) & 1u) && (marked ? first_pass : top - ev[gr][j] <= Cfg::kWindow);
+                f[j] = !now ? 0.f : marked ? __uint_as_float(0x7fffffffu) : pow2_field(127 + ev[gr][j] - top);
+                if (now) left &= ~(1u << (2 * gr + j));
+              }
+              uint32_t vr[4][VW];
+              load_v(vr, gr);
+#pragma unroll
+              for (int nt = 0; nt < kN; ++nt) {
+                uint32_t b0, b1;
+                operand_p(gr, nt, f[0], f[1], b0, b1);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                  const uint32_t a[4] = {dec_pair<kF8>(vr[0], vr[1], 2 * c), dec_pair<kF8>(vr[0], vr[1], 2 * c + 1),
+                                         dec_pair<kF8>(vr[2], vr[3], 2 * c), dec_pair<kF8>(vr[2], vr[3], 2 * c + 1)};
+                  float t[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma_16816_f16(t, a, b0, b1);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[nt][c][e] = fmaf(t[e], back, o[nt][c][e]);
+                }
+              }
+            }
           }
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ring_empty[st]);   // this warp has left the stage
+      if (lane == 0) mbar_arrive(&ring_empty[stage]);   // this warp has left the stage
+      if (++stage == (uint32_t)stages) {
+        stage = 0u;
+        phase ^= 1u;
+      }
     }
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+#pragma unroll
+    for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][e] += __shfl_xor_sync(0xffffffffu, l[nt][e], d);
+        // P was 2^kLift times the probability
+        if constexpr (kF8) l[nt][e] *= pow2_field(127 - (int)Cfg::kLift);
+      }
+    if constexpr (kF8) {
+      // and O is in units of the largest V exponent
+      const float a = pow2_field(127 - (int)Cfg::kLift), b = pow2_field(top_e);
+#pragma unroll
+      for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nt][c][e] = o[nt][c][e] * a * b;
+    }
     // all rings are empty: the join may take their place, unless a wait gave up
     if (__syncthreads_or(!ok)) {
       ok = false;
@@ -574,24 +798,26 @@ __global__ void __launch_bounds__(kDecThreads, 3)
     }
 
     // ---- join the warps' results, and write the unit out or its part to a slot
-    if (t4 == 0) {
-      sml[warp][g] = make_float2(m0, l0);
-      sml[warp][g + 8] = make_float2(m1, l1);
-    }
 #pragma unroll
-    for (int ct = 0; ct < D / 8; ++ct) {
-      so[warp][g][dec_col<D, kF8>(ct, 2 * t4)] = o[ct][0];
-      so[warp][g][dec_col<D, kF8>(ct, 2 * t4 + 1)] = o[ct][1];
-      so[warp][g + 8][dec_col<D, kF8>(ct, 2 * t4)] = o[ct][2];
-      so[warp][g + 8][dec_col<D, kF8>(ct, 2 * t4 + 1)] = o[ct][3];
-    }
+    for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * nt + 2 * t4 + e;
+        if (g == 0) sml[warp][r] = make_float2(m[nt][e], l[nt][e]);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          so[warp][r][dec_col<D, kF8>(2 * c, g)] = o[nt][c][e];
+          so[warp][r][dec_col<D, kF8>(2 * c + 1, g)] = o[nt][c][2 + e];
+        }
+      }
     __syncthreads();
     const bool whole = blk0 == 0 && blk1 == nblk;
     const long long slot = 2LL * blockIdx.x + (x == begin ? 0 : 1);
-    const int tile_rows = min(16 * row_tiles, rows - rb * 16 * row_tiles);
-    for (int idx = threadIdx.x; idx < tile_rows * (D / 4); idx += kDecThreads) {
+    const int unit_row = rb * row_tiles * kTile;
+    const int unit_rows = min(row_tiles * kTile, rows - unit_row);
+    for (int idx = threadIdx.x; idx < unit_rows * (D / 4); idx += kDecThreads) {
       const int r = idx / (D / 4), d = (idx - r * (D / 4)) * 4;
-      const int tile = r >> 4, rr = r & 15;
+      const int tile = r / kTile, rr = r % kTile;
       float mt = -INFINITY;
       for (int w = 0; w < ways; ++w) mt = fmaxf(mt, sml[tile + w * row_tiles][rr].x);
       float lt = 0.f;
@@ -607,14 +833,14 @@ __global__ void __launch_bounds__(kDecThreads, 3)
         acc.w = fmaf(ov.w, a, acc.w);
       }
       if (whole && p.area_o[0] == nullptr) {
-        const long long row = row_index(rb * 16 * row_tiles + r);
+        const long long row = row_index(unit_row + r);
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
         *reinterpret_cast<uint2*>(p.o + row * D + d) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
         if (d == 0)
           p.lse[row] = lt == 0.f ? -INFINITY : ((mt == -INFINITY ? 0.f : mt) + log2f(lt)) * 0.69314718055994530942f;
       } else {
-        const long long at = whole ? row_index(rb * 16 * row_tiles + r) : slot * p.slot_rows + r;
+        const long long at = whole ? row_index(unit_row + r) : slot * p.unit_rows + r;
         float* dst = whole ? p.area_o[prefix] : p.slot_o;
         *reinterpret_cast<float4*>(dst + at * D + d) = acc;
         if (d == 0) (whole ? p.area_ml[prefix] : p.slot_ml)[at] = make_float2(mt, lt);
@@ -633,8 +859,11 @@ __global__ void __launch_bounds__(kDecThreads, 3)
   }
   // Drain after a wait gave up: every issued copy lands before the CTA exits.
   if (!ok && rt == 0 && lane == 0)
-    for (uint32_t i = issued > (uint32_t)stages ? issued - (uint32_t)stages : 0u; i < issued; ++i)
-      drain_phase(&ring_full[i % (uint32_t)stages], (i / (uint32_t)stages) & 1u, abort_flag);
+    for (int i = 0; i < min(stages, (int)i_count); ++i) {
+      i_phase ^= i_stage == 0u ? 1u : 0u;
+      i_stage = i_stage == 0u ? (uint32_t)stages - 1u : i_stage - 1u;
+      drain_phase(&ring_full[i_stage], i_phase, abort_flag);
+    }
 }
 
 // Joins the parts of every split unit in key order, and, behind a shared prefix (area_o set), the
@@ -657,12 +886,12 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
   const bool shared = p.area_o[0] != nullptr;
   if (!shared && c0 == c1) return;   // written by the one CTA that had it
 
-  const int tile_rows = min(16 * p.row_tiles, p.GT - rb * 16 * p.row_tiles);
+  const int unit_rows = min(p.unit_rows, p.GT - rb * p.unit_rows);
   // prefix unit of a row (few rows: computed by the same kernel): its parts, if it was split
   const int pre_nblk = p.whole_units ? 1 : (p.prefix_len + kDecBlock - 1) / kDecBlock;
-  for (int idx = threadIdx.x; idx < tile_rows * (D / 4); idx += kDecThreads) {
+  for (int idx = threadIdx.x; idx < unit_rows * (D / 4); idx += kDecThreads) {
     const int r = idx / (D / 4), d = (idx - r * (D / 4)) * 4;
-    const int i = rb * 16 * p.row_tiles + r;
+    const int i = rb * p.unit_rows + r;
     const long long row = ((long long)b * p.Hkv + h) * p.GT + i;
     float m = -INFINITY, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -688,10 +917,10 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
         return;
       }
       for (long long c = f; c <= e; ++c)
-        add(p.slot_o, p.slot_ml, (2 * c + ((c == f && a0 != c * ln.share) ? 1 : 0)) * p.slot_rows + slot_row);
+        add(p.slot_o, p.slot_ml, (2 * c + ((c == f && a0 != c * ln.share) ? 1 : 0)) * p.unit_rows + slot_row);
     };
     if (p.prefix_len > 0) {
-      const int pr = b * p.GT + i, per = 16 * p.row_tiles;
+      const int pr = b * p.GT + i, per = p.unit_rows;
       const long long a0 = ((long long)h * p.prefix_row_blocks + pr / per) * pre_nblk;
       add_unit(a0, a0 + pre_nblk, 1, pr % per);
     }

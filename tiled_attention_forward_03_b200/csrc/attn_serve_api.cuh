@@ -3,6 +3,8 @@
 // translation unit: it uses that file's device set-up, error records and tensor-map encoders.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_cache_kernel.cuh"
 #include "attn_decode_kernel.cuh"
 #include "attn_fwd_rows_kernel.cuh"
@@ -87,7 +89,8 @@ struct DecodeDeviceInfo {
 };
 
 struct DecPlan {
-  int row_tiles, row_blocks, prefix_row_blocks = 0;
+  int tile_rows;             // rows of a warp: 8 or 16
+  int row_tiles, unit_rows, row_blocks, prefix_row_blocks = 0;
   int whole_units;
   unsigned grid;
   bool join;                 // the second kernel is needed
@@ -100,9 +103,6 @@ constexpr int kDecMinShare = 2;     // blocks of 64 keys
 constexpr int kDecShortBlocks = 2;  // sequences of at most this many blocks are never split
 constexpr int kDecCtasPerSm = 3;    // resident CTAs (the kernel's launch bounds)
 
-// 16-row tiles per unit: 1, 2 or 4.
-int dec_row_tiles(long long rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
-
 // `cap`: keys a sequence can have at most.  `shared`: a prefix of `prefix_len` keys comes first;
 // `prefix_here`: this kernel computes it too.
 DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms, bool shared, bool prefix_here,
@@ -110,14 +110,17 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   DecPlan pl;
   const long long cap_blocks = cap > 0 ? (cap + attn::kDecBlock - 1) / attn::kDecBlock : 1;
   const long long pre_blocks = (prefix_len + attn::kDecBlock - 1) / attn::kDecBlock;
-  pl.row_tiles = dec_row_tiles(prefix_here ? (long long)B * GT : GT);
-  pl.row_blocks = (int)((GT + 16 * pl.row_tiles - 1) / (16 * pl.row_tiles));
+  const long long most_rows = prefix_here ? (long long)B * GT : GT;
+  pl.tile_rows = most_rows <= 8 ? 8 : 16;
+  pl.row_tiles = most_rows <= 16 ? 1 : most_rows <= 32 ? 2 : 4;
+  pl.unit_rows = pl.tile_rows * pl.row_tiles;
+  pl.row_blocks = (int)((GT + pl.unit_rows - 1) / pl.unit_rows);
   long long units = (long long)B * Hkv * pl.row_blocks;
   double blocks = (double)units * (double)cap_blocks;
   bool split = cap_blocks > kDecShortBlocks;
   if (prefix_here) {
     const long long rows = (long long)B * GT;
-    pl.prefix_row_blocks = (int)((rows + 16 * pl.row_tiles - 1) / (16 * pl.row_tiles));
+    pl.prefix_row_blocks = (int)((rows + pl.unit_rows - 1) / pl.unit_rows);
     blocks += (double)Hkv * pl.prefix_row_blocks * (double)pre_blocks;
     units += (long long)Hkv * pl.prefix_row_blocks;
     split = split || pre_blocks > kDecShortBlocks;
@@ -128,8 +131,7 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   pl.grid = (unsigned)(most < (double)ctas ? (long long)most : ctas);
   if (pl.grid < 1) pl.grid = 1;
   pl.join = split || shared;
-  const int slot_rows = 16 * pl.row_tiles;
-  const size_t slots = split ? 2 * (size_t)pl.grid * slot_rows : 0;
+  const size_t slots = split ? 2 * (size_t)pl.grid * pl.unit_rows : 0;
   pl.slot_o = slots * D * sizeof(float);
   pl.slot_ml = slots * sizeof(float2);
   const size_t rows = shared ? ((size_t)B * Hkv * (size_t)GT + 63) / 64 * 64 : 0;
@@ -138,7 +140,7 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   return pl;
 }
 
-template <int D, bool kF8>
+template <int D, bool kF8, int kN>
 int launch_decode_dim(attn::DecParams& p, const DecPlan& pl, const void* k, const void* v, cudaStream_t s) {
   using Cfg = attn::DecCfg<D, kF8>;
   static DecodeDeviceInfo info[kMaxDevices];
@@ -147,7 +149,7 @@ int launch_decode_dim(attn::DecParams& p, const DecPlan& pl, const void* k, cons
   if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevices)) e = cudaErrorInvalidDevice;
   if (e == cudaSuccess) {
     std::call_once(info[dev].once, [&] {
-      info[dev].err = cudaFuncSetAttribute(reinterpret_cast<const void*>(attn::attn_decode_kernel<D, kF8>),
+      info[dev].err = cudaFuncSetAttribute(reinterpret_cast<const void*>(attn::attn_decode_kernel<D, kF8, kN>),
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, attn::kDecSmem);
     });
     e = info[dev].err;
@@ -169,7 +171,7 @@ int launch_decode_dim(attn::DecParams& p, const DecPlan& pl, const void* k, cons
     std::memset(&mk, 0, sizeof(mk));
     std::memset(&mv, 0, sizeof(mv));
   }
-  attn::attn_decode_kernel<D, kF8><<<pl.grid, attn::kDecThreads, attn::kDecSmem, s>>>(mk, mv, p);
+  attn::attn_decode_kernel<D, kF8, kN><<<pl.grid, attn::kDecThreads, attn::kDecSmem, s>>>(mk, mv, p);
   if (pl.join)
     attn::attn_decode_join_kernel<D>
         <<<(unsigned)((long long)p.B * p.Hkv * p.row_blocks), attn::kDecThreads, 0, s>>>(p, pl.grid);
@@ -184,7 +186,7 @@ int launch_decode(attn::DecParams& p, const DecPlan& pl, const void* k, const vo
   p.prefix_row_blocks = pl.prefix_row_blocks;
   p.whole_units = pl.whole_units;
   p.min_share = pl.whole_units ? 1 : kDecMinShare;
-  p.slot_rows = 16 * pl.row_tiles;
+  p.unit_rows = pl.unit_rows;
   char* w = static_cast<char*>(workspace);
   p.slot_o = reinterpret_cast<float*>(w);
   p.slot_ml = reinterpret_cast<float2*>(w + pl.slot_o);
@@ -194,12 +196,17 @@ int launch_decode(attn::DecParams& p, const DecPlan& pl, const void* k, const vo
     p.area_ml[i] = shared ? reinterpret_cast<float2*>(w + pl.area_o) : nullptr;
     w += pl.area_o + pl.area_ml;
   }
-  const bool f8 = p.ks != nullptr;
+  auto go = [&](auto dim) {
+    constexpr int D_ = decltype(dim)::value;
+    if (pl.tile_rows == 8)
+      return p.ks ? launch_decode_dim<D_, true, 1>(p, pl, k, v, s) : launch_decode_dim<D_, false, 1>(p, pl, k, v, s);
+    return p.ks ? launch_decode_dim<D_, true, 2>(p, pl, k, v, s) : launch_decode_dim<D_, false, 2>(p, pl, k, v, s);
+  };
   switch (D) {
-    case 32: return f8 ? launch_decode_dim<32, true>(p, pl, k, v, s) : launch_decode_dim<32, false>(p, pl, k, v, s);
-    case 64: return f8 ? launch_decode_dim<64, true>(p, pl, k, v, s) : launch_decode_dim<64, false>(p, pl, k, v, s);
-    case 96: return f8 ? launch_decode_dim<96, true>(p, pl, k, v, s) : launch_decode_dim<96, false>(p, pl, k, v, s);
-    default: return f8 ? launch_decode_dim<128, true>(p, pl, k, v, s) : launch_decode_dim<128, false>(p, pl, k, v, s);
+    case 32: return go(std::integral_constant<int, 32>());
+    case 64: return go(std::integral_constant<int, 64>());
+    case 96: return go(std::integral_constant<int, 96>());
+    default: return go(std::integral_constant<int, 128>());
   }
 }
 
