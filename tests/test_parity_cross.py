@@ -72,6 +72,18 @@ def test_forward(attn, d, B, hq, hkv, nq, nk, lens):
         check(f64(o[b]), f64(lse[b]), want, d, s, n)
 
 
+@pytest.mark.parametrize("lens", [[0] * 9, [0, 0, 0, 0, 0, 0, 0, 0, 130], [130] + [0] * 8, [0, 0, 0, 0, 200, 0, 0, 0, 1],
+                                  [1, 1, 1, 1, 1, 1, 1, 1, 1]])
+def test_forward_runs_of_batch_rows_without_keys(attn, lens):
+    """More tiles without a key in a row than the kernel's ring of units holds, before, behind and between others."""
+    q, k, v, _ = case(7, 9, 6, 3, 150, 260, 32, lens)
+    o, lse = attn.forward_cross(q.cuda(), k.cuda(), v.cuda(), k_lens=gpu_lens(lens))
+    settled(attn)
+    for b, n in enumerate(lens):
+        check(f64(o[b]), f64(lse[b]), attend(f64(q[b]), f64(k[b, :, :n]), f64(v[b, :, :n]), [n] * 150, 32 ** -0.5), 32,
+              32 ** -0.5, n)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3, 2.5])
 @pytest.mark.parametrize("nq", [3, 200])
 def test_forward_scales(attn, scale, nq):

@@ -190,25 +190,27 @@ __global__ void __launch_bounds__(256) attn_cache_read_kernel(CacheView c, __nv_
   vo[1] = o[1][1];
 }
 
-// Two E4M3 codes in the high bytes of r's halves -> a bf16 pair (their low bytes are ignored).
-__device__ __forceinline__ uint32_t e4m3_hi2_to_bf16(uint32_t r) {
-  const uint32_t x = ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u);   // value * 2^-120
-  uint32_t y;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x7b807b80u));  // 2^120
-  return y;
+// Products of bf16 pairs (nearest even; subnormal operands and results count).
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
-// An E8M0 factor as a bf16 pair, and four E4M3 codes times such a pair -> two bf16 pairs, exactly.
+// Two E4M3 codes in the high bytes of r's halves (the low bytes are ignored) as a bf16 pair times
+// 2^-120, exactly: the sign stays, exponent and mantissa move four bits down.
+__device__ __forceinline__ uint32_t e4m3_hi2_bits(uint32_t r) { return ((r >> 4) & 0x07f007f0u) | (r & 0x80008000u); }
+
+// Four E4M3 codes times 2^-120 f -> two bf16 pairs, exactly where the products are bf16 numbers.
+__device__ __forceinline__ uint2 e4m3x4_scaled(uint32_t w, uint32_t f) {
+  return make_uint2(mul_bf16x2(e4m3_hi2_bits(__byte_perm(w, 0u, 0x1000)), f),
+                    mul_bf16x2(e4m3_hi2_bits(__byte_perm(w, 0u, 0x3020)), f));
+}
+
+// An E8M0 factor as a bf16 pair.
 __device__ __forceinline__ uint32_t e8_bf16x2(int e8) {
   const uint32_t b = e8 == kE8Nan ? 0x7fc0u : e8 == 0 ? 0x0040u : (uint32_t)e8 << 7;
   return b | (b << 16);
-}
-
-__device__ __forceinline__ uint2 e4m3x4_times(uint32_t w, uint32_t f) {
-  uint2 r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.x) : "r"(e4m3_hi2_to_bf16(__byte_perm(w, 0u, 0x1000))), "r"(f));
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r.y) : "r"(e4m3_hi2_to_bf16(__byte_perm(w, 0u, 0x3020))), "r"(f));
-  return r;
 }
 
 }  // namespace attn

@@ -94,10 +94,14 @@ struct DecParams {
   // shared prefix: whole units go here instead of o, lse, indexed like o: [0] own keys, [1] prefix
   float* area_o[2];
   float2* area_ml[2];
-  // partial results of the prefix from the tensor-core kernel: [prefix_splits][B*Hkv*GT]
-  int prefix_splits;
-  const float* split_o;
-  const float2* split_ml;
+  // the prefix's results from the many-row kernel (tiles > 0): slots of 128 rows, two a CTA for parts of
+  // units and then a unit's own; a unit is a tile of a head, of `blocks` blocks
+  struct {
+    const float* o;
+    const float2* ml;
+    int tiles, seqs, seq_tiles, blocks;
+    long long share, ctas;
+  } many;
 };
 
 __device__ __forceinline__ int dec_len(const DecParams& p, int b) {
@@ -924,7 +928,16 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
       const long long a0 = ((long long)h * p.prefix_row_blocks + pr / per) * pre_nblk;
       add_unit(a0, a0 + pre_nblk, 1, pr % per);
     }
-    for (int s = 0; s < p.prefix_splits; ++s) add(p.split_o, p.split_ml, (long long)s * p.B * p.Hkv * p.GT + row);
+    if (p.many.tiles > 0) {
+      const int tile = p.many.seq_tiles > 1 ? b * p.many.seq_tiles + i / 128 : b / p.many.seqs;
+      const int mr = p.many.seq_tiles > 1 ? i % 128 : b % p.many.seqs * p.GT + i;
+      const long long mu = (long long)h * p.many.tiles + tile;
+      const long long a0 = mu * p.many.blocks, f = a0 / p.many.share, e = (a0 + p.many.blocks - 1) / p.many.share;
+      if (f == e) add(p.many.o, p.many.ml, (2 * p.many.ctas + mu) * 128 + mr);
+      else
+        for (long long c = f; c <= e; ++c)
+          add(p.many.o, p.many.ml, (2 * c + ((c == f && a0 != c * p.many.share) ? 1 : 0)) * 128 + mr);
+    }
     add_unit(u0, u1, 0, r);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     *reinterpret_cast<uint2*>(p.o + row * D + d) =

@@ -1,10 +1,10 @@
 // attn_fwd_rows_kernel.cuh -- attention of many query rows to keys of another length on B200
 // (sm_100a): cross attention, and the prefix that a decoding batch shares.
 //
-// The same computation as attn_fwd_colsplit_kernel.cuh -- one 128-row tile per unit, two score
-// buffers, each 128-key block's columns split between two softmax warpgroups with maxima, sums and
-// accumulators of their own, joined exactly at the end of the unit -- without a causal mask, and
-// with rows and keys that come from elsewhere:
+// The computation is attn_fwd_colsplit_kernel.cuh's -- one 128-row tile per unit, two score buffers,
+// each 128-key block's columns split between two softmax warpgroups with maxima, sums and
+// accumulators of their own, joined exactly at the end of the unit -- without a causal mask, and with
+// rows, keys and work that come from elsewhere:
 //
 //  * Rows.  All query rows that see the same keys may share a tile: the group * Nq rows of a KV head
 //    (contiguous in q), or for a shared prefix those of several sequences, which a four-dimensional
@@ -12,16 +12,20 @@
 //  * Keys, bf16: contiguous, or in pages, by TMA boxes of the largest of 128, 64, 32, 16 rows that
 //    divides a page.  Each batch row has its own count of them; the MMA warp overwrites the last
 //    value tile's rows behind it with zeros (its probabilities are 0, and 0 * NaN would not be).
-//  * Keys, E4M3 (kF8): a fourth warpgroup loads codes and exponents, converts them to bf16 exactly
-//    (a power-of-two scale rounds nothing) and stores them as TMA would, 128-byte swizzled; the next
-//    tile's loads are in flight meanwhile.  Converting once per 128 rows costs less than the
-//    exponentials of the same block, which bound the kernel, so it is hidden.
-//  * Results: O (bf16) and LSE; or (kPart) unnormalised fp32 O, maximum and sum of the unit's part
-//    of the keys, which a second kernel joins: used when the units alone would not fill the GPU and
-//    for prefixes.
+//  * Keys, E4M3 (kF8): codes and exponents go by TMA to a raw ring; a fourth warpgroup converts them
+//    to bf16, exactly (a power-of-two scale rounds nothing), and stores them as TMA would, 128-byte
+//    swizzled.  One conversion serves 128 rows and is hidden behind their exponentials.
+//  * Work: as in the decode kernel, the 128-key blocks of all units stand in one line and each CTA
+//    takes an equal, contiguous range of it, whatever the lengths; a range holds whole units and at
+//    most two parts of units, which go unnormalised, in fp32, to the CTA's two slots of the workspace
+//    and are joined by a second kernel.  (Dealing whole units out left the GPU a third idle for the
+//    uneven lengths of B8 H16 Nq500 Nk<=1500.)  One warp finds the range and hands the units to the
+//    other roles through a ring in shared memory: their code is then small enough for the
+//    instruction cache (each role computing its own schedule took 130 KB of code, and 20 to 30 % of
+//    the time).
 //
-//   warps 0-3, 4-7  softmax warpgroups     warp 8  TMA producer (kF8: Q only)     warp 9  MMA issuer
-//   warp 10  output store (not kPart)      warp 11 idle      warps 12-15 (kF8) converters
+//   warps 0-3, 4-7  softmax warpgroups     warp 8   TMA producer     warp 9  MMA issuer
+//   warp 10  output store (cross)          warp 11  scheduler        warps 12-15 (kF8) converters
 //
 // Every mbarrier wait is bounded; named barriers are only reached by all their participants.
 #pragma once
@@ -29,7 +33,6 @@
 #include <cuda_bf16.h>
 
 #include "attn_cache_kernel.cuh"
-#include "attn_fwd_colsplit_kernel.cuh"
 
 namespace attn {
 
@@ -40,6 +43,7 @@ enum : unsigned {
   kSiteRowsEpilogue = 44,
   kSiteRowsStore = 45,
   kSiteRowsConvert = 46,
+  kSiteRowsSchedule = 47,
 };
 
 // Register split.  bf16: the forward kernel's (384 threads at 168).  kF8: 512 threads at 128;
@@ -55,68 +59,135 @@ struct RowsCfg {
                 "register split exceeds the launch allocation");
 };
 
+constexpr int kRowsQueue = 4;   // units in the scheduler's ring
+constexpr int kRowsPoly = 2;    // column pairs of every 8 whose exponentials use the polynomial
+
+template <int D, bool kF8>
+struct RowsSmem {
+  static_assert(D == 32 || D == 64 || D == 96 || D == 128, "head dim must be 32, 64, 96 or 128");
+  static constexpr int kChunks = (D + 63) / 64;          // 64-column (128-byte) swizzle chunks of a bf16 row
+  static constexpr int kChunkBytes = kBlockM * 128;
+  static constexpr int kTileBytes = kChunks * kChunkBytes;
+  static constexpr int kStages = kF8 ? (kChunks == 2 ? 3 : 6) : (kChunks == 2 ? 4 : 8);   // K/V ring (bf16 tiles)
+  static constexpr int kRaw = kF8 ? 3 : 0;                // raw ring (E4M3 tiles and their exponents)
+  static constexpr int kRawBytes = kBlockN * D;
+  static constexpr int kOChunks = D / 32;                 // 32-column output chunks (64-byte rows)
+  static constexpr int kStageBytes = kBlockM * 64;        // one staged output chunk: 8 KB
+  static_assert(kOChunks * kStageBytes <= kTileBytes, "staged O must fit in a Q buffer");
+  static constexpr int kQOff = 0;                         // two Q buffers (O staging after their last use)
+  static constexpr int kKVOff = 2 * kTileBytes;
+  static constexpr int kRawOff = kKVOff + kStages * kTileBytes;
+  static constexpr int kExpOff = kRawOff + kRaw * kRawBytes;
+  static constexpr int kXOff = kExpOff + kRaw * kBlockN;  // (m, l) exchange [unit parity][warpgroup][row]
+  static constexpr int kUnitOff = kXOff + 2 * 2 * kBlockM * 8;
+  static constexpr int kBarOff = kUnitOff + kRowsQueue * 32;
+  // q_full[2] q_empty[2] o_staged[2] kv_full[S] kv_empty[S] s_full[2] p_full[2 buffers][2 halves]
+  // pv_done o_full o_free drain u_full[Q] u_empty[Q] raw_full[R] raw_empty[R]
+  static constexpr int kNumBars = 6 + 2 * kStages + 2 + 4 + 4 + 2 * kRowsQueue + 2 * kRaw;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem base, abort flag
+  static constexpr int kAlloc = kMiscOff + 16 + 1024;      // slack for 1024-byte alignment
+  static_assert(kAlloc <= 232448, "many-row kernel shared memory plan exceeds 227 KB");
+};
+
 struct RowsParams {
   float* lse;                // [B][Hkv][GT]
-  __nv_bfloat16* o;          // rows without a key are zeroed directly
-  float* part_o;             // kPart: [parts][B*Hkv*GT][D]
-  float2* part_ml;           // kPart: [parts][B*Hkv*GT]
+  __nv_bfloat16* o;          // [B][Hkv][GT][D]
+  // unnormalised results [slot][128 rows][D] and (max, sum) [slot][128]: two slots a CTA for parts of
+  // units; prefix: whole units' after them, by unit
+  float* slot_o;
+  float2* slot_ml;
   int B, Hkv, GT;
-  int num_units;             // key groups * parts * tiles
-  int tiles, parts;
-  int prefix;                // 0: a key group is (b, h); 1: it is h, with rows of all sequences
+  int tiles;                 // of a key group: (b, h), or for a prefix h
+  int prefix;                // 1: a tile has rows of all sequences
   int seqs;                  // sequences in a tile (prefix; else 1)
   int seq_tiles;             // tiles of a sequence (prefix with GT > 128; else 1)
-  int q_box_rows;            // rows a Q tile load fills: min(GT, 128) * seqs (box 128 rows when seqs == 1)
+  int q_box_rows;            // rows a Q tile load fills
+  int min_share;             // blocks a CTA takes at least
   const int* k_lens;         // [B] or null
-  int len_all;               // keys where k_lens is null
-  int max_len;               // keys there is room for
+  int len_all;               // keys where k_lens is null; no batch row has more
   // paged keys
   const int* table;          // or null: page b
   int page, num_pages;
   int box;                   // key rows of a TMA box
-  const void* k;             // kF8: codes and exponents
-  const void* v;
-  const uint8_t* ks;
+  const uint8_t* ks;         // kF8: exponents
   const uint8_t* vs;
   float c;                   // |scale| * log2(e)
   uint32_t idesc_s;          // S = Q K^T: 128 x 128 x D (negates A when scale < 0)
   uint32_t idesc_pv;         // O_h += P_h V_h: 128 x D x 64
 };
 
+// A unit as the scheduler hands it out: the tile's first sequence, first row and head, the sequence
+// of its keys, the 128-key blocks [jb, je) and the keys; where the result goes: -1 to O and LSE, else
+// the slot.  je < 0 ends the CTA's work.
 struct RowsUnit {
-  int b0, i0, h;  // first sequence, first row and head of the tile
-  int b;          // sequence of the keys (cross)
-  int part;
-  int jb, je;     // 128-key blocks
-  int len;        // keys
+  int b0, i0, h, b;
+  int jb, je, len, slot;
+};
+static_assert(sizeof(RowsUnit) == 32, "queue entry");
+
+__device__ __forceinline__ int rows_len(const RowsParams& p, int b) {
+  return p.k_lens != nullptr ? max(0, min(__ldg(p.k_lens + b), p.len_all)) : p.len_all;
+}
+__device__ __forceinline__ int rows_blocks(int len) {
+  return max(1, (int)(((long long)len + kBlockN - 1) / kBlockN));
+}
+
+// The line of blocks: key group by key group (sequences and heads; heads for a prefix), tile by tile.
+struct RowsLine {
+  long long total, share;
 };
 
-__device__ __forceinline__ void rows_unit(const RowsParams& p, int u, RowsUnit& w) {
-  const int per_group = p.tiles * p.parts;
-  const int group = u / per_group;
-  int r = u - group * per_group;
-  w.part = r / p.tiles;
-  const int tile = r - w.part * p.tiles;
-  if (p.prefix) {
-    w.h = group;
-    w.b = 0;
-    w.b0 = p.seq_tiles > 1 ? tile / p.seq_tiles : tile * p.seqs;
-    w.i0 = p.seq_tiles > 1 ? (tile - w.b0 * p.seq_tiles) * kBlockM : 0;
-  } else {
-    w.b = w.b0 = group / p.Hkv;
-    w.h = group - w.b * p.Hkv;
-    w.i0 = tile * kBlockM;
+// One warp: the line, and the sequence that holds position x with the position of its first block
+// (find >= 0: those of sequence `find`).
+__device__ __forceinline__ RowsLine rows_locate(const RowsParams& p, unsigned ctas, long long x_cta, int find, int& b,
+                                                long long& first) {
+  const int lane = threadIdx.x & 31;
+  const long long per_seq = (long long)p.Hkv * p.tiles;
+  RowsLine ln;
+  const int n = p.prefix ? 1 : p.B;
+  long long total = 0;
+  for (int c = 0; c < n; c += 32) total += c + lane < n ? rows_blocks(rows_len(p, c + lane)) : 0;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+  ln.total = total * per_seq;
+  ln.share = max((long long)p.min_share, (ln.total + ctas - 1) / ctas);
+  const long long x = x_cta * ln.share;
+  b = n;
+  first = ln.total;
+  long long at = 0;
+  for (int c = 0; c < n; c += 32) {
+    const long long mine = c + lane < n ? per_seq * rows_blocks(rows_len(p, c + lane)) : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    const long long begin = at + incl - mine;
+    const unsigned hit =
+        __ballot_sync(0xffffffffu, find >= 0 ? c + lane == find : (mine > 0 && x >= begin && x < begin + mine));
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      b = c + src;
+      first = __shfl_sync(0xffffffffu, begin, src);
+      break;
+    }
+    at += __shfl_sync(0xffffffffu, incl, 31);
   }
-  w.len = p.k_lens != nullptr ? __ldg(p.k_lens + w.b) : p.len_all;
-  w.len = max(0, min(w.len, p.max_len));
-  const long long nb = ((long long)w.len + kBlockN - 1) / kBlockN;
-  w.jb = (int)(nb * w.part / p.parts);
-  w.je = (int)(nb * (w.part + 1) / p.parts);
+  return ln;
+}
+
+// First sequence, row and head of tile `tile` of key group (b, h).
+__device__ __forceinline__ void rows_tile(const RowsParams& p, int b, int h, int tile, RowsUnit& w) {
+  w.b = b;
+  w.h = h;
+  w.b0 = !p.prefix ? b : p.seq_tiles > 1 ? tile / p.seq_tiles : tile * p.seqs;
+  w.i0 = (p.prefix ? (p.seq_tiles > 1 ? tile - w.b0 * p.seq_tiles : 0) : tile) * kBlockM;
 }
 
 // Row r of the tile: its index in q, o, lse, or -1 where the tile has no such row.
-__device__ __forceinline__ long long rows_index(const RowsParams& p, const RowsUnit& w, int r) {
-  int b = w.b0, i = w.i0 + r;
+__device__ __forceinline__ long long rows_index(const RowsParams& p, int b0, int i0, int h, int r) {
+  int b = b0, i = i0 + r;
   if (p.prefix && p.seq_tiles == 1) {
     const int s = r / p.GT;
     if (s >= p.seqs) return -1;
@@ -124,34 +195,7 @@ __device__ __forceinline__ long long rows_index(const RowsParams& p, const RowsU
     i -= s * p.GT;
   }
   if (b >= p.B || i >= p.GT) return -1;
-  return ((long long)b * p.Hkv + w.h) * p.GT + i;
-}
-
-// Position in the CTA's sequence of (unit, key block) pairs; units without a block are skipped.
-struct RowsCursor {
-  int next;       // next unit index
-  RowsUnit w;
-  int j = 0;
-  int u = -1;     // ordinal of the current unit among this CTA's units with blocks
-  bool valid = false;
-};
-
-__device__ __forceinline__ void rows_next_unit(const RowsParams& p, RowsCursor& c) {
-  for (; c.next < p.num_units;) {
-    rows_unit(p, c.next, c.w);
-    c.next += (int)gridDim.x;
-    if (c.w.jb < c.w.je) {
-      c.valid = true;
-      c.j = c.w.jb;
-      ++c.u;
-      return;
-    }
-  }
-  c.valid = false;
-}
-
-__device__ __forceinline__ void rows_advance(const RowsParams& p, RowsCursor& c) {
-  if (++c.j >= c.w.je) rows_next_unit(p, c);
+  return ((long long)b * p.Hkv + h) * p.GT + i;
 }
 
 // 4-D tiled bulk tensor load global -> shared, as tma_load_3d.
@@ -164,14 +208,44 @@ ATTN_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int 
       : "memory");
 }
 
-template <int D, bool kPart, bool kF8>
+// 1-D bulk copy global -> shared (16-byte aligned addresses, size a multiple of 16).
+ATTN_DEV void rows_bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// 2^x for a pair on the FMA pipe, as exp2_poly2 but with a degree-5 polynomial (csrc/fit_exp2_poly.py
+// 5: largest relative error 2.4e-7 in fp32).  The degree-3 one is 7e-5 low at the row's maximum,
+// which shows in the LSE of rows with few keys.
+ATTN_DEV float2 exp2_poly5(float2 x) {
+  constexpr float kRound = 12582912.0f;
+  x.x = fmaxf(x.x, -125.0f);
+  x.y = fmaxf(x.y, -125.0f);
+  const float2 j = add2(x, make_float2(kRound, kRound));
+  const float2 n = add2(j, make_float2(-kRound, -kRound));
+  const float2 f = fma2(n, make_float2(-1.0f, -1.0f), x);
+  float2 q = fma2(make_float2(0.0013276472454890609f, 0.0013276472454890609f), f,
+                  make_float2(0.009675540961325169f, 0.009675540961325169f));
+  q = fma2(q, f, make_float2(0.05550713092088699f, 0.05550713092088699f));
+  q = fma2(q, f, make_float2(0.24022120237350464f, 0.24022120237350464f));
+  q = fma2(q, f, make_float2(0.6931469440460205f, 0.6931469440460205f));
+  q = fma2(q, f, make_float2(1.0000001192092896f, 1.0000001192092896f));
+  float2 r;
+  r.x = __int_as_float(__float_as_int(q.x) + (__float_as_int(j.x) << 23));
+  r.y = __int_as_float(__float_as_int(q.y) + (__float_as_int(j.y) << 23));
+  return r;
+}
+
+template <int D, bool kF8>
 __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
     attn_fwd_rows_sm100(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ CUtensorMap tmap_o,
                         const RowsParams p) {
-  using Plan = CsPlan<D>;
+  using Plan = RowsSmem<D, kF8>;
   using Cfg = RowsCfg<kF8>;
-  constexpr int S = Plan::kStages;
+  constexpr int S = Plan::kStages, R = Plan::kRaw;
   constexpr int kSSteps = D / 16;  // K = 16 steps of S = Q K^T
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -179,10 +253,13 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
 
   uint8_t* sQ = smem + Plan::kQOff;
   uint8_t* sKV = smem + Plan::kKVOff;
+  uint8_t* sRaw = smem + Plan::kRawOff;
+  uint8_t* sExp = smem + Plan::kExpOff;
   float2* xml = reinterpret_cast<float2*>(smem + Plan::kXOff);
+  int4* units = reinterpret_cast<int4*>(smem + Plan::kUnitOff);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Plan::kBarOff);
   uint64_t* q_full = bars;                 // [2]
-  uint64_t* q_empty = bars + 2;            // [2]: released by the store warp, or (kPart) after the unit's last S
+  uint64_t* q_empty = bars + 2;            // [2]: by the store warp, or (results to a slot) after the unit's last S
   uint64_t* o_staged = bars + 4;           // [2]: the unit's O is staged in Q buffer [qb]
   uint64_t* kv_full = bars + 6;            // [S]
   uint64_t* kv_empty = kv_full + S;        // [S]
@@ -192,6 +269,10 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
   uint64_t* o_full = pv_done + 1;
   uint64_t* o_free = pv_done + 2;
   uint64_t* drain = pv_done + 3;
+  uint64_t* u_full = pv_done + 4;          // [kRowsQueue]
+  uint64_t* u_empty = u_full + kRowsQueue; // [kRowsQueue]
+  uint64_t* raw_full = u_empty + kRowsQueue;  // [R]
+  uint64_t* raw_empty = raw_full + R;         // [R]
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Plan::kMiscOff);
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + Plan::kMiscOff + 4);
 
@@ -202,18 +283,27 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
-      mbar_init(&o_staged[i], 2 * kBlockM);
+      mbar_init(&o_staged[i], 8);
       mbar_init(&s_full[i], 1);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], kBlockM);
+    for (int i = 0; i < 4; ++i) mbar_init(&p_full[i], 4);
     for (int i = 0; i < S; ++i) {
-      mbar_init(&kv_full[i], kF8 ? 128 : 1);
+      mbar_init(&kv_full[i], kF8 ? 4 : 1);
       mbar_init(&kv_empty[i], 1);
     }
     mbar_init(pv_done, 1);
     mbar_init(o_full, 1);
-    mbar_init(o_free, 2 * kBlockM);
+    mbar_init(o_free, 8);
     mbar_init(drain, 1);
+    for (int i = 0; i < kRowsQueue; ++i) {
+      mbar_init(&u_full[i], 1);
+      // softmax warps, producer, MMA warp, store warp, converter warps
+      mbar_init(&u_empty[i], 8 + 1 + 1 + (p.prefix ? 0 : 1) + (kF8 ? 4 : 0));
+    }
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
+    }
     *abort_flag = 0u;
     fence_mbar_init();
   }
@@ -223,104 +313,209 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
   }
   if (warp == 8 && lane == 0) {
     tma_prefetch_desc(&tmap_q);
-    if (!kF8) {
-      tma_prefetch_desc(&tmap_k);
-      tma_prefetch_desc(&tmap_v);
-    }
-    if (!kPart) tma_prefetch_desc(&tmap_o);
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_v);
+    if (!p.prefix) tma_prefetch_desc(&tmap_o);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  if (warp == 8) {
+  // Unit `ord` of the ring, once the scheduler has written it (false: a wait gave up).
+  auto take = [&](uint32_t ord, RowsUnit& w, unsigned site) -> bool {
+    const uint32_t q = ord % kRowsQueue;
+    if (!wait_phase(&u_full[q], (ord / kRowsQueue) & 1u, abort_flag, site)) return false;
+    const int4 a = units[2 * q], b = units[2 * q + 1];
+    w = RowsUnit{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    return true;
+  };
+  auto release = [&](uint32_t ord) { mbar_arrive(&u_empty[ord % kRowsQueue]); };
+  // A position in the CTA's sequence of (unit, key block) pairs.
+  struct Cursor {
+    uint32_t ord = 0u;   // units taken
+    int j = 0;
+    bool valid = false;
+    RowsUnit w;
+  };
+  // The next unit (valid = false: none, or a wait gave up); with `give` the one left behind is given
+  // back.  `wide`: a whole warp calls (every lane has read a unit before one gives it back), else one
+  // lane.  (A role's first cursor keeps nothing back: it is never more than two units ahead of its
+  // second, and the ring holds four.)
+  auto next_unit = [&](Cursor& c, bool give, bool wide, unsigned site) {
+    if (c.valid && give) {
+      if (wide) __syncwarp();
+      if (!wide || lane == 0) release(c.ord - 1u);
+    }
+    c.valid = take(c.ord, c.w, site) && c.w.je >= 0;   // (the end marker is given back by no one)
+    c.j = c.w.jb;
+    ++c.ord;
+  };
+
+  if (warp == 11) {
+    // ------------------------------------------------------------ scheduler
+    regs_decrease<Cfg::kControl>();
+    int b;
+    long long first;
+    const RowsLine ln = rows_locate(p, gridDim.x, blockIdx.x, -1, b, first);
+    const long long begin = (long long)blockIdx.x * ln.share, end = min(ln.total, begin + ln.share);
+    const long long per_seq = (long long)p.Hkv * p.tiles;
+    uint32_t ord = 0u;
+    bool ok = true;
+    auto put = [&](const RowsUnit& w) {
+      const uint32_t q = ord % kRowsQueue;
+      if (ord >= kRowsQueue)
+        ok = wait_phase(&u_empty[q], (ord / kRowsQueue - 1u) & 1u, abort_flag, kSiteRowsSchedule);
+      if (!ok) return;
+      units[2 * q] = make_int4(w.b0, w.i0, w.h, w.b);
+      units[2 * q + 1] = make_int4(w.jb, w.je, w.len, w.slot);
+      mbar_arrive(&u_full[q]);
+      ++ord;
+    };
+    // Twice over the range: the units with keys to the ring (one lane), then zeros for those without
+    // (the whole warp, while the last units are computed).
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      int seq = b;
+      long long at = first;
+      for (long long x = begin; x < end && ok;) {
+        RowsUnit w;
+        w.len = rows_len(p, seq);
+        const int nblk = rows_blocks(w.len);
+        const int unit = (int)((x - at) / nblk);
+        const int blk0 = (int)((x - at) - (long long)unit * nblk);
+        const int blk1 = (int)min((long long)nblk, blk0 + (end - x));
+        const int h = unit / p.tiles;
+        rows_tile(p, seq, h, unit - h * p.tiles, w);
+        if (pass == 0 && w.len > 0 && lane == 0) {
+          const bool whole = blk0 == 0 && blk1 == nblk;
+          w.jb = blk0;
+          w.je = blk1;
+          w.slot = !whole ? 2 * (int)blockIdx.x + (x == begin ? 0 : 1) : p.prefix ? 2 * (int)gridDim.x + unit : -1;
+          put(w);
+        }
+        if (pass == 1 && w.len == 0) {
+          const int n = min(kBlockM, p.GT - w.i0);   // (cross attention: a tile's rows are contiguous)
+          const long long row = ((long long)seq * p.Hkv + h) * p.GT + w.i0;
+          for (int i = lane; i < n * (D / 8); i += 32)
+            reinterpret_cast<uint4*>(p.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+          for (int i = lane; i < n; i += 32) p.lse[row + i] = -INFINITY;
+        }
+        x += blk1 - blk0;
+        if (x >= at + per_seq * nblk) {
+          at += per_seq * nblk;
+          ++seq;
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (pass == 0 && ok && lane == 0) {
+        RowsUnit w{};
+        w.je = -1;
+        put(w);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
     regs_decrease<Cfg::kControl>();
     if (lane == 0) {
       const uint64_t pol_kv = l2_policy_evict_last();
       const uint64_t pol_q = l2_policy_evict_first();
+      constexpr int kLoadStages = kF8 ? R : S;
+      uint64_t* full = kF8 ? raw_full : kv_full;
+      uint64_t* empty = kF8 ? raw_empty : kv_empty;
       Ring ring;
       uint32_t filled = 0u, fill_par = 0u;      // per stage: ever filled / parity of its last fill
       uint32_t q_par = 3u, q_filled = 0u, q_fill_par = 0u;   // per Q buffer, as in the column-split kernel
       // Block j of the unit's keys: one box, or several that lie one after the other in the tile.
       // Boxes behind the last key are not loaded (their rows are masked, and V's overwritten).
-      auto load_kv = [&](const CUtensorMap* map, const RowsUnit& w, int j) -> bool {
-        if (!wait_phase(&kv_empty[ring.stage], ring.phase ^ 1u, abort_flag, kSiteRowsProducer)) return false;
+      auto load_kv = [&](bool is_k, const RowsUnit& w, int j) -> bool {
+        if (!wait_phase(&empty[ring.stage], ring.phase ^ 1u, abort_flag, kSiteRowsProducer)) return false;
+        const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
+        uint64_t* bar = &full[ring.stage];
         const int rows = min(kBlockN, w.len - j * kBlockN);
         const int boxes = (rows + p.box - 1) / p.box;
-        mbar_arrive_expect_tx(&kv_full[ring.stage], (uint32_t)(boxes * p.box * 128 * Plan::kChunks));
-        uint8_t* dst = sKV + ring.stage * Plan::kTileBytes;
+        uint32_t bytes = (uint32_t)(boxes * p.box) * (kF8 ? (uint32_t)D : 128u * Plan::kChunks);
+        if constexpr (kF8) {
+          // exponents: one copy a box; for no page, ones (the codes are zeros)
+          uint8_t* dst = sExp + ring.stage * kBlockN;
+          for (int i = 0; i < boxes; ++i) {
+            const int pg = (j * kBlockN + i * p.box) / p.page;
+            if ((unsigned)__ldg(p.table + pg) < (unsigned)p.num_pages) {
+              bytes += (uint32_t)p.box;
+            } else {
+              for (int q = 0; q < p.box; q += 16)
+                *reinterpret_cast<uint4*>(dst + i * p.box + q) =
+                    make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+              fence_proxy_async_smem();
+            }
+          }
+        }
+        mbar_arrive_expect_tx(bar, bytes);
         for (int i = 0; i < boxes; ++i) {
-          const int pos = j * kBlockN + i * p.box;
-          int id = w.b, row = pos;
+          int id = w.b, row = j * kBlockN + i * p.box;
           if (p.table != nullptr) {
-            const int pg = pos / p.page;
+            const int pg = row / p.page;
             id = __ldg(p.table + pg);
-            row = pos - pg * p.page;
+            row -= pg * p.page;
           }
           // a page that is none lies outside the tensor: zeros
-          const int plane = (unsigned)id < (unsigned)p.num_pages ? id * p.Hkv + w.h : p.num_pages * p.Hkv;
+          const bool is_page = (unsigned)id < (unsigned)p.num_pages;
+          const int plane = is_page ? id * p.Hkv + w.h : p.num_pages * p.Hkv;
+          if constexpr (kF8) {
+            tma_load_3d(sRaw + ring.stage * Plan::kRawBytes + i * p.box * D, map, bar, 0, row, plane, pol_kv);
+            if (is_page)
+              rows_bulk_load(sExp + ring.stage * kBlockN + i * p.box,
+                             (is_k ? p.ks : p.vs) + ((long long)plane * p.page + row), (uint32_t)p.box, bar);
+          } else {
+            uint8_t* dst = sKV + ring.stage * Plan::kTileBytes + i * p.box * 128;
 #pragma unroll
-          for (int ch = 0; ch < Plan::kChunks; ++ch)
-            tma_load_3d(dst + ch * Plan::kChunkBytes + i * p.box * 128, map, &kv_full[ring.stage], ch * 64, row, plane,
-                        pol_kv);
+            for (int ch = 0; ch < Plan::kChunks; ++ch)
+              tma_load_3d(dst + ch * Plan::kChunkBytes, map, bar, ch * 64, row, plane, pol_kv);
+          }
         }
         filled |= 1u << ring.stage;
         fill_par = (fill_par & ~(1u << ring.stage)) | (ring.phase << ring.stage);
-        ring.advance<S>();
+        ring.advance<kLoadStages>();
         return true;
       };
-      // The unit's Q tile when the block is its first, then (bf16) the block's K.
-      auto load_k = [&](const RowsCursor& c) -> bool {
-        if (c.j == c.w.jb) {
-          const int qb = c.u & 1;
-          if (!wait_phase(&q_empty[qb], (q_par >> qb) & 1u, abort_flag, kSiteRowsProducer)) return false;
-          q_par ^= 1u << qb;
-          mbar_arrive_expect_tx(&q_full[qb], (uint32_t)(p.q_box_rows * 128 * Plan::kChunks));
-#pragma unroll
-          for (int ch = 0; ch < Plan::kChunks; ++ch)
-            tma_load_4d(sQ + qb * Plan::kTileBytes + ch * Plan::kChunkBytes, &tmap_q, &q_full[qb], ch * 64, c.w.i0,
-                        c.w.h, c.w.b0, pol_q);
-          if (q_filled & (1u << qb)) q_fill_par ^= 1u << qb;
-          q_filled |= 1u << qb;
-        }
-        return kF8 ? true : load_kv(&tmap_k, c.w, c.j);
-      };
-      RowsCursor sc, pc;
-      sc.next = pc.next = (int)blockIdx.x;
-      rows_next_unit(p, sc);
+      // Tiles in the order the MMA warp reads them: K(0), K(1), then V(g), K(g+2) for g = 0, 1, ...
+      Cursor sc, pc;
+      next_unit(sc, false, false, kSiteRowsProducer);
+      next_unit(pc, true, false, kSiteRowsProducer);
       bool ok = true;
-      if constexpr (kF8) {
-        while (ok && sc.valid) {
-          ok = load_k(sc);
-          rows_next_unit(p, sc);
+      for (int i = 0; ok && (sc.valid || pc.valid); ++i) {
+        if (i >= 2) {
+          if (!pc.valid || !(ok = load_kv(false, pc.w, pc.j))) break;
+          if (++pc.j >= pc.w.je) next_unit(pc, true, false, kSiteRowsProducer);
         }
-      } else {
-        rows_next_unit(p, pc);
-        // The order the MMA warp reads the ring in: K(0), K(1), then V(g), K(g+2) for g = 0, 1, ...
-        for (int i = 0; i < 2 && ok && sc.valid; ++i) {
-          ok = load_k(sc);
-          rows_advance(p, sc);
-        }
-        while (ok && pc.valid) {
-          ok = load_kv(&tmap_v, pc.w, pc.j);
-          if (ok && sc.valid) {
-            ok = load_k(sc);
-            rows_advance(p, sc);
+        if (sc.valid) {
+          if (sc.j == sc.w.jb) {   // the unit's Q tile
+            const int qb = (int)(sc.ord - 1u) & 1;
+            if (!(ok = wait_phase(&q_empty[qb], (q_par >> qb) & 1u, abort_flag, kSiteRowsProducer))) break;
+            q_par ^= 1u << qb;
+            mbar_arrive_expect_tx(&q_full[qb], (uint32_t)(p.q_box_rows * 128 * Plan::kChunks));
+#pragma unroll
+            for (int ch = 0; ch < Plan::kChunks; ++ch)
+              tma_load_4d(sQ + qb * Plan::kTileBytes + ch * Plan::kChunkBytes, &tmap_q, &q_full[qb], ch * 64, sc.w.i0,
+                          sc.w.h, sc.w.b0, pol_q);
+            if (q_filled & (1u << qb)) q_fill_par ^= 1u << qb;
+            q_filled |= 1u << qb;
           }
-          rows_advance(p, pc);
+          if (!(ok = load_kv(true, sc.w, sc.j))) break;
+          if (++sc.j >= sc.w.je) next_unit(sc, false, false, kSiteRowsProducer);
         }
       }
       // Drain: every issued copy must have landed before the CTA may exit.
-      for (int s = 0; s < S; ++s)
-        if (filled & (1u << s)) drain_phase(&kv_full[s], (fill_par >> s) & 1u, abort_flag);
+      for (int s = 0; s < kLoadStages; ++s)
+        if (filled & (1u << s)) drain_phase(&full[s], (fill_par >> s) & 1u, abort_flag);
       for (int t = 0; t < 2; ++t)
         if (q_filled & (1u << t)) drain_phase(&q_full[t], (q_fill_par >> t) & 1u, abort_flag);
     }
     __syncwarp();
   } else if (warp == 9) {
-    // ------------------------------------------------------------ MMA issuer (as the column-split kernel's)
+    // ------------------------------------------------------------ MMA issuer
+    // The whole warp walks the units (warp-uniform control flow); one elected lane issues.
     regs_decrease<Cfg::kControl>();
     {
       Ring ring;
@@ -331,63 +526,14 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
       const uint64_t desc_v = smem_desc_mnmajor_sw128(smem_u32(sKV), Plan::kChunkBytes);
       const uint32_t idesc_s = p.idesc_s, idesc_pv = p.idesc_pv;
       auto adv = [](uint64_t d, uint32_t bytes) -> uint64_t { return d + (uint64_t)(bytes >> 4); };
-      auto commit = [&](uint64_t* bar) {
-        if (elect_one()) tc_commit(bar);
-        __syncwarp();
-      };
       auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
         const bool mine = wait_phase(bar, parity, abort_flag, kSiteRowsMma);
         return __all_sync(0xffffffffu, mine);
       };
-      auto next_stage = [&](bool& ok) -> uint32_t {
-        const uint32_t st = ring.stage;
-        ok = wait_all(&kv_full[st], ring.phase);
-        ring.advance<S>();
-        return st;
-      };
-      uint32_t gs = 0;  // blocks whose S has been issued
-      auto issue_s = [&](const RowsCursor& c) -> bool {
-        const int qb = c.u & 1;
-        if (c.j == c.w.jb) {
-          if (!wait_all(&q_full[qb], (q_par >> qb) & 1u)) return false;
-          q_par ^= 1u << qb;
-        }
-        bool ok;
-        const uint32_t st = next_stage(ok);
-        if (!ok) return false;
-        tc_fence_after();
-        const uint64_t da = adv(desc_q, qb * Plan::kTileBytes);
-        const uint64_t db = adv(desc_k, st * Plan::kTileBytes);
-        const uint32_t d_tmem = tmem + (gs & 1u) * 128;
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < kSSteps; ++kk) {
-            const uint32_t off = (kk >> 2) * Plan::kChunkBytes + (kk & 3) * 32;
-            mma_ss(d_tmem, adv(da, off), adv(db, off), idesc_s, kk > 0 ? 1u : 0u);
-          }
-        }
-        __syncwarp();
-        commit(&s_full[gs & 1u]);
-        commit(&kv_empty[st]);
-        if (kPart && c.j == c.w.je - 1) commit(&q_empty[qb]);
-        ++gs;
-        return true;
-      };
-      auto issue_pv = [&](int h, uint32_t sbuf, uint32_t vst, bool accumulate) {
-        const uint64_t dv = adv(desc_v, vst * Plan::kTileBytes);
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts(tmem + 256 + 128 * h, tmem + sbuf * 128 + 64 * h + kk * 8, adv(dv, (4 * h + kk) * 2048),
-                   idesc_pv, (accumulate || kk > 0) ? 1u : 0u);
-        }
-        __syncwarp();
-      };
       // Rows of the unit's last V tile behind its keys become zeros (the converters do it for kF8;
       // TMA does where the keys end with the tensor).
-      auto clear_padding = [&](const RowsCursor& c, uint32_t st) {
-        const int first = c.w.len - c.j * kBlockN;
-        if (kF8 || first >= kBlockN || (p.table == nullptr && c.w.len == p.page)) return;
+      auto clear_padding = [&](int first, uint32_t st) {
+#pragma unroll 1
         for (int i = first * 8 + lane; i < kBlockN * 8; i += 32)
 #pragma unroll
           for (int ch = 0; ch < Plan::kChunks; ++ch)
@@ -395,45 +541,78 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       };
-
-      RowsCursor sc, pc;
-      sc.next = pc.next = (int)blockIdx.x;
-      rows_next_unit(p, sc);
-      rows_next_unit(p, pc);
+      Cursor sc, pc;
+      next_unit(sc, false, true, kSiteRowsMma);
+      next_unit(pc, true, true, kSiteRowsMma);
       bool ok = true;
-      for (int i = 0; i < 2 && ok && sc.valid; ++i) {
-        ok = issue_s(sc);
-        rows_advance(p, sc);
-      }
-      uint32_t gp = 0;  // blocks whose P V has been issued
-      while (ok && pc.valid) {
-        const uint32_t b = gp & 1u, ph = (gp >> 1) & 1u;
-        const bool first = pc.j == pc.w.jb;
-        if (!(ok = wait_all(&p_full[2 * b], ph))) break;
-        if (first) {
-          if (!(ok = wait_all(o_free, of_par))) break;
-          of_par ^= 1u;
+      // S(i) goes to score buffer i & 1 after P(i-2) V(i-2) has been issued (issue order).
+      for (uint32_t i = 0; ok && __all_sync(0xffffffffu, sc.valid || pc.valid); ++i) {
+        if (i >= 2u) {
+          const uint32_t g = i - 2u, b = g & 1u, ph = (g >> 1) & 1u;
+          if (!__all_sync(0xffffffffu, pc.valid)) break;
+          const bool first = pc.j == pc.w.jb, last = pc.j == pc.w.je - 1;
+          const uint32_t vst = ring.stage;
+          if (!(ok = wait_all(&kv_full[vst], ring.phase))) break;
+          ring.advance<S>();
+          const int live = pc.w.len - pc.j * kBlockN;
+          if (!kF8 && live < kBlockN && !(p.table == nullptr && pc.w.len == p.page)) clear_padding(live, vst);
+          if (first) {
+            if (!(ok = wait_all(o_free, of_par))) break;
+            of_par ^= 1u;
+          }
+          const uint64_t dv = adv(desc_v, vst * Plan::kTileBytes);
+          // O_h += P_h(g) V(g)[64h : 64h+64]: four K = 16 steps, P_h from TMEM (8 columns per step),
+          // V as an MN-major operand (16 key rows of 128 bytes per step)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!(ok = wait_all(&p_full[2 * b + h], ph))) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(tmem + 256 + 128 * h, tmem + b * 128 + 64 * h + kk * 8, adv(dv, (4 * h + kk) * 2048), idesc_pv,
+                       (!first || kk > 0) ? 1u : 0u);
+              if (h == 1) {
+                tc_commit(pv_done);
+                tc_commit(&kv_empty[vst]);
+                if (last) tc_commit(o_full);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (++pc.j >= pc.w.je) next_unit(pc, true, true, kSiteRowsMma);
         }
-        const uint32_t vst = next_stage(ok);
-        if (!ok) break;
-        clear_padding(pc, vst);
-        tc_fence_after();
-        issue_pv(0, b, vst, !first);
-        if (!(ok = wait_all(&p_full[2 * b + 1], ph))) break;
-        tc_fence_after();
-        issue_pv(1, b, vst, !first);
-        commit(pv_done);
-        commit(&kv_empty[vst]);
-        if (pc.j == pc.w.je - 1) commit(o_full);
-        if (sc.valid) {
-          if (!(ok = issue_s(sc))) break;
-          rows_advance(p, sc);
+        if (__all_sync(0xffffffffu, sc.valid)) {
+          const int qb = (int)(sc.ord - 1u) & 1;
+          const bool last = sc.j == sc.w.je - 1;
+          if (sc.j == sc.w.jb) {
+            if (!(ok = wait_all(&q_full[qb], (q_par >> qb) & 1u))) break;
+            q_par ^= 1u << qb;
+          }
+          const uint32_t st = ring.stage;
+          if (!(ok = wait_all(&kv_full[st], ring.phase))) break;
+          ring.advance<S>();
+          tc_fence_after();
+          const uint64_t da = adv(desc_q, qb * Plan::kTileBytes);
+          const uint64_t db = adv(desc_k, st * Plan::kTileBytes);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < kSSteps; ++kk) {
+              const uint32_t off = (kk >> 2) * Plan::kChunkBytes + (kk & 3) * 32;
+              mma_ss(tmem + (i & 1u) * 128, adv(da, off), adv(db, off), idesc_s, kk > 0 ? 1u : 0u);
+            }
+            tc_commit(&s_full[i & 1u]);
+            tc_commit(&kv_empty[st]);
+            if (last && sc.w.slot >= 0) tc_commit(&q_empty[qb]);
+          }
+          __syncwarp();
+          if (++sc.j >= sc.w.je) next_unit(sc, false, true, kSiteRowsMma);
         }
-        ++gp;
-        rows_advance(p, pc);
       }
       // Drain: all MMAs issued by this warp complete before TMEM is released.
-      commit(drain);
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
       drain_phase(drain, 0u, abort_flag);
     }
     __syncwarp();
@@ -449,28 +628,21 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
     uint32_t g = 0, o_par = 0;
     bool ok = true;
     int u = 0;
-    for (int unit = blockIdx.x; ok && unit < p.num_units; unit += (int)gridDim.x) {
+    for (uint32_t ord = 0; ok; ++ord) {
       RowsUnit w;
-      rows_unit(p, unit, w);
-      const long long row = rows_index(p, w, r);
-      if (w.jb == w.je) {
-        // no keys (in this part): nothing is computed, the row's result is empty
-        if (row >= 0) {
-          if constexpr (kPart) {
-            if (h == 0) p.part_ml[(long long)w.part * p.B * p.Hkv * p.GT + row] = make_float2(-INFINITY, 0.f);
-          } else {
-            for (int ch = h; ch < Plan::kOChunks; ch += 2)
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                reinterpret_cast<uint4*>(p.o + row * D + ch * 32)[q] = make_uint4(0u, 0u, 0u, 0u);
-            if (h == 0) p.lse[row] = -INFINITY;
-          }
-        }
-        continue;
+      if (!__all_sync(0xffffffffu, take(ord, w, kSiteRowsSoftmax)) || w.je < 0) {
+        // the end, or a wait that gave up: each warp leaves through one more agreement, which those
+        // still in a unit join with its own
+        bar_and(7, 2 * kBlockM, false);
+        break;
       }
+      __syncwarp();
+      if (lane == 0) release(ord);
+      const long long row = rows_index(p, w.b0, w.i0, w.h, r);
       const int key_lim = w.len - 1;
       float m = -INFINITY, l = 0.f;
 
+#pragma unroll 1
       for (int j = w.jb; j < w.je; ++j, ++g) {
         if (!ok) continue;  // after a failed wait: reach the end-of-unit agreement without further waits
         const uint32_t b = g & 1u;
@@ -526,7 +698,7 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
           // S(g) completing implies P(g-2) V has; P(g-1) V may still be running.
           if (!(ok = wait_phase(pv_done, (g - 1u) & 1u, abort_flag, kSiteRowsSoftmax))) continue;
           tc_fence_after();
-#pragma unroll
+#pragma unroll 1
           for (int ch = 0; ch < D / 32; ++ch) {
             uint32_t ov[32];
             tmem_ld32(t_oh + ch * 32, ov);
@@ -548,8 +720,8 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
           for (int i = 0; i < 64; i += 2) {
             const float2 x = fma2(make_float2(s[i], s[i + 1]), c2, nm2);
             float2 pr;
-            if (((i >> 1) & 7) < poly_pairs_per8<D>()) {
-              pr = exp2_poly2(x);
+            if (((i >> 1) & 7) < kRowsPoly) {
+              pr = exp2_poly5(x);
             } else {
               pr.x = ex2_approx(x.x);
               pr.y = ex2_approx(x.y);
@@ -563,7 +735,8 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_full[2 * b + h]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * b + h]);
       }
 
       // ---- end of the unit: agree on success, exchange (m_h, l_h), join and write O and LSE.
@@ -578,16 +751,17 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
       const float a0 = (ml0.x == -INFINITY) ? 0.f : ex2_approx(ml0.x - mt);
       const float a1 = (ml1.x == -INFINITY) ? 0.f : ex2_approx(ml1.x - mt);
       const float lt = fmaf(ml1.y, a1, ml0.y * a0);
-      const float inv_l = kPart ? 1.f : 1.f / lt;
+      const float inv_l = w.slot >= 0 ? 1.f : 1.f / lt;
       const float w0 = a0 * inv_l, w1 = a1 * inv_l;
       tc_fence_after();
       if (h >= Plan::kOChunks) {
         // no output chunk for this warpgroup (D = 32): its O columns are not read
         tc_fence_before();
-        mbar_arrive(o_free);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_free);
       }
       const uint32_t stage_row = smem_u32(sQ + (u & 1) * Plan::kTileBytes) + r * 64;
-#pragma unroll
+#pragma unroll 1
       for (int ch = h; ch < Plan::kOChunks; ch += 2) {
         uint32_t x0[32], x1[32];
         tmem_ld32(t_o0 + ch * 32, x0);
@@ -598,47 +772,52 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
         if (ch + 2 >= Plan::kOChunks) {
           // this warpgroup's last reads of O: the next unit's P V may overwrite it
           tc_fence_before();
-          mbar_arrive(o_free);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
         }
-        auto joined = [&](int i) { return fmaf(__uint_as_float(x1[i]), w1, __uint_as_float(x0[i]) * w0); };
-        if constexpr (kPart) {
-          if (row >= 0) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)w.part * p.B * p.Hkv * p.GT + row) * D + ch * 32);
+        float x[32];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(joined(4 * i), joined(4 * i + 1), joined(4 * i + 2), joined(4 * i + 3));
+        for (int i = 0; i < 32; ++i) x[i] = fmaf(__uint_as_float(x1[i]), w1, __uint_as_float(x0[i]) * w0);
+        if (w.slot >= 0) {
+          float4* dst = reinterpret_cast<float4*>(p.slot_o + ((long long)w.slot * kBlockM + r) * D + ch * 32);
+          if (row >= 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
           }
         } else {
-          // staged in this unit's Q buffer, 64-byte swizzle, as in the column-split kernel
-          uint32_t packed[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) packed[i] = pack_bf16x2(joined(2 * i), joined(2 * i + 1));
+          // staged in this unit's Q buffer (its last S has completed), 64-byte swizzle, as in the
+          // column-split kernel
           const uint32_t row_addr = stage_row + ch * Plan::kStageBytes;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            st_shared_v4(row_addr + ((q ^ ((r >> 1) & 3)) << 4), packed[4 * q], packed[4 * q + 1], packed[4 * q + 2],
-                         packed[4 * q + 3]);
+            st_shared_v4(row_addr + ((q ^ ((r >> 1) & 3)) << 4), pack_bf16x2(x[8 * q], x[8 * q + 1]),
+                         pack_bf16x2(x[8 * q + 2], x[8 * q + 3]), pack_bf16x2(x[8 * q + 4], x[8 * q + 5]),
+                         pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
         }
       }
-      if constexpr (kPart) {
-        if (h == 0 && row >= 0) p.part_ml[(long long)w.part * p.B * p.Hkv * p.GT + row] = make_float2(mt, lt);
+      if (w.slot >= 0) {
+        if (h == 0) p.slot_ml[(long long)w.slot * kBlockM + r] = make_float2(mt, lt);
       } else {
         // make the staged rows visible to the TMA (async proxy), then hand them to the store warp
         fence_proxy_async_smem();
-        mbar_arrive(&o_staged[u & 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_staged[u & 1]);
         if (h == 0 && row >= 0) p.lse[row] = (mt + log2f(lt)) * 0.69314718055994530942f;
       }
       ++u;
     }
-  } else if (warp == 10 && !kPart) {
-    // ------------------------------------------------------------ output store warp (as the column-split kernel's)
+  } else if (warp == 10) {
+    // ------------------------------------------------------------ output store warp (cross attention)
+    // Per whole unit: wait until both softmax warpgroups have staged O in the unit's Q buffer, store
+    // it with TMA tensor stores (rows past the tensor are not written), wait until the stores have
+    // read the buffer and give it back to the producer.
     regs_decrease<Cfg::kControl>();
-    if (lane == 0) {
+    if (lane == 0 && !p.prefix) {
       uint32_t st_par = 0u;  // bit qb: parity of the next wait on o_staged[qb]
-      RowsCursor c;
-      c.next = (int)blockIdx.x;
-      for (rows_next_unit(p, c); c.valid; rows_next_unit(p, c)) {
-        const int qb = c.u & 1;
+      Cursor c;
+      for (next_unit(c, true, false, kSiteRowsStore); c.valid; next_unit(c, true, false, kSiteRowsStore)) {
+        if (c.w.slot >= 0) continue;
+        const int qb = (int)(c.ord - 1u) & 1;
         if (!wait_phase(&o_staged[qb], (st_par >> qb) & 1u, abort_flag, kSiteRowsStore)) break;
         st_par ^= 1u << qb;
         const uint8_t* stage = sQ + qb * Plan::kTileBytes;
@@ -653,87 +832,81 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
       bulk_wait_group0();
     }
     __syncwarp();
-  } else if (warp < 12) {
-    regs_decrease<Cfg::kControl>();
   } else if constexpr (kF8) {
-    // ------------------------------------------------------------ converters: E4M3 pages -> bf16 tiles
-    // A 128-row tile takes kPasses passes; in each, kLanes lanes share a row (16 codes each) and the
-    // warpgroup covers kRows rows, a whole number of 16-row groups or a whole fraction of one.
+    // ------------------------------------------------------------ converters: E4M3 -> bf16 tiles
+    // A 128-row tile takes kPasses passes; in each, kLanes lanes share a row (16 codes each).
     regs_decrease<Cfg::kConvert>();
     constexpr int kLanes = D / 16;                    // 2, 4, 6, 8
-    constexpr int kRows = kLanes == 6 ? 16 : 128 / kLanes;   // D = 96: 96 of the 128 threads have a piece
+    constexpr int kRows = 128 / kLanes / 16 * 16;     // 64, 32, 16 (96 of the 128 threads), 16
     constexpr int kPasses = kBlockN / kRows;
     const int tid = threadIdx.x - 384;
-    const int pr = tid / kLanes, piece = tid - pr * kLanes;
+    const int pr = tid / kLanes, col = (tid - pr * kLanes) * 16;
     const bool mine = pr < kRows;
-    Ring ring;
+    const uint32_t at = (uint32_t)((col >> 6) * Plan::kChunkBytes), q = (uint32_t)(col & 63) >> 3;
+    Ring ring, raw;
     bool ok = true;
-    auto load_tile = [&](const RowsCursor& c, bool is_k, uint4 (&w)[kPasses], uint32_t (&e)[kPasses]) {
-      const uint8_t* codes = static_cast<const uint8_t*>(is_k ? p.k : p.v);
-      const uint8_t* exps = is_k ? p.ks : p.vs;
+    auto convert = [&](int len, int j) -> bool {
+      if (!wait_phase(&raw_full[raw.stage], raw.phase, abort_flag, kSiteRowsConvert)) return false;
+      const uint8_t* codes = sRaw + raw.stage * Plan::kRawBytes;
+      const uint8_t* exps = sExp + raw.stage * kBlockN;
+      uint4 x[kPasses];
+      uint32_t e[kPasses];
+      uint32_t top = 0u;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const int pos = c.j * kBlockN + i * kRows + pr;
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        e[i] = 127u;
-        if (!mine || pos >= c.w.len) continue;
-        const int pg = pos / p.page;
-        const int id = __ldg(p.table + pg);
-        if ((unsigned)id >= (unsigned)p.num_pages) continue;
-        const long long row = ((long long)id * p.Hkv + c.w.h) * p.page + (pos - pg * p.page);
-        w[i] = __ldg(reinterpret_cast<const uint4*>(codes + row * D) + piece);
-        e[i] = __ldg(exps + row);
+        const int r = i * kRows + pr;
+        const bool live = mine && j * kBlockN + r < len;
+        x[i] = live ? *reinterpret_cast<const uint4*>(codes + r * D + col) : make_uint4(0u, 0u, 0u, 0u);
+        e[i] = live ? exps[r] : 127u;
+        top = max(top, e[i]);
       }
-    };
-    auto store_tile = [&](const uint4 (&w)[kPasses], const uint32_t (&e)[kPasses]) {
-      ok = ok && wait_phase(&kv_empty[ring.stage], ring.phase ^ 1u, abort_flag, kSiteRowsConvert);
-      if (!ok) return;
-      const uint32_t base = smem_u32(sKV) + ring.stage * Plan::kTileBytes;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&raw_empty[raw.stage]);
+      raw.advance<R == 0 ? 1 : R>();
+      if (!wait_phase(&kv_empty[ring.stage], ring.phase ^ 1u, abort_flag, kSiteRowsConvert)) return false;
+      const uint32_t base = smem_u32(sKV) + ring.stage * Plan::kTileBytes + at;
+      // bits -> value * 2^-120, times 2^(e - 7) in one multiplication while that is a bf16 number,
+      // else (exponents above 2^7, and rows marked NaN) times 2^120 and the scale
+      const bool far = __any_sync(0xffffffffu, top > 134u);
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        if (!mine) continue;
-        const int r = i * kRows + pr, col = piece * 16;
-        const uint32_t at = base + (col >> 6) * Plan::kChunkBytes + r * 128;
-        const uint32_t q = (uint32_t)(col & 63) >> 3;
-        const uint32_t f = e8_bf16x2((int)e[i]);
-        const uint2 x0 = e4m3x4_times(w[i].x, f), x1 = e4m3x4_times(w[i].y, f);
-        const uint2 x2 = e4m3x4_times(w[i].z, f), x3 = e4m3x4_times(w[i].w, f);
-        st_shared_v4(at + ((q ^ (r & 7)) << 4), x0.x, x0.y, x1.x, x1.y);
-        st_shared_v4(at + (((q + 1) ^ (r & 7)) << 4), x2.x, x2.y, x3.x, x3.y);
+        const int r = i * kRows + pr;
+        const uint32_t f = far ? 0x7b807b80u : (e[i] + 120u) * 0x00800080u;
+        uint2 y[4] = {e4m3x4_scaled(x[i].x, f), e4m3x4_scaled(x[i].y, f), e4m3x4_scaled(x[i].z, f),
+                      e4m3x4_scaled(x[i].w, f)};
+        if (far) {
+          const uint32_t f2 = e8_bf16x2((int)e[i]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = make_uint2(mul_bf16x2(y[k].x, f2), mul_bf16x2(y[k].y, f2));
+        }
+        if (mine) {
+          const uint32_t row = base + r * 128;
+          st_shared_v4(row + ((q ^ (r & 7)) << 4), y[0].x, y[0].y, y[1].x, y[1].y);
+          st_shared_v4(row + (((q + 1) ^ (r & 7)) << 4), y[2].x, y[2].y, y[3].x, y[3].y);
+        }
       }
       fence_proxy_async_smem();
-      mbar_arrive(&kv_full[ring.stage]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&kv_full[ring.stage]);
       ring.advance<S>();
-    };
-    // Tiles in the order the MMA warp reads them: K(0), K(1), then V(g), K(g+2); the loads of the
-    // next one are issued before the current one is converted.
-    RowsCursor sc, pc;
-    sc.next = pc.next = (int)blockIdx.x;
-    rows_next_unit(p, sc);
-    rows_next_unit(p, pc);
-    int nk = 0, nv = 0;   // K and V tiles handed out
-    auto next_tile = [&](uint4 (&w)[kPasses], uint32_t (&e)[kPasses]) -> bool {
-      if (sc.valid && nk < nv + 2) {
-        load_tile(sc, true, w, e);
-        rows_advance(p, sc);
-        ++nk;
-        return true;
-      }
-      if (!pc.valid) return false;
-      load_tile(pc, false, w, e);
-      rows_advance(p, pc);
-      ++nv;
       return true;
     };
-    uint4 wa[kPasses], wb[kPasses];
-    uint32_t ea[kPasses], eb[kPasses];
-    bool have = next_tile(wa, ea);
-    while (have && ok) {
-      have = next_tile(wb, eb);
-      store_tile(wa, ea);
-      if (!have || !ok) break;
-      have = next_tile(wa, ea);
-      store_tile(wb, eb);
+    Cursor sc, pc;
+    next_unit(sc, false, true, kSiteRowsConvert);
+    next_unit(pc, true, true, kSiteRowsConvert);
+    for (int i = 0; ok && __all_sync(0xffffffffu, sc.valid || pc.valid); ++i) {
+      // V(i-2), then K(i): one copy of the code serves both
+#pragma unroll 1
+      for (int half = 0; half < 2 && ok; ++half) {
+        if ((half == 0 && i < 2) || !__all_sync(0xffffffffu, half ? sc.valid : pc.valid)) continue;
+        ok = __all_sync(0xffffffffu, convert(half ? sc.w.len : pc.w.len, half ? sc.j : pc.j));
+        if (!ok) break;
+        if (half) {
+          if (++sc.j >= sc.w.je) next_unit(sc, false, true, kSiteRowsConvert);
+        } else {
+          if (++pc.j >= pc.w.je) next_unit(pc, true, true, kSiteRowsConvert);
+        }
+      }
     }
   }
 
@@ -745,34 +918,47 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
   }
 }
 
-// Joins the parts of every row in key order: O (bf16) and LSE.  One thread per four columns.
+// Cross attention: joins the parts of every unit that was split, in key order, into O and LSE.  Block
+// (c, y): the unit at the end of CTA c's range, where its first part is in that range; a warp a row,
+// eight rows a block.
 template <int D>
-__global__ void __launch_bounds__(256) attn_rows_join_kernel(const float* __restrict__ part_o,
-                                                             const float2* __restrict__ part_ml, int parts,
-                                                             long long rows, __nv_bfloat16* __restrict__ o,
-                                                             float* __restrict__ lse) {
-  const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  const long long row = idx / (D / 4);
-  const int d = (int)(idx - row * (D / 4)) * 4;
-  if (row >= rows) return;
-  float m = -INFINITY, l = 0.f;
-  for (int s = 0; s < parts; ++s) m = fmaxf(m, part_ml[s * rows + row].x);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < parts; ++s) {
-    const float2 ml = part_ml[s * rows + row];
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;   // a part without keys: nothing was written
-    const float w = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
-    const float4 v = *reinterpret_cast<const float4*>(part_o + (s * rows + row) * D + d);
-    l = fmaf(ml.y, w, l);
-    acc.x = fmaf(v.x, w, acc.x);
-    acc.y = fmaf(v.y, w, acc.y);
-    acc.z = fmaf(v.z, w, acc.z);
-    acc.w = fmaf(v.w, w, acc.w);
+__global__ void __launch_bounds__(256) attn_rows_join_kernel(const RowsParams p, unsigned ctas) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int b;
+  long long first;
+  const RowsLine ln = rows_locate(p, ctas, (long long)blockIdx.x + 1, -1, b, first);
+  const long long x = ((long long)blockIdx.x + 1) * ln.share;
+  if (x >= ln.total) return;
+  const int nblk = rows_blocks(rows_len(p, b));
+  const int unit = (int)((x - first) / nblk);
+  const long long u0 = first + (long long)unit * nblk, u1 = u0 + nblk;
+  // split here, and not before
+  if (u0 == x || u0 / ln.share != blockIdx.x) return;
+  const int r = blockIdx.y * 8 + warp;
+  const int h = unit / p.tiles;
+  RowsUnit w;
+  rows_tile(p, b, h, unit - h * p.tiles, w);
+  const long long row = rows_index(p, w.b0, w.i0, h, r);
+  if (row < 0) return;
+  const long long c0 = blockIdx.x, c1 = (u1 - 1) / ln.share;
+  auto slot = [&](long long c) { return (2 * c + ((c == c0 && u0 != c * ln.share) ? 1 : 0)) * kBlockM + r; };
+  float m = -INFINITY;
+  for (long long c = c0; c <= c1; ++c) m = fmaxf(m, p.slot_ml[slot(c)].x);
+  float l = 0.f;
+  float acc[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+  for (long long c = c0; c <= c1; ++c) {
+    const float2 ml = p.slot_ml[slot(c)];
+    const float a = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - m);
+    l = fmaf(ml.y, a, l);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(p.slot_o[slot(c) * D + 32 * i + lane], a, acc[i]);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  *reinterpret_cast<uint2*>(o + row * D + d) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (d == 0) lse[row] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.69314718055994530942f;
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) p.o[row * D + 32 * i + lane] = __float2bfloat16_rn(acc[i] * inv);
+  if (lane == 0) p.lse[row] = ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.69314718055994530942f;
 }
 
 }  // namespace attn

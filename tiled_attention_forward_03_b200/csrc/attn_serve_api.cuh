@@ -60,9 +60,10 @@ int launch_status(const char* what) {
 }
 
 // A tensor of bf16 (elem_bytes 2) or E4M3 bytes (1) as TMA loads it: `rank` dimensions, D fastest,
-// boxes of 128 bytes of D and the given extents with 128-byte swizzle; elements outside read as zero.
+// boxes of the given extents, with 128-byte swizzle (rows of 128 bytes) or without; elements outside
+// read as zero.
 int encode_rows_map(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims, const cuuint32_t* box,
-                    int elem_bytes = 2) {
+                    int elem_bytes = 2, bool swizzle = true) {
   auto enc = tensor_map_encoder();
   if (!enc) {
     std::snprintf(g_last_cuda_error, sizeof(g_last_cuda_error), "cuTensorMapEncodeTiled entry point unavailable");
@@ -73,7 +74,8 @@ int encode_rows_map(CUtensorMap* map, const void* base, int rank, const cuuint64
   for (int i = 0; i + 1 < rank; ++i) strides[i] = bytes *= dims[i];
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = enc(map, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r == CUDA_SUCCESS) return ATTN_OK;
   record_driver_error("cuTensorMapEncodeTiled", (int)r);
@@ -273,17 +275,17 @@ RowsDeviceInfo g_rows_dev[kMaxDevices];
 template <int D>
 cudaError_t rows_setup_dim() {
   cudaError_t e = cudaSuccess;
-  auto setup = [&](const void* fn, int regs) {
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, attn::CsPlan<D>::kAlloc);
+  auto setup = [&](const void* fn, int regs, int smem) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     cudaFuncAttributes fa{};
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, fn);
     // the register split (setmaxnreg) needs exactly the launch allocation it was sized for
     if (e == cudaSuccess && fa.numRegs != regs) e = cudaErrorInvalidDeviceFunction;
   };
-  setup(reinterpret_cast<const void*>(attn::attn_fwd_rows_sm100<D, false, false>), attn::RowsCfg<false>::kRegsLaunch);
-  setup(reinterpret_cast<const void*>(attn::attn_fwd_rows_sm100<D, true, false>), attn::RowsCfg<false>::kRegsLaunch);
-  setup(reinterpret_cast<const void*>(attn::attn_fwd_rows_sm100<D, true, true>), attn::RowsCfg<true>::kRegsLaunch);
+  setup(reinterpret_cast<const void*>(attn::attn_fwd_rows_sm100<D, false>), attn::RowsCfg<false>::kRegsLaunch,
+        attn::RowsSmem<D, false>::kAlloc);
+  setup(reinterpret_cast<const void*>(attn::attn_fwd_rows_sm100<D, true>), attn::RowsCfg<true>::kRegsLaunch,
+        attn::RowsSmem<D, true>::kAlloc);
   return e;
 }
 
@@ -308,56 +310,33 @@ bool rows_device_setup() {
   return false;
 }
 
-// How many parts the keys of each tile are cut into, so that `units` tiles fill the GPU: the number
-// with the least estimated time, counted in 128-key blocks (about 1 us each): waves of units, each
-// its blocks and two more for its start and end, and four for the joining kernel where it is not
-// needed anyway.
-int rows_parts(long long units, long long blocks, int num_sms, bool parted) {
-  int best = 1;
-  double least = 0;
-  const long long most = blocks / 2 < 64 ? (blocks / 2 < 1 ? 1 : blocks / 2) : 64;
-  for (int n = 1; n <= most; ++n) {
-    const double waves = (double)((units * n + num_sms - 1) / num_sms);
-    const double cost = waves * ((double)((blocks + n - 1) / n) + 2) + (n > 1 && !parted ? 4 : 0);
-    if (n == 1 || cost < least) {
-      best = n;
-      least = cost;
-    }
-  }
-  return best;
-}
-
 template <int D>
 void launch_rows_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
-                     const attn::RowsParams& p, bool part, bool f8, unsigned grid, cudaStream_t s) {
-  constexpr int smem = attn::CsPlan<D>::kAlloc;
+                     const attn::RowsParams& p, bool f8, bool join, unsigned grid, cudaStream_t s) {
   if (f8)
-    attn::attn_fwd_rows_sm100<D, true, true><<<grid, attn::RowsCfg<true>::kThreads, smem, s>>>(mq, mk, mv, mo, p);
-  else if (part)
-    attn::attn_fwd_rows_sm100<D, true, false><<<grid, attn::RowsCfg<false>::kThreads, smem, s>>>(mq, mk, mv, mo, p);
+    attn::attn_fwd_rows_sm100<D, true>
+        <<<grid, attn::RowsCfg<true>::kThreads, attn::RowsSmem<D, true>::kAlloc, s>>>(mq, mk, mv, mo, p);
   else
-    attn::attn_fwd_rows_sm100<D, false, false><<<grid, attn::RowsCfg<false>::kThreads, smem, s>>>(mq, mk, mv, mo, p);
+    attn::attn_fwd_rows_sm100<D, false>
+        <<<grid, attn::RowsCfg<false>::kThreads, attn::RowsSmem<D, false>::kAlloc, s>>>(mq, mk, mv, mo, p);
+  if (join) attn::attn_rows_join_kernel<D><<<dim3(grid - 1, attn::kBlockM / 8), 256, 0, s>>>(p, grid);
 }
 
-template <int D>
-void launch_rows_join_dim(const float* part_o, const float2* part_ml, int parts, long long rows, void* o, float* lse,
-                          cudaStream_t s) {
-  attn::attn_rows_join_kernel<D><<<(unsigned)((rows * (D / 4) + 255) / 256), 256, 0, s>>>(
-      part_o, part_ml, parts, rows, reinterpret_cast<__nv_bfloat16*>(o), lse);
-}
+constexpr int kRowsMinShare = 2;   // blocks of 128 keys
 
-// The tiles of a problem.
+// The tiles of a problem, the grid and the workspace.
 struct RowsPlan {
-  int tiles, seqs = 1, seq_tiles = 1, parts = 1;
-  long long units = 0;             // without the parts
-  size_t part_o = 0, part_ml = 0;  // bytes
-  size_t bytes() const { return part_o + part_ml; }
+  int tiles = 0, seqs = 1, seq_tiles = 1;
+  long long blocks = 0;            // of a unit, at most
+  unsigned grid = 1;
+  size_t slot_o = 0, slot_ml = 0;  // bytes
+  size_t bytes() const { return slot_o + slot_ml; }
 };
 
 RowsPlan rows_plan(int B, int Hkv, long long GT, int D, long long max_len, int num_sms, bool prefix) {
   RowsPlan pl;
-  const long long blocks = (max_len + attn::kBlockN - 1) / attn::kBlockN;
   const long long per_seq = (GT + attn::kBlockM - 1) / attn::kBlockM;
+  pl.blocks = max_len > 0 ? (max_len + attn::kBlockN - 1) / attn::kBlockN : 1;
   if (!prefix) {
     pl.tiles = (int)per_seq;
   } else if (GT <= attn::kBlockM) {
@@ -367,28 +346,27 @@ RowsPlan rows_plan(int B, int Hkv, long long GT, int D, long long max_len, int n
     pl.seq_tiles = (int)per_seq;
     pl.tiles = (int)(B * per_seq);
   }
-  pl.units = (long long)(prefix ? Hkv : (long long)B * Hkv) * pl.tiles;
-  pl.parts = rows_parts(pl.units, blocks, num_sms, prefix);
-  if (prefix || pl.parts > 1) {
-    const size_t rows = ((size_t)B * Hkv * (size_t)GT * pl.parts + 63) / 64 * 64;
-    pl.part_o = rows * D * sizeof(float);
-    pl.part_ml = rows * sizeof(float2);
-  }
+  const long long units = (long long)(prefix ? Hkv : (long long)B * Hkv) * pl.tiles;
+  const double most = (double)units * (double)pl.blocks / kRowsMinShare + 1;
+  pl.grid = most < (double)num_sms ? (unsigned)most : (unsigned)num_sms;
+  const size_t slots = 2 * (size_t)pl.grid + (prefix ? (size_t)units : 0);
+  pl.slot_o = slots * attn::kBlockM * D * sizeof(float);
+  pl.slot_ml = slots * attn::kBlockM * sizeof(float2);
   return pl;
 }
 
 // Fills the sizes and launches; p's key, output and length fields are the caller's.
 int launch_rows(attn::RowsParams& p, const RowsPlan& pl, const void* q, const void* k, const void* v, void* o, int D,
-                bool prefix, bool f8, float scale, void* workspace, int num_sms, cudaStream_t s) {
+                bool prefix, float scale, void* workspace, cudaStream_t s) {
   if (!rows_device_setup()) return ATTN_ERR_CUDA;
+  const bool f8 = p.ks != nullptr;
   p.tiles = pl.tiles;
-  p.parts = pl.parts;
   p.seqs = pl.seqs;
   p.seq_tiles = pl.seq_tiles;
   p.prefix = prefix ? 1 : 0;
-  p.num_units = (int)(pl.units * pl.parts);
-  p.part_o = reinterpret_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + pl.part_o);
+  p.min_share = kRowsMinShare;
+  p.slot_o = reinterpret_cast<float*>(workspace);
+  p.slot_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + pl.slot_o);
   p.o = reinterpret_cast<__nv_bfloat16*>(o);
   const bool many = prefix && pl.seq_tiles == 1;   // a tile holds whole sequences
   p.q_box_rows = many ? p.GT * pl.seqs : attn::kBlockM;
@@ -397,8 +375,6 @@ int launch_rows(attn::RowsParams& p, const RowsPlan& pl, const void* q, const vo
   p.idesc_s = attn::idesc_bf16_f32(attn::kBlockM, attn::kBlockN, false, false, scale < 0.f);
   p.idesc_pv = attn::idesc_bf16_f32(attn::kBlockM, D, false, true, false);
   CUtensorMap mq, mk, mv, mo;
-  std::memset(&mk, 0, sizeof(mk));
-  std::memset(&mv, 0, sizeof(mv));
   std::memset(&mo, 0, sizeof(mo));
   int st;
   const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)p.GT, (cuuint64_t)p.Hkv, (cuuint64_t)p.B};
@@ -407,30 +383,19 @@ int launch_rows(attn::RowsParams& p, const RowsPlan& pl, const void* q, const vo
   p.box = attn::kBlockN;
   if (p.table != nullptr)
     while (p.page % p.box != 0) p.box /= 2;
-  if (!f8) {
-    const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)p.page, (cuuint64_t)p.num_pages * (cuuint64_t)p.Hkv};
-    const cuuint32_t kb[3] = {64, (cuuint32_t)p.box, 1};
-    if ((st = encode_rows_map(&mk, k, 3, kd, kb)) != ATTN_OK) return st;
-    if ((st = encode_rows_map(&mv, v, 3, kd, kb)) != ATTN_OK) return st;
-  }
-  const bool part = pl.part_o > 0;
-  if (!part && (st = encode_map_o(&mo, o, (long long)p.B * p.Hkv, p.GT, D)) != ATTN_OK) return st;
-  const unsigned grid = (unsigned)(p.num_units < num_sms ? p.num_units : num_sms);
+  const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)p.page, (cuuint64_t)p.num_pages * (cuuint64_t)p.Hkv};
+  const cuuint32_t kb[3] = {(cuuint32_t)(f8 ? D : 64), (cuuint32_t)p.box, 1};
+  if ((st = encode_rows_map(&mk, k, 3, kd, kb, f8 ? 1 : 2, !f8)) != ATTN_OK) return st;
+  if ((st = encode_rows_map(&mv, v, 3, kd, kb, f8 ? 1 : 2, !f8)) != ATTN_OK) return st;
+  if (!prefix && (st = encode_map_o(&mo, o, (long long)p.B * p.Hkv, p.GT, D)) != ATTN_OK) return st;
+  const bool join = !prefix && pl.grid > 1;
   switch (D) {
-    case 32: launch_rows_dim<32>(mq, mk, mv, mo, p, part, f8, grid, s); break;
-    case 64: launch_rows_dim<64>(mq, mk, mv, mo, p, part, f8, grid, s); break;
-    case 96: launch_rows_dim<96>(mq, mk, mv, mo, p, part, f8, grid, s); break;
-    default: launch_rows_dim<128>(mq, mk, mv, mo, p, part, f8, grid, s); break;
+    case 32: launch_rows_dim<32>(mq, mk, mv, mo, p, f8, join, pl.grid, s); break;
+    case 64: launch_rows_dim<64>(mq, mk, mv, mo, p, f8, join, pl.grid, s); break;
+    case 96: launch_rows_dim<96>(mq, mk, mv, mo, p, f8, join, pl.grid, s); break;
+    default: launch_rows_dim<128>(mq, mk, mv, mo, p, f8, join, pl.grid, s); break;
   }
-  if ((st = launch_status("many-row kernel launch")) != ATTN_OK || prefix || !part) return st;
-  const long long rows = (long long)p.B * p.Hkv * p.GT;
-  switch (D) {
-    case 32: launch_rows_join_dim<32>(p.part_o, p.part_ml, pl.parts, rows, o, p.lse, s); break;
-    case 64: launch_rows_join_dim<64>(p.part_o, p.part_ml, pl.parts, rows, o, p.lse, s); break;
-    case 96: launch_rows_join_dim<96>(p.part_o, p.part_ml, pl.parts, rows, o, p.lse, s); break;
-    default: launch_rows_join_dim<128>(p.part_o, p.part_ml, pl.parts, rows, o, p.lse, s); break;
-  }
-  return launch_status("join kernel launch");
+  return launch_status("many-row kernel launch");
 }
 
 // At most this many rows go through the decode kernel; more, through the tensor-core kernel.
@@ -606,21 +571,24 @@ int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cac
     r.B = B;
     r.Hkv = Hkv;
     r.GT = (int)GT;
-    r.len_all = r.max_len = prefix_len;
+    r.len_all = prefix_len;
     r.table = prefix_table;
     r.page = page_size;
     r.num_pages = num_pages;
-    r.k = k_cache;
-    r.v = v_cache;
     r.ks = p.ks;
     r.vs = p.vs;
     char* w = static_cast<char*>(workspace) + pl.dec.bytes();
-    if ((st = launch_rows(r, pl.rows, q, k_cache, v_cache, o, D, true, p.ks != nullptr, scale, w, num_sms, s)) !=
-        ATTN_OK)
-      return st;
-    p.prefix_splits = pl.rows.parts;
-    p.split_o = r.part_o;
-    p.split_ml = r.part_ml;
+    if ((st = launch_rows(r, pl.rows, q, k_cache, v_cache, o, D, true, scale, w, s)) != ATTN_OK) return st;
+    p.many.o = r.slot_o;
+    p.many.ml = r.slot_ml;
+    p.many.tiles = r.tiles;
+    p.many.seqs = r.seqs;
+    p.many.seq_tiles = r.seq_tiles;
+    p.many.blocks = (int)pl.rows.blocks;
+    p.many.ctas = pl.rows.grid;
+    const long long total = (long long)Hkv * r.tiles * pl.rows.blocks;
+    p.many.share = (total + p.many.ctas - 1) / p.many.ctas;
+    if (p.many.share < kRowsMinShare) p.many.share = kRowsMinShare;
   }
   return launch_decode(p, pl.dec, k_cache, v_cache, D, true, workspace, s);
 }
@@ -670,10 +638,10 @@ int attn_fwd_cross(const void* q, const void* k, const void* v, const int* k_len
   r.Hkv = Hkv;
   r.GT = (int)GT;
   r.k_lens = k_lens;
-  r.len_all = r.max_len = Nk;
+  r.len_all = Nk;
   r.page = Nk;
   r.num_pages = B;
-  return launch_rows(r, pl, q, k, v, o, D, false, false, scale, workspace, num_sms, s);
+  return launch_rows(r, pl, q, k, v, o, D, false, scale, workspace, s);
 }
 
 }  // extern "C"
