@@ -8,21 +8,21 @@ import pytest
 BLOCK = 64
 
 
-def blocks_of(n, whole):
-    return 1 if whole else max(1, -(-n // BLOCK))
+def blocks_of(n):
+    return max(1, -(-n // BLOCK))
 
 
 class Line:
-    def __init__(self, lens, hkv, row_blocks, prefix_len, prefix_row_blocks, whole, min_share, ctas):
-        self.lens, self.hkv, self.rb, self.whole = lens, hkv, row_blocks, whole
-        self.pre_nblk = blocks_of(prefix_len, whole) if prefix_len else 0
+    def __init__(self, lens, hkv, row_blocks, prefix_len, prefix_row_blocks, min_share, ctas):
+        self.lens, self.hkv, self.rb = lens, hkv, row_blocks
+        self.pre_nblk = blocks_of(prefix_len) if prefix_len else 0
         self.pre_rb, self.prefix_len = prefix_row_blocks, prefix_len
         self.prefix = hkv * prefix_row_blocks * self.pre_nblk
         self.first = []
         at = self.prefix
         for n in lens:
             self.first.append(at)
-            at += hkv * row_blocks * blocks_of(n, whole)
+            at += hkv * row_blocks * blocks_of(n)
         self.total = at
         self.share = max(min_share, -(-at // ctas))
 
@@ -30,7 +30,7 @@ class Line:
         if x < self.prefix:
             return -1, 0
         for b, n in enumerate(self.lens):
-            if x < self.first[b] + self.hkv * self.rb * blocks_of(n, self.whole):
+            if x < self.first[b] + self.hkv * self.rb * blocks_of(n):
                 return b, self.first[b]
         return len(self.lens), 0
 
@@ -42,7 +42,7 @@ def cta_writes(ln, cta):
     seq, first = ln.locate(begin)
     x = begin
     while x < end:
-        nblk = ln.pre_nblk if seq < 0 else blocks_of(ln.lens[seq], ln.whole)
+        nblk = ln.pre_nblk if seq < 0 else blocks_of(ln.lens[seq])
         rbs = ln.pre_rb if seq < 0 else ln.rb
         unit, blk0 = divmod(x - first, nblk)
         blk1 = min(nblk, blk0 + end - x)
@@ -70,10 +70,9 @@ def test_every_block_once_and_every_part_joined(seed):
     B, hkv, rb = r.choice([1, 2, 3, 7, 40]), r.choice([1, 2, 5]), r.choice([1, 1, 3])
     lens = [r.choice([0, 1, 63, 64, 65, r.randrange(3000)]) for _ in range(B)]
     prefix = r.choice([0, 0, 1, 64, 1000])
-    whole = r.random() < 0.25
-    min_share = 1 if whole else 2
+    min_share = 2
     ctas = r.choice([1, 2, 5, 17, 100, 444])
-    ln = Line(lens, hkv, rb, prefix, r.choice([1, 2]) if prefix else 0, whole, min_share, ctas)
+    ln = Line(lens, hkv, rb, prefix, r.choice([1, 2]) if prefix else 0, min_share, ctas)
     seen, slots, wholes = {}, {}, set()
     for c in range(ctas):
         for key, b0, b1, is_whole, slot in cta_writes(ln, c):
@@ -89,7 +88,7 @@ def test_every_block_once_and_every_part_joined(seed):
     units = [(-1, h, q) for h in range(hkv) for q in range(ln.pre_rb if prefix else 0)]
     units += [(b, h, q) for b in range(B) for h in range(hkv) for q in range(rb)]
     for seq, h, q in units:
-        nblk = ln.pre_nblk if seq < 0 else blocks_of(lens[seq], whole)
+        nblk = ln.pre_nblk if seq < 0 else blocks_of(lens[seq])
         u0 = (0 if seq < 0 else ln.first[seq]) + (h * (ln.pre_rb if seq < 0 else rb) + q) * nblk
         got = parts(ln, u0, u0 + nblk)
         if got == "whole":

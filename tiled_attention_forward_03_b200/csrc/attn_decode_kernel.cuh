@@ -44,6 +44,11 @@
 // second kernel joins the parts of each split unit in key order.  No atomics, no state in the
 // workspace: results depend on the inputs alone.
 //
+// kWarp: many short sequences (one row tile).  Each warp takes whole units of its own, with its own
+// ring; nothing is joined between warps, and a shared prefix's result (computed by the many-row
+// kernel) is joined in registers as the unit is written.  Sharing such units among a CTA's warps took
+// three times as long (B128 Hkv8 N<=256 behind a prefix: 37 us), most of it between units.
+//
 // A CTA's four warps take `row_tiles` tiles of 16 rows (1, 2 or 4; or one of 8) and share the keys 4 / row_tiles
 // ways; the warps of one way share its ring (a stage is refilled once all of them have left it).
 // Their results are joined in shared memory, in the ring's place.  Every wait is bounded.
@@ -83,7 +88,7 @@ struct DecParams {
   // shared prefix handled here (prefix_len > 0): an extra first sequence with all rows of the batch
   const int* prefix_table;
   int prefix_len, prefix_row_blocks;
-  int whole_units;           // 1: CTAs take whole units only (every sequence is short)
+  int whole_units;           // 1: the warp form: warps take whole units
   int min_share;             // blocks a CTA takes at least
   float c;                   // scale * log2(e)
   __nv_bfloat16* o;          // [B][Hkv][GT][D]
@@ -109,8 +114,45 @@ __device__ __forceinline__ int dec_len(const DecParams& p, int b) {
   return (int)max(0LL, min(n, p.cap));
 }
 
-__device__ __forceinline__ int dec_blocks(const DecParams& p, int len) {
-  return p.whole_units ? 1 : max(1, (int)(((long long)len + kDecBlock - 1) / kDecBlock));
+__device__ __forceinline__ int dec_blocks(int len) {
+  return max(1, (int)(((long long)len + kDecBlock - 1) / kDecBlock));
+}
+
+// Weight of a result with running maximum ml.x and sum ml.y against maximum m (none: 0; NaN stays).
+__device__ __forceinline__ float dec_weight(float2 ml, float m) {
+  return ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - m);
+}
+
+// LSE of a row from its maximum (base 2) and sum.
+__device__ __forceinline__ float dec_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.69314718055994530942f;
+}
+
+// Programmatic dependent launch: the next kernel of the stream may start (it waits for this one's
+// end before it reads its results), and the wait for the end of the kernel before.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The many-row kernel's results for row i of sequence b and head h: n of them, rows `at(k)` of
+// p.many.o and p.many.ml.
+struct DecParts {
+  int n;
+  long long f, first_slot, row, whole;
+  __device__ __forceinline__ long long at(int k) const {
+    return (whole >= 0 ? whole : k == 0 ? first_slot : 2 * (f + k)) * 128 + row;
+  }
+};
+__device__ __forceinline__ DecParts dec_prefix_parts(const DecParams& p, int b, int h, int i) {
+  DecParts r;
+  const int tile = p.many.seq_tiles > 1 ? b * p.many.seq_tiles + i / 128 : b / p.many.seqs;
+  r.row = p.many.seq_tiles > 1 ? i % 128 : b % p.many.seqs * p.GT + i;
+  const long long unit = (long long)h * p.many.tiles + tile, u0 = unit * p.many.blocks;
+  r.f = u0 / p.many.share;
+  const long long e = (u0 + p.many.blocks - 1) / p.many.share;
+  r.n = (int)(e - r.f) + 1;
+  r.whole = r.n == 1 ? 2 * p.many.ctas + unit : -1;
+  r.first_slot = 2 * r.f + (u0 != r.f * p.many.share ? 1 : 0);
+  return r;
 }
 
 // The line of blocks: the prefix's first, then sequence by sequence; within a sequence KV head by
@@ -131,7 +173,7 @@ __device__ __forceinline__ DecLine dec_locate(const DecParams& p, unsigned ctas,
   const int per = (p.B + kDecThreads - 1) / kDecThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += dec_blocks(p, dec_len(p, b));
+  for (int b = b0; b < b1; ++b) mine += dec_blocks(dec_len(p, b));
   mine *= per_seq;
   long long incl = mine;
 #pragma unroll
@@ -142,9 +184,7 @@ __device__ __forceinline__ DecLine dec_locate(const DecParams& p, unsigned ctas,
   if (lane == 31) sh[warp] = incl;
   __syncthreads();
   DecLine ln;
-  ln.prefix = p.prefix_len > 0 ? (long long)p.Hkv * p.prefix_row_blocks *
-                                     (p.whole_units ? 1 : (p.prefix_len + kDecBlock - 1) / kDecBlock)
-                               : 0;
+  ln.prefix = p.prefix_len > 0 ? (long long)p.Hkv * p.prefix_row_blocks * ((p.prefix_len + kDecBlock - 1) / kDecBlock) : 0;
   long long before = ln.prefix, total = ln.prefix;
 #pragma unroll
   for (int w = 0; w < kDecThreads / 32; ++w) {
@@ -158,7 +198,7 @@ __device__ __forceinline__ DecLine dec_locate(const DecParams& p, unsigned ctas,
   if (find_seq >= 0 ? (find_seq >= b0 && find_seq < b1) : (x >= at && x < at + mine)) {
     int b = b0;
     for (; b < b1; ++b) {
-      const long long n = per_seq * dec_blocks(p, dec_len(p, b));
+      const long long n = per_seq * dec_blocks(dec_len(p, b));
       if (find_seq >= 0 ? b == find_seq : x < at + n) break;
       at += n;
     }
@@ -323,7 +363,7 @@ __device__ __forceinline__ uint32_t dec_pair(const uint32_t* r0, const uint32_t*
 }
 
 // kN: tiles of 8 rows a warp takes (1: units of at most 8 rows; else 2).
-template <int D, bool kF8, int kN>
+template <int D, bool kF8, int kN, bool kWarp>
 __global__ void __launch_bounds__(kDecThreads, 3)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const DecParams p) {
@@ -358,10 +398,18 @@ __global__ void __launch_bounds__(kDecThreads, 3)
     }
   }
 
-  int seq;
-  long long first;
-  const DecLine ln = dec_locate(p, gridDim.x, blockIdx.x, -1, scratch, seq, first);   // (its barriers order the above)
-  const long long begin = (long long)blockIdx.x * ln.share, end = min(ln.total, begin + ln.share);
+  launch_dependents();
+  int seq = 0;
+  long long first = 0, begin, end;
+  if constexpr (kWarp) {
+    __syncthreads();
+    begin = (long long)blockIdx.x * 4 + warp;
+    end = (long long)p.B * p.Hkv;
+  } else {
+    const DecLine ln = dec_locate(p, gridDim.x, blockIdx.x, -1, scratch, seq, first);   // (its barriers order the above)
+    begin = (long long)blockIdx.x * ln.share;
+    end = min(ln.total, begin + ln.share);
+  }
   // ring positions (stage, parity of its use) of the next issue (the way's first warp) and of the
   // next step, over all units; uses of the ring before its first refill need no wait
   uint32_t i_stage = 0u, i_phase = 0u, i_count = 0u, stage = 0u, phase = 0u;
@@ -369,21 +417,22 @@ __global__ void __launch_bounds__(kDecThreads, 3)
   const int no_plane = p.num_pages * p.Hkv;          // outside the tensor maps: zeros
   bool ok = true;
 
-  for (long long x = begin; x < end;) {
-    // ---- the unit at line position x, and the part of it in this CTA's range
-    const bool prefix = seq < 0;
+  for (long long x = begin; x < end && ok;) {
+    // ---- the unit at line position x, and the part of it in this CTA's range (kWarp: unit x)
+    if constexpr (kWarp) seq = (int)(x / p.Hkv);
+    const bool prefix = !kWarp && seq < 0;
     const int len = prefix ? p.prefix_len : dec_len(p, seq);
-    const int nblk = prefix ? (p.whole_units ? 1 : (len + kDecBlock - 1) / kDecBlock) : dec_blocks(p, len);
+    const int nblk = kWarp ? 1 : prefix ? (len + kDecBlock - 1) / kDecBlock : dec_blocks(len);
     const int row_blocks = prefix ? p.prefix_row_blocks : p.row_blocks;
     const int rows = prefix ? p.B * p.GT : p.GT;
-    const int unit = (int)((x - first) / nblk);
-    const int blk0 = (int)((x - first) - (long long)unit * nblk);
-    const int blk1 = (int)min((long long)nblk, blk0 + (end - x));
-    const int h = unit / row_blocks, rb = unit - h * row_blocks;
+    const int unit = kWarp ? 0 : (int)((x - first) / nblk);
+    const int blk0 = kWarp ? 0 : (int)((x - first) - (long long)unit * nblk);
+    const int blk1 = kWarp ? 1 : (int)min((long long)nblk, blk0 + (end - x));
+    const int h = kWarp ? (int)(x - (long long)seq * p.Hkv) : unit / row_blocks, rb = kWarp ? 0 : unit - h * row_blocks;
     const int* table = prefix ? p.prefix_table : (p.table ? p.table + (size_t)seq * p.max_pages : nullptr);
     const int i0 = (rb * row_tiles + rt) * kTile;   // first row of this warp's tile
-    const int key_begin = p.whole_units ? 0 : blk0 * kDecBlock;
-    const int key_end = p.whole_units ? len : (int)min((long long)len, (long long)blk1 * kDecBlock);
+    const int key_begin = blk0 * kDecBlock;
+    const int key_end = kWarp ? len : (int)min((long long)len, (long long)blk1 * kDecBlock);
 
     // row i of the unit -> its index in q, o, lse
     auto row_index = [&](int i) -> long long {
@@ -392,8 +441,8 @@ __global__ void __launch_bounds__(kDecThreads, 3)
       return ((long long)b * p.Hkv + h) * p.GT + (i - (int)b * p.GT);
     };
     // this way's steps: keys key_begin + (kg + ways * n) * kStep
-    const int stride = ways * Cfg::kStep;
-    const int k_first = key_begin + kg * Cfg::kStep;
+    const int stride = kWarp ? Cfg::kStep : ways * Cfg::kStep;
+    const int k_first = kWarp ? 0 : key_begin + kg * Cfg::kStep;
     const int steps = k_first < key_end ? (key_end - k_first + stride - 1) / stride : 0;
     // page pg of the unit -> its plane in the tensor maps
     auto plane_of = [&](int pg) -> int {
@@ -795,6 +844,53 @@ __global__ void __launch_bounds__(kDecThreads, 3)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[nt][c][e] = o[nt][c][e] * a * b;
     }
+    if constexpr (kWarp) {
+      if (!ok) break;
+      // ---- write the unit: lane (g, t) has rows 2t, 2t + 1 of each tile and the columns of group g
+      if (p.many.tiles > 0) wait_for_previous();   // the prefix's results, from the kernel before
+#pragma unroll
+      for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int i = 8 * nt + 2 * t4 + e;
+          if (i >= rows) continue;
+          const long long row = row_index(i);
+          float mt = m[nt][e], lt = l[nt][e];
+          float acc[D / 8];
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            acc[2 * c] = o[nt][c][e];
+            acc[2 * c + 1] = o[nt][c][2 + e];
+          }
+          if (p.many.tiles > 0) {
+            const DecParts pt = dec_prefix_parts(p, seq, h, i);
+            for (int k = 0; k < pt.n; ++k) {
+              const long long at = pt.at(k);
+              const float2 ml = p.many.ml[at];
+              const float mn = fmaxf(mt, ml.x);
+              const float a = dec_weight(make_float2(mt, lt), mn), w = dec_weight(ml, mn);
+              mt = mn;
+              lt = fmaf(ml.y, w, lt * a);
+#pragma unroll
+              for (int ct = 0; ct < D / 8; ct += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(p.many.o + at * D + dec_col<D, kF8>(ct, g));
+                acc[ct] = fmaf(v.x, w, acc[ct] * a);
+                acc[ct + 1] = fmaf(v.y, w, acc[ct + 1] * a);
+                acc[ct + 2] = fmaf(v.z, w, acc[ct + 2] * a);
+                acc[ct + 3] = fmaf(v.w, w, acc[ct + 3] * a);
+              }
+            }
+          }
+          const float inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll
+          for (int ct = 0; ct < D / 8; ct += 4)
+            *reinterpret_cast<uint2*>(p.o + row * D + dec_col<D, kF8>(ct, g)) =
+                make_uint2(pack_bf16x2(acc[ct] * inv, acc[ct + 1] * inv), pack_bf16x2(acc[ct + 2] * inv, acc[ct + 3] * inv));
+          if (g == 0) p.lse[row] = dec_lse(mt, lt);
+        }
+      x += (long long)gridDim.x * 4;
+      continue;
+    }
     // all rings are empty: the join may take their place, unless a wait gave up
     if (__syncthreads_or(!ok)) {
       ok = false;
@@ -828,7 +924,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int w = 0; w < ways; ++w) {
         const float2 ml = sml[tile + w * row_tiles][rr];
-        const float a = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - mt);
+        const float a = dec_weight(ml, mt);
         const float4 ov = *reinterpret_cast<const float4*>(&so[tile + w * row_tiles][rr][d]);
         lt = fmaf(ml.y, a, lt);
         acc.x = fmaf(ov.x, a, acc.x);
@@ -841,8 +937,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
         const float inv = lt == 0.f ? 0.f : 1.f / lt;
         *reinterpret_cast<uint2*>(p.o + row * D + d) =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-        if (d == 0)
-          p.lse[row] = lt == 0.f ? -INFINITY : ((mt == -INFINITY ? 0.f : mt) + log2f(lt)) * 0.69314718055994530942f;
+        if (d == 0) p.lse[row] = dec_lse(mt, lt);
       } else {
         const long long at = whole ? row_index(unit_row + r) : slot * p.unit_rows + r;
         float* dst = whole ? p.area_o[prefix] : p.slot_o;
@@ -861,6 +956,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
       ++seq;
     }
   }
+  if (!kWarp && p.many.tiles > 0) wait_for_previous();   // the joining kernel relies on the one before, too
   // Drain after a wait gave up: every issued copy lands before the CTA exits.
   if (!ok && rt == 0 && lane == 0)
     for (int i = 0; i < min(stages, (int)i_count); ++i) {
@@ -871,11 +967,14 @@ __global__ void __launch_bounds__(kDecThreads, 3)
 }
 
 // Joins the parts of every split unit in key order, and, behind a shared prefix (area_o set), the
-// prefix's result with each row's own.  One block per (sequence, KV head, row block).  Bound by
-// launch and a few dependent reads; the parts are still in L2.
+// prefix's results with each row's own.  Block (unit, y): a warp for each of four rows of the unit.
+// Lane k takes part k's maximum, sum and place (32 at a time), then the warp adds the parts' rows.
+// Bound by launch and three dependent reads (lengths, sums, rows; the parts are in L2): started by the
+// first kernel's end, it takes about 3 us.
 template <int D>
 __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const DecParams p, unsigned ctas) {
   __shared__ long long scratch[16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned unit = blockIdx.x;
   const unsigned per_seq = (unsigned)p.Hkv * (unsigned)p.row_blocks;
   const int b = (int)(unit / per_seq);
@@ -884,66 +983,72 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
   int seq;
   long long first;
   const DecLine ln = dec_locate(p, ctas, 0, b, scratch, seq, first);
-  const int nblk = dec_blocks(p, dec_len(p, b));
+  const int nblk = dec_blocks(dec_len(p, b));
   const long long u0 = first + (long long)hr * nblk, u1 = u0 + nblk;
-  const long long c0 = u0 / ln.share, c1 = (u1 - 1) / ln.share;
   const bool shared = p.area_o[0] != nullptr;
-  if (!shared && c0 == c1) return;   // written by the one CTA that had it
+  if (!shared && u0 / ln.share == (u1 - 1) / ln.share) return;   // written by the one CTA that had it
+  const int r = (int)blockIdx.y * 4 + warp, i = rb * p.unit_rows + r;
+  if (r >= p.unit_rows || i >= p.GT) return;
+  const long long row = ((long long)b * p.Hkv + h) * p.GT + i;
+  wait_for_previous();
 
-  const int unit_rows = min(p.unit_rows, p.GT - rb * p.unit_rows);
-  // prefix unit of a row (few rows: computed by the same kernel): its parts, if it was split
-  const int pre_nblk = p.whole_units ? 1 : (p.prefix_len + kDecBlock - 1) / kDecBlock;
-  for (int idx = threadIdx.x; idx < unit_rows * (D / 4); idx += kDecThreads) {
-    const int r = idx / (D / 4), d = (idx - r * (D / 4)) * 4;
-    const int i = rb * p.unit_rows + r;
-    const long long row = ((long long)b * p.Hkv + h) * p.GT + i;
-    float m = -INFINITY, l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float* po, const float2* pml, long long at) {
-      const float2 ml = pml[at];
-      if (ml.x == -INFINITY && ml.y == 0.f) return;   // no keys: nothing to add
-      const float4 v = *reinterpret_cast<const float4*>(po + at * D + d);
-      const float mn = fmaxf(m, ml.x);
-      const float a = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2_approx(m - mn);
-      const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - mn);
+  float m = -INFINITY, l = 0.f;
+  float acc[D / 32];
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) acc[c] = 0.f;
+  // n results at rows at(k) of po, pml
+  auto add = [&](int n, const float* po, const float2* pml, auto at) {
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      const bool mine = k0 + lane < n;
+      const long long place = mine ? at(k0 + lane) : 0;
+      const float2 ml = mine ? pml[place] : make_float2(-INFINITY, 0.f);
+      float mn = ml.x;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+      mn = fmaxf(m, mn);
+      const float a = dec_weight(make_float2(m, l), mn), w = dec_weight(ml, mn);
+      float sum = ml.y * w;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       m = mn;
-      l = fmaf(ml.y, w, l * a);
-      acc.x = fmaf(v.x, w, acc.x * a);
-      acc.y = fmaf(v.y, w, acc.y * a);
-      acc.z = fmaf(v.z, w, acc.z * a);
-      acc.w = fmaf(v.w, w, acc.w * a);
-    };
-    // the parts of the unit [a0, a1) of the line; its rows start at `r` of a slot
-    auto add_unit = [&](long long a0, long long a1, int part, int slot_row) {
-      const long long f = a0 / ln.share, e = (a1 - 1) / ln.share;
-      if (f == e) {
-        add(p.area_o[part], p.area_ml[part], row);
-        return;
+      l = fmaf(l, a, sum);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) acc[c] *= a;
+      const int here = min(32, n - k0);
+#pragma unroll 4
+      for (int k = 0; k < here; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const long long pk = __shfl_sync(0xffffffffu, place, k);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) acc[c] = fmaf(po[pk * D + 32 * c + lane], wk, acc[c]);
       }
-      for (long long c = f; c <= e; ++c)
-        add(p.slot_o, p.slot_ml, (2 * c + ((c == f && a0 != c * ln.share) ? 1 : 0)) * p.unit_rows + slot_row);
-    };
-    if (p.prefix_len > 0) {
-      const int pr = b * p.GT + i, per = p.unit_rows;
-      const long long a0 = ((long long)h * p.prefix_row_blocks + pr / per) * pre_nblk;
-      add_unit(a0, a0 + pre_nblk, 1, pr % per);
     }
-    if (p.many.tiles > 0) {
-      const int tile = p.many.seq_tiles > 1 ? b * p.many.seq_tiles + i / 128 : b / p.many.seqs;
-      const int mr = p.many.seq_tiles > 1 ? i % 128 : b % p.many.seqs * p.GT + i;
-      const long long mu = (long long)h * p.many.tiles + tile;
-      const long long a0 = mu * p.many.blocks, f = a0 / p.many.share, e = (a0 + p.many.blocks - 1) / p.many.share;
-      if (f == e) add(p.many.o, p.many.ml, (2 * p.many.ctas + mu) * 128 + mr);
-      else
-        for (long long c = f; c <= e; ++c)
-          add(p.many.o, p.many.ml, (2 * c + ((c == f && a0 != c * p.many.share) ? 1 : 0)) * 128 + mr);
-    }
-    add_unit(u0, u1, 0, r);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    *reinterpret_cast<uint2*>(p.o + row * D + d) =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (d == 0) p.lse[row] = l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.69314718055994530942f;
+  };
+  // the parts [a0, a1) of the line, of a unit whose rows start at `slot_row`'s of a slot; whole: an area's row
+  auto add_unit = [&](long long a0, long long a1, int part, int slot_row) {
+    const long long f = a0 / ln.share, e = (a1 - 1) / ln.share;
+    if (f == e)
+      add(1, p.area_o[part], p.area_ml[part], [&](int) { return row; });
+    else
+      add((int)(e - f) + 1, p.slot_o, p.slot_ml, [&](int k) {
+        return (2 * (f + k) + ((k == 0 && a0 != f * ln.share) ? 1 : 0)) * p.unit_rows + slot_row;
+      });
+  };
+  if (p.prefix_len > 0) {   // few rows: computed by the same kernel
+    const int pre_nblk = (p.prefix_len + kDecBlock - 1) / kDecBlock;
+    const int pr = b * p.GT + i;
+    const long long a0 = ((long long)h * p.prefix_row_blocks + pr / p.unit_rows) * pre_nblk;
+    add_unit(a0, a0 + pre_nblk, 1, pr % p.unit_rows);
   }
+  if (p.many.tiles > 0) {
+    const DecParts pt = dec_prefix_parts(p, b, h, i);
+    add(pt.n, p.many.o, p.many.ml, [&](int k) { return pt.at(k); });
+  }
+  add_unit(u0, u1, 0, r);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) p.o[row * D + 32 * c + lane] = __float2bfloat16_rn(acc[c] * inv);
+  if (lane == 0) p.lse[row] = dec_lse(m, l);
 }
 
 }  // namespace attn

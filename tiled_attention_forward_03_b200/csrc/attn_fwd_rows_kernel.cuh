@@ -32,7 +32,7 @@
 
 #include <cuda_bf16.h>
 
-#include "attn_cache_kernel.cuh"
+#include "attn_decode_kernel.cuh"
 
 namespace attn {
 
@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  launch_dependents();
 
   // Unit `ord` of the ring, once the scheduler has written it (false: a wait gave up).
   auto take = [&](uint32_t ord, RowsUnit& w, unsigned site) -> bool {
@@ -417,8 +418,10 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
     __syncwarp();
   } else if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
+    // The whole warp: lane i loads box i of a tile (at most eight), whose page it has looked up before
+    // the wait for the stage.
     regs_decrease<Cfg::kControl>();
-    if (lane == 0) {
+    {
       const uint64_t pol_kv = l2_policy_evict_last();
       const uint64_t pol_q = l2_policy_evict_first();
       constexpr int kLoadStages = kF8 ? R : S;
@@ -427,48 +430,49 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
       Ring ring;
       uint32_t filled = 0u, fill_par = 0u;      // per stage: ever filled / parity of its last fill
       uint32_t q_par = 3u, q_filled = 0u, q_fill_par = 0u;   // per Q buffer, as in the column-split kernel
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool mine = wait_phase(bar, parity, abort_flag, kSiteRowsProducer);
+        return __all_sync(0xffffffffu, mine);
+      };
       // Block j of the unit's keys: one box, or several that lie one after the other in the tile.
       // Boxes behind the last key are not loaded (their rows are masked, and V's overwritten).
       auto load_kv = [&](bool is_k, const RowsUnit& w, int j) -> bool {
-        if (!wait_phase(&empty[ring.stage], ring.phase ^ 1u, abort_flag, kSiteRowsProducer)) return false;
+        const int rows = min(kBlockN, w.len - j * kBlockN);
+        const bool mine = lane * p.box < rows;
+        int id = w.b, row = j * kBlockN + lane * p.box;
+        if (p.table != nullptr && mine) {
+          const int pg = row / p.page;
+          id = __ldg(p.table + pg);
+          row -= pg * p.page;
+        }
+        if (!wait_all(&empty[ring.stage], ring.phase ^ 1u)) return false;
         const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
         uint64_t* bar = &full[ring.stage];
-        const int rows = min(kBlockN, w.len - j * kBlockN);
-        const int boxes = (rows + p.box - 1) / p.box;
-        uint32_t bytes = (uint32_t)(boxes * p.box) * (kF8 ? (uint32_t)D : 128u * Plan::kChunks);
+        // a page that is none lies outside the tensor: zeros, and (kF8) exponents of 1
+        const bool is_page = (unsigned)id < (unsigned)p.num_pages;
+        const int plane = is_page ? id * p.Hkv + w.h : p.num_pages * p.Hkv;
+        const unsigned boxes = __popc(__ballot_sync(0xffffffffu, mine));
+        uint32_t bytes = boxes * (uint32_t)p.box * (kF8 ? (uint32_t)D : 128u * Plan::kChunks);
         if constexpr (kF8) {
-          // exponents: one copy a box; for no page, ones (the codes are zeros)
-          uint8_t* dst = sExp + ring.stage * kBlockN;
-          for (int i = 0; i < boxes; ++i) {
-            const int pg = (j * kBlockN + i * p.box) / p.page;
-            if ((unsigned)__ldg(p.table + pg) < (unsigned)p.num_pages) {
-              bytes += (uint32_t)p.box;
-            } else {
-              for (int q = 0; q < p.box; q += 16)
-                *reinterpret_cast<uint4*>(dst + i * p.box + q) =
-                    make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
-              fence_proxy_async_smem();
-            }
+          bytes += __popc(__ballot_sync(0xffffffffu, mine && is_page)) * (uint32_t)p.box;
+          if (mine && !is_page) {
+            for (int q = 0; q < p.box; q += 16)
+              *reinterpret_cast<uint4*>(sExp + ring.stage * kBlockN + lane * p.box + q) =
+                  make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+            fence_proxy_async_smem();
           }
         }
-        mbar_arrive_expect_tx(bar, bytes);
-        for (int i = 0; i < boxes; ++i) {
-          int id = w.b, row = j * kBlockN + i * p.box;
-          if (p.table != nullptr) {
-            const int pg = row / p.page;
-            id = __ldg(p.table + pg);
-            row -= pg * p.page;
-          }
-          // a page that is none lies outside the tensor: zeros
-          const bool is_page = (unsigned)id < (unsigned)p.num_pages;
-          const int plane = is_page ? id * p.Hkv + w.h : p.num_pages * p.Hkv;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+        __syncwarp();
+        if (mine) {
           if constexpr (kF8) {
-            tma_load_3d(sRaw + ring.stage * Plan::kRawBytes + i * p.box * D, map, bar, 0, row, plane, pol_kv);
+            tma_load_3d(sRaw + ring.stage * Plan::kRawBytes + lane * p.box * D, map, bar, 0, row, plane, pol_kv);
             if (is_page)
-              rows_bulk_load(sExp + ring.stage * kBlockN + i * p.box,
+              rows_bulk_load(sExp + ring.stage * kBlockN + lane * p.box,
                              (is_k ? p.ks : p.vs) + ((long long)plane * p.page + row), (uint32_t)p.box, bar);
           } else {
-            uint8_t* dst = sKV + ring.stage * Plan::kTileBytes + i * p.box * 128;
+            uint8_t* dst = sKV + ring.stage * Plan::kTileBytes + lane * p.box * 128;
 #pragma unroll
             for (int ch = 0; ch < Plan::kChunks; ++ch)
               tma_load_3d(dst + ch * Plan::kChunkBytes, map, bar, ch * 64, row, plane, pol_kv);
@@ -481,29 +485,34 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
       };
       // Tiles in the order the MMA warp reads them: K(0), K(1), then V(g), K(g+2) for g = 0, 1, ...
       Cursor sc, pc;
-      next_unit(sc, false, false, kSiteRowsProducer);
-      next_unit(pc, true, false, kSiteRowsProducer);
+      next_unit(sc, false, true, kSiteRowsProducer);
+      next_unit(pc, true, true, kSiteRowsProducer);
       bool ok = true;
-      for (int i = 0; ok && (sc.valid || pc.valid); ++i) {
-        if (i >= 2) {
-          if (!pc.valid || !(ok = load_kv(false, pc.w, pc.j))) break;
-          if (++pc.j >= pc.w.je) next_unit(pc, true, false, kSiteRowsProducer);
-        }
-        if (sc.valid) {
-          if (sc.j == sc.w.jb) {   // the unit's Q tile
+      for (int i = 0; ok && __all_sync(0xffffffffu, sc.valid || pc.valid); ++i) {
+#pragma unroll 1
+        for (int half = 0; half < 2 && ok; ++half) {   // V(i-2), then K(i)
+          if ((half == 0 && i < 2) || !__all_sync(0xffffffffu, half ? sc.valid : pc.valid)) continue;
+          if (half && sc.j == sc.w.jb) {   // the unit's Q tile
             const int qb = (int)(sc.ord - 1u) & 1;
-            if (!(ok = wait_phase(&q_empty[qb], (q_par >> qb) & 1u, abort_flag, kSiteRowsProducer))) break;
+            if (!(ok = wait_all(&q_empty[qb], (q_par >> qb) & 1u))) break;
             q_par ^= 1u << qb;
-            mbar_arrive_expect_tx(&q_full[qb], (uint32_t)(p.q_box_rows * 128 * Plan::kChunks));
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&q_full[qb], (uint32_t)(p.q_box_rows * 128 * Plan::kChunks));
 #pragma unroll
-            for (int ch = 0; ch < Plan::kChunks; ++ch)
-              tma_load_4d(sQ + qb * Plan::kTileBytes + ch * Plan::kChunkBytes, &tmap_q, &q_full[qb], ch * 64, sc.w.i0,
-                          sc.w.h, sc.w.b0, pol_q);
+              for (int ch = 0; ch < Plan::kChunks; ++ch)
+                tma_load_4d(sQ + qb * Plan::kTileBytes + ch * Plan::kChunkBytes, &tmap_q, &q_full[qb], ch * 64,
+                            sc.w.i0, sc.w.h, sc.w.b0, pol_q);
+            }
+            __syncwarp();
             if (q_filled & (1u << qb)) q_fill_par ^= 1u << qb;
             q_filled |= 1u << qb;
           }
-          if (!(ok = load_kv(true, sc.w, sc.j))) break;
-          if (++sc.j >= sc.w.je) next_unit(sc, false, false, kSiteRowsProducer);
+          if (!(ok = load_kv(half != 0, half ? sc.w : pc.w, half ? sc.j : pc.j))) break;
+          if (half) {
+            if (++sc.j >= sc.w.je) next_unit(sc, false, true, kSiteRowsProducer);
+          } else {
+            if (++pc.j >= pc.w.je) next_unit(pc, true, true, kSiteRowsProducer);
+          }
         }
       }
       // Drain: every issued copy must have landed before the CTA may exit.
@@ -920,45 +929,79 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
 
 // Cross attention: joins the parts of every unit that was split, in key order, into O and LSE.  Block
 // (c, y): the unit at the end of CTA c's range, where its first part is in that range; a warp a row,
-// eight rows a block.
+// 32 rows a block, in turns of eight.
 template <int D>
 __global__ void __launch_bounds__(256) attn_rows_join_kernel(const RowsParams p, unsigned ctas) {
+  __shared__ int4 unit_s[2];
+  __shared__ long long place_s[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int b;
-  long long first;
-  const RowsLine ln = rows_locate(p, ctas, (long long)blockIdx.x + 1, -1, b, first);
-  const long long x = ((long long)blockIdx.x + 1) * ln.share;
-  if (x >= ln.total) return;
-  const int nblk = rows_blocks(rows_len(p, b));
-  const int unit = (int)((x - first) / nblk);
-  const long long u0 = first + (long long)unit * nblk, u1 = u0 + nblk;
-  // split here, and not before
-  if (u0 == x || u0 / ln.share != blockIdx.x) return;
-  const int r = blockIdx.y * 8 + warp;
-  const int h = unit / p.tiles;
-  RowsUnit w;
-  rows_tile(p, b, h, unit - h * p.tiles, w);
-  const long long row = rows_index(p, w.b0, w.i0, h, r);
-  if (row < 0) return;
-  const long long c0 = blockIdx.x, c1 = (u1 - 1) / ln.share;
-  auto slot = [&](long long c) { return (2 * c + ((c == c0 && u0 != c * ln.share) ? 1 : 0)) * kBlockM + r; };
-  float m = -INFINITY;
-  for (long long c = c0; c <= c1; ++c) m = fmaxf(m, p.slot_ml[slot(c)].x);
-  float l = 0.f;
-  float acc[D / 32];
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-  for (long long c = c0; c <= c1; ++c) {
-    const float2 ml = p.slot_ml[slot(c)];
-    const float a = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : ex2_approx(ml.x - m);
-    l = fmaf(ml.y, a, l);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(p.slot_o[slot(c) * D + 32 * i + lane], a, acc[i]);
+  if (warp == 0) {
+    int b;
+    long long first;
+    const long long c = blockIdx.x;
+    const RowsLine ln = rows_locate(p, ctas, c + 1, -1, b, first);
+    const long long x = (c + 1) * ln.share;
+    int n = 0;
+    RowsUnit w{};
+    long long u0 = 0;
+    if (x < ln.total) {
+      const int nblk = rows_blocks(rows_len(p, b));
+      const int unit = (int)((x - first) / nblk);
+      u0 = first + (long long)unit * nblk;
+      if (u0 != x && u0 / ln.share == c) {   // split here, and not before
+        n = (int)((u0 + nblk - 1) / ln.share - c) + 1;
+        const int h = unit / p.tiles;
+        rows_tile(p, b, h, unit - h * p.tiles, w);
+      }
+    }
+    if (lane == 0) {
+      unit_s[0] = make_int4(w.b0, w.i0, w.h, n);
+      place_s[0] = 2 * c + (u0 != c * ln.share ? 1 : 0);
+    }
   }
-  const float inv = 1.f / l;
+  __syncthreads();
+  const int4 unit = unit_s[0];
+  const long long first_slot = place_s[0], c0 = blockIdx.x;
+  const int n = unit.w;
+  if (n == 0) return;
+  wait_for_previous();
+  for (int r = blockIdx.y * 32 + warp; r < (int)blockIdx.y * 32 + 32; r += 8) {
+    const long long row = rows_index(p, unit.x, unit.y, unit.z, r);
+    if (row < 0) return;   // (rows that are none come last)
+    float m = -INFINITY, l = 0.f;
+    float acc[D / 32];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) p.o[row * D + 32 * i + lane] = __float2bfloat16_rn(acc[i] * inv);
-  if (lane == 0) p.lse[row] = ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.69314718055994530942f;
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      const bool mine = k0 + lane < n;
+      const long long place = (k0 + lane == 0 ? first_slot : 2 * (c0 + k0 + lane)) * kBlockM + r;
+      const float2 ml = mine ? p.slot_ml[place] : make_float2(-INFINITY, 0.f);
+      float mn = ml.x;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+      mn = fmaxf(m, mn);
+      const float a = dec_weight(make_float2(m, l), mn), w = dec_weight(ml, mn);
+      float sum = ml.y * w;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      m = mn;
+      l = fmaf(l, a, sum);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) acc[i] *= a;
+      const int here = min(32, n - k0);
+#pragma unroll 4
+      for (int k = 0; k < here; ++k) {
+        const float wk = __shfl_sync(0xffffffffu, w, k);
+        const long long pk = __shfl_sync(0xffffffffu, place, k);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(p.slot_o[pk * D + 32 * i + lane], wk, acc[i]);
+      }
+    }
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) p.o[row * D + 32 * i + lane] = __float2bfloat16_rn(acc[i] * inv);
+    if (lane == 0) p.lse[row] = dec_lse(m, l);
+  }
 }
 
 }  // namespace attn

@@ -85,6 +85,23 @@ int encode_rows_map(CUtensorMap* map, const void* base, int rank, const cuuint64
 // ---------------------------------------------------------------- decode schedule
 
 // Few rows over long keys: how attn_decode_kernel is launched, and its workspace.
+// Launches a kernel that may start before the one before it in the stream has ended (it waits for that
+// end itself, where it reads its results).
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 struct DecodeDeviceInfo {
   std::once_flag once;
   cudaError_t err = cudaSuccess;
@@ -102,8 +119,11 @@ struct DecPlan {
 };
 
 constexpr int kDecMinShare = 2;     // blocks of 64 keys
-constexpr int kDecShortBlocks = 2;  // sequences of at most this many blocks are never split
 constexpr int kDecCtasPerSm = 3;    // resident CTAs (the kernel's launch bounds)
+// Warps take whole units where no sequence has more than this many blocks, and there are units for
+// all CTAs (or sequences are so short that there is nothing to share).  Measured on B200: at the end of
+// the file's head comment, and E4M3 Hkv8 D128, all lengths at the limit: see the table of the notes.
+constexpr int kDecShortBlocks = 16, kDecTinyBlocks = 2;
 
 // `cap`: keys a sequence can have at most.  `shared`: a prefix of `prefix_len` keys comes first;
 // `prefix_here`: this kernel computes it too.
@@ -117,32 +137,30 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   pl.row_tiles = most_rows <= 16 ? 1 : most_rows <= 32 ? 2 : 4;
   pl.unit_rows = pl.tile_rows * pl.row_tiles;
   pl.row_blocks = (int)((GT + pl.unit_rows - 1) / pl.unit_rows);
-  long long units = (long long)B * Hkv * pl.row_blocks;
+  const long long ctas = (long long)kDecCtasPerSm * num_sms;
+  const long long units = (long long)B * Hkv * pl.row_blocks;
+  pl.whole_units = !prefix_here && pl.row_tiles == 1 &&
+                   (cap_blocks <= kDecTinyBlocks || (cap_blocks <= kDecShortBlocks && units >= ctas));
   double blocks = (double)units * (double)cap_blocks;
-  bool split = cap_blocks > kDecShortBlocks;
   if (prefix_here) {
     const long long rows = (long long)B * GT;
     pl.prefix_row_blocks = (int)((rows + pl.unit_rows - 1) / pl.unit_rows);
     blocks += (double)Hkv * pl.prefix_row_blocks * (double)pre_blocks;
-    units += (long long)Hkv * pl.prefix_row_blocks;
-    split = split || pre_blocks > kDecShortBlocks;
   }
-  pl.whole_units = split ? 0 : 1;
-  const double most = split ? blocks / kDecMinShare + 1 : (double)units;
-  const long long ctas = (long long)kDecCtasPerSm * num_sms;
+  const double most = pl.whole_units ? (double)((units + 3) / 4) : blocks / kDecMinShare + 1;
   pl.grid = (unsigned)(most < (double)ctas ? (long long)most : ctas);
   if (pl.grid < 1) pl.grid = 1;
-  pl.join = split || shared;
-  const size_t slots = split ? 2 * (size_t)pl.grid * pl.unit_rows : 0;
+  pl.join = !pl.whole_units;
+  const size_t slots = pl.whole_units ? 0 : 2 * (size_t)pl.grid * pl.unit_rows;
   pl.slot_o = slots * D * sizeof(float);
   pl.slot_ml = slots * sizeof(float2);
-  const size_t rows = shared ? ((size_t)B * Hkv * (size_t)GT + 63) / 64 * 64 : 0;
+  const size_t rows = shared && !pl.whole_units ? ((size_t)B * Hkv * (size_t)GT + 63) / 64 * 64 : 0;
   pl.area_o = rows * D * sizeof(float);
   pl.area_ml = rows * sizeof(float2);
   return pl;
 }
 
-template <int D, bool kF8, int kN>
+template <int D, bool kF8, int kN, bool kWarp>
 int launch_decode_dim(attn::DecParams& p, const DecPlan& pl, const void* k, const void* v, cudaStream_t s) {
   using Cfg = attn::DecCfg<D, kF8>;
   static DecodeDeviceInfo info[kMaxDevices];
@@ -151,7 +169,7 @@ int launch_decode_dim(attn::DecParams& p, const DecPlan& pl, const void* k, cons
   if (e == cudaSuccess && (dev < 0 || dev >= kMaxDevices)) e = cudaErrorInvalidDevice;
   if (e == cudaSuccess) {
     std::call_once(info[dev].once, [&] {
-      info[dev].err = cudaFuncSetAttribute(reinterpret_cast<const void*>(attn::attn_decode_kernel<D, kF8, kN>),
+      info[dev].err = cudaFuncSetAttribute(reinterpret_cast<const void*>(attn::attn_decode_kernel<D, kF8, kN, kWarp>),
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, attn::kDecSmem);
     });
     e = info[dev].err;
@@ -173,10 +191,21 @@ int launch_decode_dim(attn::DecParams& p, const DecPlan& pl, const void* k, cons
     std::memset(&mk, 0, sizeof(mk));
     std::memset(&mv, 0, sizeof(mv));
   }
-  attn::attn_decode_kernel<D, kF8, kN><<<pl.grid, attn::kDecThreads, attn::kDecSmem, s>>>(mk, mv, p);
-  if (pl.join)
-    attn::attn_decode_join_kernel<D>
-        <<<(unsigned)((long long)p.B * p.Hkv * p.row_blocks), attn::kDecThreads, 0, s>>>(p, pl.grid);
+  // behind the many-row kernel of a shared prefix it may start early
+  auto kern = attn::attn_decode_kernel<D, kF8, kN, kWarp>;
+  if (p.many.tiles > 0)
+    e = launch_behind(kern, dim3(pl.grid), attn::kDecThreads, attn::kDecSmem, s, mk, mv, p);
+  else
+    kern<<<pl.grid, attn::kDecThreads, attn::kDecSmem, s>>>(mk, mv, p);
+  if (e == cudaSuccess && pl.join)
+    e = launch_behind(attn::attn_decode_join_kernel<D>,
+                      dim3((unsigned)((long long)p.B * p.Hkv * p.row_blocks), (unsigned)((pl.unit_rows + 3) / 4)),
+                      attn::kDecThreads, 0, s, p, pl.grid);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    record_cuda_error("decode kernel launch", e);
+    return ATTN_ERR_CUDA;
+  }
   return launch_status("decode kernel launch");
 }
 
@@ -187,22 +216,28 @@ int launch_decode(attn::DecParams& p, const DecPlan& pl, const void* k, const vo
   p.row_blocks = pl.row_blocks;
   p.prefix_row_blocks = pl.prefix_row_blocks;
   p.whole_units = pl.whole_units;
-  p.min_share = pl.whole_units ? 1 : kDecMinShare;
+  p.min_share = kDecMinShare;
   p.unit_rows = pl.unit_rows;
   char* w = static_cast<char*>(workspace);
   p.slot_o = reinterpret_cast<float*>(w);
   p.slot_ml = reinterpret_cast<float2*>(w + pl.slot_o);
   w += pl.slot_o + pl.slot_ml;
   for (int i = 0; i < 2; ++i) {
-    p.area_o[i] = shared ? reinterpret_cast<float*>(w) : nullptr;
-    p.area_ml[i] = shared ? reinterpret_cast<float2*>(w + pl.area_o) : nullptr;
+    p.area_o[i] = shared && pl.join ? reinterpret_cast<float*>(w) : nullptr;
+    p.area_ml[i] = shared && pl.join ? reinterpret_cast<float2*>(w + pl.area_o) : nullptr;
     w += pl.area_o + pl.area_ml;
   }
+  auto pick = [&](auto dim, auto tiles, auto warps) {
+    constexpr int D_ = decltype(dim)::value, N_ = decltype(tiles)::value;
+    constexpr bool W_ = decltype(warps)::value;
+    return p.ks ? launch_decode_dim<D_, true, N_, W_>(p, pl, k, v, s) : launch_decode_dim<D_, false, N_, W_>(p, pl, k, v, s);
+  };
   auto go = [&](auto dim) {
-    constexpr int D_ = decltype(dim)::value;
     if (pl.tile_rows == 8)
-      return p.ks ? launch_decode_dim<D_, true, 1>(p, pl, k, v, s) : launch_decode_dim<D_, false, 1>(p, pl, k, v, s);
-    return p.ks ? launch_decode_dim<D_, true, 2>(p, pl, k, v, s) : launch_decode_dim<D_, false, 2>(p, pl, k, v, s);
+      return pl.whole_units ? pick(dim, std::integral_constant<int, 1>(), std::true_type())
+                            : pick(dim, std::integral_constant<int, 1>(), std::false_type());
+    return pl.whole_units ? pick(dim, std::integral_constant<int, 2>(), std::true_type())
+                          : pick(dim, std::integral_constant<int, 2>(), std::false_type());
   };
   switch (D) {
     case 32: return go(std::integral_constant<int, 32>());
@@ -319,7 +354,7 @@ void launch_rows_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   else
     attn::attn_fwd_rows_sm100<D, false>
         <<<grid, attn::RowsCfg<false>::kThreads, attn::RowsSmem<D, false>::kAlloc, s>>>(mq, mk, mv, mo, p);
-  if (join) attn::attn_rows_join_kernel<D><<<dim3(grid - 1, attn::kBlockM / 8), 256, 0, s>>>(p, grid);
+  if (join) launch_behind(attn::attn_rows_join_kernel<D>, dim3(grid - 1, attn::kBlockM / 32), 256, 0, s, p, grid);
 }
 
 constexpr int kRowsMinShare = 2;   // blocks of 128 keys
