@@ -14,6 +14,7 @@ cannot be loaded, importing this package raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -804,13 +805,20 @@ def forward_rope(q, k, v, cos_t, sin_t, causal: bool = False, scale: float | Non
 
 def _expect(t, name, dtype, shape, device):
     """As _check, and the tensor must be on `device`."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _check(t, name, dtype, shape)
+    raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _raw_stream(stream, device) -> int:
+    """The cudaStream_t of `stream`, or of torch's current stream on `device`."""
     import torch
 
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.device != device or t.shape != shape \
-            or not t.is_contiguous():
-        _check(t, name, dtype, shape)
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _scratch(nbytes: int, device, stream):
@@ -824,13 +832,32 @@ def _scratch(nbytes: int, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-def _on(device):
-    """Makes `device` current for the calls inside, where it is not already."""
-    import contextlib
+class _On:
+    """Makes a device current inside, where it is not already."""
 
-    import torch
+    __slots__ = ("index", "before")
 
-    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        import torch
+
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        import torch
+
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(what: str, device_index: int, *sizes) -> int:
+    """lib.<what>(*sizes) for the current device (device_index), a function of the sizes alone; -1 where refused."""
+    return getattr(lib, what)(*sizes)
 
 
 def _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, device):
@@ -846,14 +873,15 @@ def _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, device):
         raise TypeError(f"k_cache must be torch.bfloat16 or torch.float8_e4m3fn, got {k_cache.dtype}")
     if f8 != (k_scale is not None) or f8 != (v_scale is not None):
         raise ValueError("k_scale and v_scale come with a float8_e4m3fn cache, and only with one")
-    if k_cache.device.type != "cuda":
+    if not k_cache.is_cuda:
         raise ValueError("k_cache must be a CUDA tensor")
-    _expect(k_cache, "k_cache", k_cache.dtype, (num_pages, Hkv, page, D), device)
-    _expect(v_cache, "v_cache", k_cache.dtype, (num_pages, Hkv, page, D), device)
+    shape = k_cache.shape
+    _expect(k_cache, "k_cache", k_cache.dtype, shape, device)
+    _expect(v_cache, "v_cache", k_cache.dtype, shape, device)
     if f8:
-        _expect(k_scale, "k_scale", torch.float8_e8m0fnu, (num_pages, Hkv, page), device)
-        _expect(v_scale, "v_scale", torch.float8_e8m0fnu, (num_pages, Hkv, page), device)
-    _expect(block_table, "block_table", torch.int32, (B, max_pages), device)
+        _expect(k_scale, "k_scale", torch.float8_e8m0fnu, shape[:3], device)
+        _expect(v_scale, "v_scale", torch.float8_e8m0fnu, shape[:3], device)
+    _expect(block_table, "block_table", torch.int32, block_table.shape, device)
     _expect(lens, "lens", torch.int32, (B,), device)
     return B, Hkv, D, num_pages, page, max_pages
 
@@ -882,11 +910,11 @@ def cache_append(k, v, k_cache, v_cache, block_table, lens, new_lens=None, k_sca
     _expect(v, "v", torch.bfloat16, (B, Hkv, T, D), dev)
     if new_lens is not None:
         _expect(new_lens, "new_lens", torch.int32, (B,), dev)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with _on(dev):
+    s = _raw_stream(stream, dev)
+    with _On(dev):
         st = lib.attn_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
                                    _ptr(v_scale), block_table.data_ptr(), lens.data_ptr(), _ptr(new_lens), B, Hkv, T,
-                                   D, num_pages, page, max_pages, s.cuda_stream)
+                                   D, num_pages, page, max_pages, s)
     if st != ATTN_OK:
         raise AttnError(st, "attn_cache_append")
 
@@ -900,16 +928,20 @@ def cache_read(k_cache, v_cache, block_table, lens, N: int, k_scale=None, v_scal
 
     dev = k_cache.device
     B, Hkv, D, num_pages, page, max_pages = _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, dev)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    s = _raw_stream(stream, dev)
     shape = (B, Hkv, N, D)
-    k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if k_out is None else k_out
-    v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if v_out is None else v_out
-    _expect(k_out, "k_out", torch.bfloat16, shape, dev)
-    _expect(v_out, "v_out", torch.bfloat16, shape, dev)
-    with _on(dev):
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _expect(k_out, "k_out", torch.bfloat16, shape, dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _expect(v_out, "v_out", torch.bfloat16, shape, dev)
+    with _On(dev):
         st = lib.attn_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
                                  block_table.data_ptr(), lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, Hkv,
-                                 N, D, num_pages, page, max_pages, s.cuda_stream)
+                                 N, D, num_pages, page, max_pages, s)
     if st != ATTN_OK:
         raise AttnError(st, "attn_cache_read")
     return k_out, v_out
@@ -920,13 +952,17 @@ def _decode_outputs(q, Hkv, B, D, out, lse):
 
     if q.dim() != 4:
         raise ValueError("q must be 4-D [B, Hq, T, D]")
-    Hq, T = q.shape[1], q.shape[2]
+    _, Hq, T, _ = shape = q.shape
     dev = q.device
     _expect(q, "q", torch.bfloat16, (B, Hq, T, D), dev)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev) if lse is None else lse
-    _expect(out, "out", torch.bfloat16, (B, Hq, T, D), dev)
-    _expect(lse, "lse", torch.float32, (B, Hq, T), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _expect(out, "out", torch.bfloat16, shape, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+    else:
+        _expect(lse, "lse", torch.float32, (B, Hq, T), dev)
     return Hq, T, out, lse
 
 
@@ -945,13 +981,13 @@ def forward_decode(q, k_cache, v_cache, block_table, lens, k_scale=None, v_scale
     Hq, T, out, lse = _decode_outputs(q, Hkv, B, D, out, lse)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with _on(dev):
-        nbytes = lib.attn_fwd_decode_workspace_bytes(B, Hq, Hkv, T, D, page, max_pages)
+    s = _raw_stream(stream, dev)
+    with _On(dev):
+        nbytes = _workspace_bytes("attn_fwd_decode_workspace_bytes", dev.index, B, Hq, Hkv, T, D, page, max_pages)
         ws = _scratch(nbytes, dev, stream) if nbytes > 0 else None
         st = lib.attn_fwd_decode(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
                                  block_table.data_ptr(), lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
-                                 T, D, num_pages, page, max_pages, scale, _ptr(ws), max(nbytes, 0), s.cuda_stream)
+                                 T, D, num_pages, page, max_pages, scale, _ptr(ws), max(nbytes, 0), s)
     if st != ATTN_OK:
         raise AttnError(st, "attn_fwd_decode")
     return out, lse
@@ -974,14 +1010,15 @@ def forward_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len: int, bl
         raise ValueError(f"prefix_len {prefix_len} does not fit prefix_table's {prefix_table.numel()} pages of {page}")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with _on(dev):
-        nbytes = lib.attn_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, T, D, page, max_pages, prefix_len)
+    s = _raw_stream(stream, dev)
+    with _On(dev):
+        nbytes = _workspace_bytes("attn_fwd_shared_prefix_workspace_bytes", dev.index, B, Hq, Hkv, T, D, page, max_pages,
+                                  prefix_len)
         ws = _scratch(nbytes, dev, stream) if nbytes > 0 else None
         st = lib.attn_fwd_shared_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
                                         _ptr(v_scale), prefix_table.data_ptr(), prefix_len, block_table.data_ptr(),
                                         lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, T, D, num_pages,
-                                        page, max_pages, scale, _ptr(ws), max(nbytes, 0), s.cuda_stream)
+                                        page, max_pages, scale, _ptr(ws), max(nbytes, 0), s)
     if st != ATTN_OK:
         raise AttnError(st, "attn_fwd_shared_prefix")
     return out, lse
@@ -1011,19 +1048,23 @@ def forward_cross(q, k, v, k_lens=None, scale: float | None = None, out=None, ls
     import torch
 
     B, Hq, Hkv, Nq, Nk, D, dev = _cross_checks(q, k, v, k_lens)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev) if lse is None else lse
-    _expect(out, "out", torch.bfloat16, (B, Hq, Nq, D), dev)
-    _expect(lse, "lse", torch.float32, (B, Hq, Nq), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _expect(out, "out", torch.bfloat16, (B, Hq, Nq, D), dev)
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+    else:
+        _expect(lse, "lse", torch.float32, (B, Hq, Nq), dev)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with _on(dev):
-        nbytes = lib.attn_fwd_cross_workspace_bytes(B, Hq, Hkv, Nq, Nk, D)
+    s = _raw_stream(stream, dev)
+    with _On(dev):
+        nbytes = _workspace_bytes("attn_fwd_cross_workspace_bytes", dev.index, B, Hq, Hkv, Nq, Nk, D)
         ws = _scratch(nbytes, dev, stream) if nbytes > 0 else None
         st = lib.attn_fwd_cross(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_lens), out.data_ptr(),
                                 lse.data_ptr(), B, Hq, Hkv, Nq, Nk, D, scale, _ptr(ws), max(nbytes, 0),
-                                s.cuda_stream)
+                                s)
     if st != ATTN_OK:
         raise AttnError(st, "attn_fwd_cross")
     return out, lse
@@ -1049,13 +1090,13 @@ def backward_cross(q, k, v, o, lse, dout, k_lens=None, scale: float | None = Non
     _expect(dv, "dv", torch.bfloat16, k_shape, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    with _on(dev):
-        nbytes = lib.attn_bwd_cross_workspace_bytes(B, Hq, Hkv, Nq)
+    s = _raw_stream(stream, dev)
+    with _On(dev):
+        nbytes = _workspace_bytes("attn_bwd_cross_workspace_bytes", dev.index, B, Hq, Hkv, Nq)
         ws = _scratch(nbytes, dev, stream) if nbytes > 0 else None
         st = lib.attn_bwd_cross(q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(k_lens), o.data_ptr(), lse.data_ptr(),
                                 dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Nq, Nk, D,
-                                scale, _ptr(ws), max(nbytes, 0), s.cuda_stream)
+                                scale, _ptr(ws), max(nbytes, 0), s)
     if st != ATTN_OK:
         raise AttnError(st, "attn_bwd_cross")
     return dq, dk, dv

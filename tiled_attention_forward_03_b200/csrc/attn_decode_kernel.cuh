@@ -88,7 +88,7 @@ struct DecParams {
   // shared prefix handled here (prefix_len > 0): an extra first sequence with all rows of the batch
   const int* prefix_table;
   int prefix_len, prefix_row_blocks;
-  int whole_units;           // 1: the warp form: warps take whole units
+  int whole_units;           // 1: units are not split (each stands in the line as one block)
   int min_share;             // blocks a CTA takes at least
   float c;                   // scale * log2(e)
   __nv_bfloat16* o;          // [B][Hkv][GT][D]
@@ -114,8 +114,8 @@ __device__ __forceinline__ int dec_len(const DecParams& p, int b) {
   return (int)max(0LL, min(n, p.cap));
 }
 
-__device__ __forceinline__ int dec_blocks(int len) {
-  return max(1, (int)(((long long)len + kDecBlock - 1) / kDecBlock));
+__device__ __forceinline__ int dec_blocks(const DecParams& p, int len) {
+  return p.whole_units ? 1 : max(1, (int)(((long long)len + kDecBlock - 1) / kDecBlock));
 }
 
 // Weight of a result with running maximum ml.x and sum ml.y against maximum m (none: 0; NaN stays).
@@ -126,6 +126,14 @@ __device__ __forceinline__ float dec_weight(float2 ml, float m) {
 // LSE of a row from its maximum (base 2) and sum.
 __device__ __forceinline__ float dec_lse(float m, float l) {
   return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.69314718055994530942f;
+}
+
+// 1-D bulk copy global -> shared (16-byte aligned addresses, size a multiple of 16).
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // Programmatic dependent launch: the next kernel of the stream may start (it waits for this one's
@@ -173,7 +181,7 @@ __device__ __forceinline__ DecLine dec_locate(const DecParams& p, unsigned ctas,
   const int per = (p.B + kDecThreads - 1) / kDecThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += dec_blocks(dec_len(p, b));
+  for (int b = b0; b < b1; ++b) mine += dec_blocks(p, dec_len(p, b));
   mine *= per_seq;
   long long incl = mine;
 #pragma unroll
@@ -198,7 +206,7 @@ __device__ __forceinline__ DecLine dec_locate(const DecParams& p, unsigned ctas,
   if (find_seq >= 0 ? (find_seq >= b0 && find_seq < b1) : (x >= at && x < at + mine)) {
     int b = b0;
     for (; b < b1; ++b) {
-      const long long n = per_seq * dec_blocks(dec_len(p, b));
+      const long long n = per_seq * dec_blocks(p, dec_len(p, b));
       if (find_seq >= 0 ? b == find_seq : x < at + n) break;
       at += n;
     }
@@ -273,7 +281,10 @@ struct DecCfg {
   static constexpr int kJoinBytes = 4 * 16 * kRowStride * 4;
   static_assert(kJoinBytes <= kDecStages * kDecStageBytes, "the join takes the rings' place");
 };
-constexpr int kDecSmem = kDecStages * kDecStageBytes + 1024;   // slack for 1024-byte alignment
+// E4M3: a stage's exponents, K's then V's (32 keys at most), behind all the stages; slack for
+// 1024-byte alignment
+constexpr int kDecExpBytes = 64;
+constexpr int kDecSmem = kDecStages * (kDecStageBytes + kDecExpBytes) + 1024;
 
 // Byte `b` of row `r` in a tile of 128-byte rows as TMA swizzles it.
 __device__ __forceinline__ uint32_t dec_sw(uint32_t r, uint32_t b) { return r * 128 + (b ^ ((r & 7) << 4)); }
@@ -302,6 +313,11 @@ __device__ __forceinline__ void lds16(uint32_t* w, uint32_t addr) {
 }
 __device__ __forceinline__ void lds8(uint32_t* w, uint32_t addr) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+}
+__device__ __forceinline__ int lds1(uint32_t addr) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
+  return (int)r;
 }
 __device__ __forceinline__ void lds4(uint32_t* w, uint32_t addr) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
@@ -383,6 +399,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
   const int kg = warp / row_tiles, rt = warp - kg * row_tiles, ways = 4 / row_tiles;
   const int stages = kDecStages / ways;                 // of this way's ring
   const uint32_t ring = smem_u32(smem) + kg * stages * kDecStageBytes;
+  uint8_t* const exps = smem + kDecStages * kDecStageBytes + kg * stages * kDecExpBytes;
   uint64_t* ring_full = full + kg * stages;
   uint64_t* ring_empty = empty + kg * stages;
   if (threadIdx.x == 0) {
@@ -422,7 +439,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
     if constexpr (kWarp) seq = (int)(x / p.Hkv);
     const bool prefix = !kWarp && seq < 0;
     const int len = prefix ? p.prefix_len : dec_len(p, seq);
-    const int nblk = kWarp ? 1 : prefix ? (len + kDecBlock - 1) / kDecBlock : dec_blocks(len);
+    const int nblk = kWarp ? 1 : prefix ? (len + kDecBlock - 1) / kDecBlock : dec_blocks(p, len);
     const int row_blocks = prefix ? p.prefix_row_blocks : p.row_blocks;
     const int rows = prefix ? p.B * p.GT : p.GT;
     const int unit = kWarp ? 0 : (int)((x - first) / nblk);
@@ -431,8 +448,8 @@ __global__ void __launch_bounds__(kDecThreads, 3)
     const int h = kWarp ? (int)(x - (long long)seq * p.Hkv) : unit / row_blocks, rb = kWarp ? 0 : unit - h * row_blocks;
     const int* table = prefix ? p.prefix_table : (p.table ? p.table + (size_t)seq * p.max_pages : nullptr);
     const int i0 = (rb * row_tiles + rt) * kTile;   // first row of this warp's tile
-    const int key_begin = blk0 * kDecBlock;
-    const int key_end = kWarp ? len : (int)min((long long)len, (long long)blk1 * kDecBlock);
+    const int key_begin = blk0 * kDecBlock;   // (of a unit that is not split: 0)
+    const int key_end = (kWarp || p.whole_units) ? len : (int)min((long long)len, (long long)blk1 * kDecBlock);
 
     // row i of the unit -> its index in q, o, lse
     auto row_index = [&](int i) -> long long {
@@ -474,13 +491,35 @@ __global__ void __launch_bounds__(kDecThreads, 3)
       if (i_count >= (uint32_t)stages &&
           !wait_phase(&ring_empty[i_stage], i_phase ^ 1u, abort_flag, kSiteDecodeEmpty))
         return false;
-      int boxes = 0;
-#pragma unroll
-      for (int i = 0; i < kMaxBoxes; ++i) boxes += iplane[i] >= 0 ? 1 : 0;
-      mbar_arrive_expect_tx(&ring_full[i_stage], (uint32_t)(2 * Cfg::kChunks * boxes * p.box * 128));
+      uint32_t bytes = 0u;
 #pragma unroll
       for (int i = 0; i < kMaxBoxes; ++i) {
         if (iplane[i] < 0) continue;
+        bytes += (uint32_t)(2 * Cfg::kChunks * p.box * 128);
+        if constexpr (kF8) {
+          if (iplane[i] != no_plane) {
+            bytes += 2u * (uint32_t)p.box;
+          } else {   // zero codes: any exponent does, but those of the stage's last use may be NaN
+            for (int q = 0; q < p.box; q += 16) {
+              uint4* dst = reinterpret_cast<uint4*>(exps + i_stage * kDecExpBytes + i * p.box + q);
+              dst[0] = dst[2] = make_uint4(0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+      }
+      mbar_arrive_expect_tx(&ring_full[i_stage], bytes);
+#pragma unroll
+      for (int i = 0; i < kMaxBoxes; ++i) {
+        if (iplane[i] < 0) continue;
+        if constexpr (kF8) {
+          if (iplane[i] != no_plane) {
+            const long long at = (long long)iplane[i] * p.page + iw[i].row;
+            uint8_t* dst = exps + i_stage * kDecExpBytes + i * p.box;
+            bulk_load(dst, p.ks + at, (uint32_t)p.box, &ring_full[i_stage]);
+            bulk_load(dst + 32, p.vs + at, (uint32_t)p.box, &ring_full[i_stage]);
+          }
+        }
 #pragma unroll
         for (int c = 0; c < Cfg::kChunks; ++c) {
           uint8_t* dst = smem + (kg * stages + i_stage) * kDecStageBytes + c * Cfg::kChunkBytes + i * p.box * 128;
@@ -557,33 +596,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
       }
     }
     if (p.causal && !prefix) lim_min = len - p.T + 1;
-    // E4M3: exponent bytes of keys g and g + 8 of each group of the next step (for no page: 1, of
-    // zero rows), and the largest V exponent so far (0: none yet)
-    uint32_t sk[G][2], sv[G][2];
-    int top_e = 0;
-    Walk sw[G];
-#pragma unroll
-    for (int gr = 0; gr < G; ++gr) sw[gr] = walk_at(k_first + 16 * gr);
-    auto load_scales = [&](int n) {   // of step n, where sw stands; moves sw on
-      if constexpr (kF8) {
-#pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) sk[gr][j] = sv[gr][j] = 127u;
-          const int plane = (n < steps && k_first + n * stride + 16 * gr < key_end) ? plane_of(sw[gr].pg) : no_plane;
-          if (plane != no_plane) {
-            const long long e = (long long)plane * p.page + sw[gr].row + g;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              sk[gr][j] = __ldg(p.ks + e + 8 * j);
-              sv[gr][j] = __ldg(p.vs + e + 8 * j);
-            }
-          }
-          walk_on(sw[gr], stride);
-        }
-      }
-    };
-    load_scales(0);
+    int top_e = 0;   // E4M3: the largest V exponent so far (0: none yet)
 
     for (int n = 0; n < steps && ok; ++n) {
       const int k = k_first + n * stride;
@@ -619,18 +632,23 @@ __global__ void __launch_bounds__(kDecThreads, 3)
         int ev[G][2];   // E4M3: V exponents of keys g, g + 8
 #pragma unroll
         for (int gr = 0; gr < G; ++gr) {
+          float kf[2] = {1.f, 1.f};
+          if constexpr (kF8) {
+            // (a marked row has codes 0: 0 * infinity is the NaN it stands for)
+            const uint32_t at = smem_u32(exps) + stage * kDecExpBytes + 16 * gr + g;
+            kf[0] = pow2_field(lds1(at));
+            kf[1] = pow2_field(lds1(at + 8));
+            ev[gr][0] = lds1(at + 32);
+            ev[gr][1] = lds1(at + 40);
+          }
 #pragma unroll
           for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               s[gr][nt][e] *= cf[nt][e & 1];
-              // (a marked row has codes 0: 0 * infinity is the NaN it stands for)
-              if constexpr (kF8) s[gr][nt][e] *= pow2_field((int)sk[gr][e >> 1]);
+              if constexpr (kF8) s[gr][nt][e] *= kf[e >> 1];
             }
-          ev[gr][0] = (int)sv[gr][0];
-          ev[gr][1] = (int)sv[gr][1];
         }
-        load_scales(n + 1);
         const bool tail = k + Cfg::kStep > key_end;
         if (tail || k + Cfg::kStep > lim_min) {
 #pragma unroll
@@ -983,7 +1001,7 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
   int seq;
   long long first;
   const DecLine ln = dec_locate(p, ctas, 0, b, scratch, seq, first);
-  const int nblk = dec_blocks(dec_len(p, b));
+  const int nblk = dec_blocks(p, dec_len(p, b));
   const long long u0 = first + (long long)hr * nblk, u1 = u0 + nblk;
   const bool shared = p.area_o[0] != nullptr;
   if (!shared && u0 / ln.share == (u1 - 1) / ln.share) return;   // written by the one CTA that had it

@@ -208,14 +208,6 @@ ATTN_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int 
       : "memory");
 }
 
-// 1-D bulk copy global -> shared (16-byte aligned addresses, size a multiple of 16).
-ATTN_DEV void rows_bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // 2^x for a pair on the FMA pipe, as exp2_poly2 but with a degree-5 polynomial (csrc/fit_exp2_poly.py
 // 5: largest relative error 2.4e-7 in fp32).  The degree-3 one is 7e-5 low at the row's maximum,
 // which shows in the LSE of rows with few keys.
@@ -469,7 +461,7 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
           if constexpr (kF8) {
             tma_load_3d(sRaw + ring.stage * Plan::kRawBytes + lane * p.box * D, map, bar, 0, row, plane, pol_kv);
             if (is_page)
-              rows_bulk_load(sExp + ring.stage * kBlockN + lane * p.box,
+              bulk_load(sExp + ring.stage * kBlockN + lane * p.box,
                              (is_k ? p.ks : p.vs) + ((long long)plane * p.page + row), (uint32_t)p.box, bar);
           } else {
             uint8_t* dst = sKV + ring.stage * Plan::kTileBytes + lane * p.box * 128;

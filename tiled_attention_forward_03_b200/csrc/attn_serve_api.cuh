@@ -110,7 +110,8 @@ struct DecodeDeviceInfo {
 struct DecPlan {
   int tile_rows;             // rows of a warp: 8 or 16
   int row_tiles, unit_rows, row_blocks, prefix_row_blocks = 0;
-  int whole_units;
+  int whole_units;           // units are not split
+  bool warps;                // and warps take them
   unsigned grid;
   bool join;                 // the second kernel is needed
   size_t slot_o, slot_ml;    // bytes
@@ -124,6 +125,8 @@ constexpr int kDecCtasPerSm = 3;    // resident CTAs (the kernel's launch bounds
 // all CTAs (or sequences are so short that there is nothing to share).  Measured on B200: at the end of
 // the file's head comment, and E4M3 Hkv8 D128, all lengths at the limit: see the table of the notes.
 constexpr int kDecShortBlocks = 16, kDecTinyBlocks = 2;
+// Else a CTA takes whole units where no sequence has more than this many blocks: a launch less.
+constexpr int kDecWholeBlocks = 8;
 
 // `cap`: keys a sequence can have at most.  `shared`: a prefix of `prefix_len` keys comes first;
 // `prefix_here`: this kernel computes it too.
@@ -139,15 +142,16 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   pl.row_blocks = (int)((GT + pl.unit_rows - 1) / pl.unit_rows);
   const long long ctas = (long long)kDecCtasPerSm * num_sms;
   const long long units = (long long)B * Hkv * pl.row_blocks;
-  pl.whole_units = !prefix_here && pl.row_tiles == 1 &&
-                   (cap_blocks <= kDecTinyBlocks || (cap_blocks <= kDecShortBlocks && units >= ctas));
+  pl.warps = !prefix_here && pl.row_tiles == 1 &&
+             (cap_blocks <= kDecTinyBlocks || (cap_blocks <= kDecShortBlocks && units >= ctas));
+  pl.whole_units = pl.warps || (!shared && cap_blocks <= kDecWholeBlocks) ? 1 : 0;
   double blocks = (double)units * (double)cap_blocks;
   if (prefix_here) {
     const long long rows = (long long)B * GT;
     pl.prefix_row_blocks = (int)((rows + pl.unit_rows - 1) / pl.unit_rows);
     blocks += (double)Hkv * pl.prefix_row_blocks * (double)pre_blocks;
   }
-  const double most = pl.whole_units ? (double)((units + 3) / 4) : blocks / kDecMinShare + 1;
+  const double most = pl.warps ? (double)((units + 3) / 4) : pl.whole_units ? (double)units : blocks / kDecMinShare + 1;
   pl.grid = (unsigned)(most < (double)ctas ? (long long)most : ctas);
   if (pl.grid < 1) pl.grid = 1;
   pl.join = !pl.whole_units;
@@ -216,7 +220,7 @@ int launch_decode(attn::DecParams& p, const DecPlan& pl, const void* k, const vo
   p.row_blocks = pl.row_blocks;
   p.prefix_row_blocks = pl.prefix_row_blocks;
   p.whole_units = pl.whole_units;
-  p.min_share = kDecMinShare;
+  p.min_share = pl.whole_units ? 1 : kDecMinShare;
   p.unit_rows = pl.unit_rows;
   char* w = static_cast<char*>(workspace);
   p.slot_o = reinterpret_cast<float*>(w);
@@ -234,9 +238,9 @@ int launch_decode(attn::DecParams& p, const DecPlan& pl, const void* k, const vo
   };
   auto go = [&](auto dim) {
     if (pl.tile_rows == 8)
-      return pl.whole_units ? pick(dim, std::integral_constant<int, 1>(), std::true_type())
+      return pl.warps ? pick(dim, std::integral_constant<int, 1>(), std::true_type())
                             : pick(dim, std::integral_constant<int, 1>(), std::false_type());
-    return pl.whole_units ? pick(dim, std::integral_constant<int, 2>(), std::true_type())
+    return pl.warps ? pick(dim, std::integral_constant<int, 2>(), std::true_type())
                           : pick(dim, std::integral_constant<int, 2>(), std::false_type());
   };
   switch (D) {
