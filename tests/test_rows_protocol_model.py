@@ -14,11 +14,12 @@ from test_colsplit_protocol_model import Barrier, Deadlock
 QUEUE = 4
 
 
-def run_cta(units, rng, f8=False, prefix=False, stages=4, raw_stages=3, queue=QUEUE, mistake=None):
+def run_cta(units, rng, f8=False, prefix=False, stages=4, raw_stages=5, queue=QUEUE, mistake=None):
     """units: (blocks, to_slot) in order."""
     seq = [(u, w, j) for u, w in enumerate(units) for j in range(w[0])]
     bars = {}
-    n_take = 2 + 1 + 1 + (0 if prefix else 1) + (1 if f8 else 0)   # (each softmax warpgroup and the converters as one)
+    bufs = 1 if f8 else 2   # Q buffers
+    n_take = 2 + 1 + 1 + (0 if prefix else 1) + (2 if f8 else 0)   # (each warpgroup as one)
     for i in range(queue):
         bars[f"u_full{i}"], bars[f"u_empty{i}"] = Barrier(f"u_full{i}", 1), Barrier(f"u_empty{i}", n_take)
     for i in range(2):
@@ -112,7 +113,7 @@ def run_cta(units, rng, f8=False, prefix=False, stages=4, raw_stages=3, queue=QU
 
         def load_k(c):
             if c.j == 0:
-                qb = c.u & 1
+                qb = c.u % bufs
                 yield from W(f"q_empty{qb}", q_par[qb], q_uses[qb] - 1)
                 q_par[qb] ^= 1
                 q_uses[qb] += 1
@@ -122,23 +123,28 @@ def run_cta(units, rng, f8=False, prefix=False, stages=4, raw_stages=3, queue=QU
 
         yield from ordered(Cursor(first_gives), Cursor(True), load_k, lambda c: load("V", c))
 
-    def converter():
+    def converter(group):
+        """Warpgroup `group` of the converters: the tiles of its parity."""
         r, raw = Ring(stages), Ring(raw_stages)
+        n = [0]
 
         def convert(kind, c):
-            st = raw.stage
-            yield from W(f"raw_full{st}", raw.phase, raw.uses[st])
-            tile = state["raw"][st]
-            assert tile == (kind, c.u, c.j), f"converters expect {(kind, c.u, c.j)}, the raw stage holds {tile}"
-            bars[f"raw_empty{st}"].arrive()
+            mine = n[0] & 1 == group
+            n[0] += 1
+            if mine:
+                st, kv = raw.stage, r.stage
+                yield from W(f"raw_full{st}", raw.phase, raw.uses[st])
+                if mistake != "converters do not wait":
+                    yield from W(f"kv_empty{kv}", r.phase ^ 1, r.uses[kv] - 1)
+                tile = state["raw"][st]
+                assert tile == (kind, c.u, c.j), f"converters expect {(kind, c.u, c.j)}, the raw stage holds {tile}"
+                assert state["busy"][kv] == 0, "converted over a tile still being read"
+                yield ("step",)
+                assert state["raw"][st] == tile, "raw stage refilled while being read"
+                state["stage"][kv] = tile
+                bars[f"raw_empty{st}"].arrive()
+                bars[f"kv_full{kv}"].arrive()
             raw.step()
-            yield ("step",)
-            kv = r.stage
-            if mistake != "converters do not wait":
-                yield from W(f"kv_empty{kv}", r.phase ^ 1, r.uses[kv] - 1)
-            assert state["busy"][kv] == 0, "converted over a tile still being read"
-            state["stage"][kv] = tile
-            bars[f"kv_full{kv}"].arrive()
             r.step()
 
         yield from ordered(Cursor(first_gives), Cursor(True), lambda c: convert("K", c), lambda c: convert("V", c))
@@ -174,7 +180,7 @@ def run_cta(units, rng, f8=False, prefix=False, stages=4, raw_stages=3, queue=QU
                     tensor_q.append(("commit", "o_full"))
                 yield from pc.advance()
             if sc.valid:
-                qb = sc.u & 1
+                qb = sc.u % bufs
                 if sc.j == 0:
                     yield from W(f"q_full{qb}", q_par[qb], q_uses[qb])
                     q_par[qb] ^= 1
@@ -252,7 +258,7 @@ def run_cta(units, rng, f8=False, prefix=False, stages=4, raw_stages=3, queue=QU
     if not prefix:
         agents["store"] = store()
     if f8:
-        agents["converter"] = converter()
+        agents["converter0"], agents["converter1"] = converter(0), converter(1)
     pending, done = {a: None for a in agents}, set()
 
     def tensor():

@@ -51,9 +51,16 @@ __device__ __forceinline__ long long cache_row(const CacheView& c, int b, int h,
   if (pos < 0 || pos > 0x7fffffffLL) return -1;
   const uint32_t pg = fast_div((uint32_t)pos, c.div_page);
   if (pg >= (uint32_t)c.max_pages) return -1;
-  const int id = c.table[(size_t)b * c.max_pages + pg];
+  const int id = __ldg(c.table + (size_t)b * c.max_pages + pg);
   if ((unsigned)id >= (unsigned)c.num_pages) return -1;
   return ((long long)id * c.Hkv + h) * c.page + ((uint32_t)pos - pg * (uint32_t)c.page);
+}
+
+// Larger of each pair of unsigned 16-bit halves.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // E8M0 byte of a row from the largest magnitude bits (bf16 without the sign) of its elements.
@@ -64,66 +71,87 @@ __device__ __forceinline__ int e8_of_amax(uint32_t bits) {
 }
 
 // Appends rows t < new_lens[b] of k, v [B][Hkv][T][D] at positions lens[b] + t.  A group of G lanes
-// takes one row of K and the same row of V (16 bytes a lane, both loads issued before any use); the
-// row's largest magnitude is a shuffle over the group.  Measured on B200: the 57 MB of a quantised
-// prompt batch (B4 H8 T4096 ragged, D128) at the rate given in the table of the design notes; a
-// single token a sequence is launch-bound.
-template <int D, bool kF8>
+// takes kRows rows of K and of V (16 bytes a lane and row, all loads issued before any use); a row's
+// largest magnitude is a shuffle over the group.  kRows = 4 where the rows fill the GPU several times
+// over: with one the 57 MB of a quantised prompt batch (B4 Hkv8 T<=4096 D128) took 25 us, seven waves
+// of three dependent reads each.
+template <int D, bool kF8, int kRows>
 __global__ void __launch_bounds__(256) attn_cache_append_kernel(const __nv_bfloat16* __restrict__ k,
                                                                 const __nv_bfloat16* __restrict__ v, CacheView c,
                                                                 const int* __restrict__ new_lens, int T,
                                                                 FastDiv div_t, FastDiv div_h, uint32_t rows) {
   constexpr int kLanes = D / 8;                                       // lanes with data
-  constexpr int G = kLanes <= 4 ? 4 : kLanes <= 8 ? 8 : kLanes <= 16 ? 16 : 32;
-  const uint32_t row = (uint32_t)(((unsigned long long)blockIdx.x * blockDim.x + threadIdx.x) / G);
+  constexpr int G = kLanes <= 4 ? 4 : kLanes <= 8 ? 8 : 16;
+  const unsigned long long first = ((unsigned long long)blockIdx.x * blockDim.x + threadIdx.x) / G * kRows;
   const int lane = threadIdx.x & (G - 1);
-  if (row >= rows) return;   // whole groups leave together
-  const bool live = lane < kLanes;
-  uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-  if (live) {
-    x[0] = __ldcs(reinterpret_cast<const uint4*>(k + (size_t)row * D) + lane);
-    x[1] = __ldcs(reinterpret_cast<const uint4*>(v + (size_t)row * D) + lane);
+  if (first >= rows) return;   // whole groups leave together
+  // each step's loads of all rows before the next step's: counts and lengths, data and pages
+  uint32_t bs[kRows], hs[kRows];
+  int ts[kRows], have[kRows], news[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const uint32_t row = (uint32_t)min(first + i, (unsigned long long)rows - 1);
+    const uint32_t bh = fast_div(row, div_t);
+    ts[i] = (int)(row - bh * (uint32_t)T);
+    bs[i] = fast_div(bh, div_h);
+    hs[i] = bh - bs[i] * (uint32_t)c.Hkv;
+    news[i] = first + i < rows ? (new_lens != nullptr ? __ldg(new_lens + bs[i]) : T) : 0;
+    have[i] = __ldg(c.lens + bs[i]);
   }
-  const uint32_t bh = fast_div(row, div_t);
-  const int t = (int)(row - bh * (uint32_t)T);
-  const uint32_t b = fast_div(bh, div_h);
-  const int h = (int)(bh - b * (uint32_t)c.Hkv);
-  if (new_lens != nullptr && t >= new_lens[b]) return;
-  const long long dst = cache_row(c, (int)b, h, (long long)c.lens[b] + t);
-  if (dst < 0) return;
-  if constexpr (!kF8) {
-    if (live) {
-      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.k) + dst * D)[lane] = x[0];
-      reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.v) + dst * D)[lane] = x[1];
-    }
-  } else {
-    const unsigned mask = (G == 32 ? 0xffffffffu : ((1u << G) - 1u) << (threadIdx.x & 31 & ~(G - 1)));
+  uint4 x[kRows][2];
+  int ids[kRows];
+  uint32_t in_page[kRows];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      uint32_t top = 0u;
+  for (int i = 0; i < kRows; ++i) {
+    const long long pos = (long long)have[i] + ts[i];
+    const bool live = ts[i] < news[i] && pos >= 0 && pos <= 0x7fffffffLL;
+    const uint32_t pg = fast_div((uint32_t)pos, c.div_page);
+    in_page[i] = (uint32_t)pos - pg * (uint32_t)c.page;
+    const bool placed = live && pg < (uint32_t)c.max_pages;
+    ids[i] = placed ? __ldg(c.table + (size_t)bs[i] * c.max_pages + pg) : -1;
+    const bool load = placed && lane < kLanes;
+    x[i][0] = load ? __ldcs(reinterpret_cast<const uint4*>(k + (size_t)(first + i) * D) + lane) : make_uint4(0u, 0u, 0u, 0u);
+    x[i][1] = load ? __ldcs(reinterpret_cast<const uint4*>(v + (size_t)(first + i) * D) + lane) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  long long dst[kRows];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+  for (int i = 0; i < kRows; ++i)
+    dst[i] = (unsigned)ids[i] < (unsigned)c.num_pages ? ((long long)ids[i] * c.Hkv + hs[i]) * c.page + in_page[i] : -1;
+  const unsigned mask = ((G == 16 ? 0xffffu : G == 8 ? 0xffu : 0xfu)) << (threadIdx.x & 31 & ~(G - 1));
 #pragma unroll
-      for (int d = G / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(mask, top, d, G));
-      const int e8 = e8_of_amax(top);
-      uint2 out = make_uint2(0u, 0u);
-      if (e8 != kE8Nan) {
-        const float inv = __uint_as_float((uint32_t)(254 - e8) << 23);   // 2^-e
-        const float lim = e8 >= 247 ? 240.f : 448.f;
-        float y[8];
+  for (int i = 0; i < kRows; ++i) {
+    if (dst[i] < 0) continue;   // (the whole group)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[2 * e] = __uint_as_float(w[e] << 16) * inv;
-          y[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * inv;
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (!kF8) {
+        if (lane < kLanes) reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(j ? c.v : c.k) + dst[i] * D)[lane] = x[i][j];
+      } else {
+        const uint32_t w[4] = {x[i][j].x, x[i][j].y, x[i][j].z, x[i][j].w};
+        // largest magnitude bits, two columns at a time (integer order is the order of magnitudes)
+        uint32_t top = max_u16x2(max_u16x2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                 max_u16x2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+#pragma unroll
+        for (int d = G / 2; d > 0; d >>= 1) top = max_u16x2(top, __shfl_xor_sync(mask, top, d, G));
+        const int e8 = e8_of_amax(max(top & 0xffffu, top >> 16));
+        uint2 out = make_uint2(0u, 0u);
+        if (e8 != kE8Nan) {
+          const float inv = __uint_as_float((uint32_t)(254 - e8) << 23);   // 2^-e
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[2 * e] = __uint_as_float(w[e] << 16) * inv;
+            y[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u) * inv;
+          }
+          if (e8 >= 247) {   // (the conversion itself stops at 448)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = fminf(fmaxf(y[e], -240.f), 240.f);
+          }
+          out.x = pack_e4m3x4(y[0], y[1], y[2], y[3]);
+          out.y = pack_e4m3x4(y[4], y[5], y[6], y[7]);
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = fminf(fmaxf(y[e], -lim), lim);
-        out.x = pack_e4m3x4(y[0], y[1], y[2], y[3]);
-        out.y = pack_e4m3x4(y[4], y[5], y[6], y[7]);
+        if (lane < kLanes) reinterpret_cast<uint2*>(static_cast<uint8_t*>(j ? c.v : c.k) + dst[i] * D)[lane] = out;
+        if (lane == 0) (j ? c.vs : c.ks)[dst[i]] = (uint8_t)e8;
       }
-      if (live) reinterpret_cast<uint2*>(static_cast<uint8_t*>(i ? c.v : c.k) + dst * D)[lane] = out;
-      if (lane == 0) (i ? c.vs : c.ks)[dst] = (uint8_t)e8;
     }
   }
 }
@@ -143,51 +171,55 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16(uint32_t w, int e8) {
 }
 
 // Positions [0, N) of every sequence into k_out, v_out [B][Hkv][N][D] (bf16): zeros at and past
-// lens[b] and where the table names no page.  A thread takes 16 columns of one row of K and of V.
-template <int D, bool kF8>
+// lens[b] and where the table names no page.  A thread takes 8 columns (16 bytes of output, so that a
+// warp's stores are contiguous) of kItems rows of K and of V, a block's width apart.
+template <int D, bool kF8, int kItems>
 __global__ void __launch_bounds__(256) attn_cache_read_kernel(CacheView c, __nv_bfloat16* __restrict__ k_out,
                                                               __nv_bfloat16* __restrict__ v_out, int N, FastDiv div_n,
                                                               FastDiv div_h, unsigned long long items) {
-  constexpr int kPieces = D / 16;
-  const unsigned long long item = (unsigned long long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (item >= items) return;
-  const uint32_t row = (uint32_t)(item / kPieces);
-  const int d = (int)(item - (unsigned long long)row * kPieces) * 16;
-  const uint32_t bh = fast_div(row, div_n);
-  const int pos = (int)(row - bh * (uint32_t)N);
-  const uint32_t b = fast_div(bh, div_h);
-  const int h = (int)(bh - b * (uint32_t)c.Hkv);
-  const long long src = pos < c.lens[b] ? cache_row(c, (int)b, h, pos) : -1;
-  uint4 o[2][2] = {};
-  if (src >= 0) {
-    if constexpr (kF8) {
-      const uint4 kw = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.k) + src * D + d));
-      const uint4 vw = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.v) + src * D + d));
-      const int ek = c.ks[src], ev = c.vs[src];
+  constexpr int kPieces = D / 8;
+  const unsigned long long first = (unsigned long long)blockIdx.x * (blockDim.x * kItems) + threadIdx.x;
+  uint4 o[kItems][2];
+  int e[kItems][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 w = i ? vw : kw;
-        const int e = i ? ev : ek;
-        const uint2 a0 = e4m3x4_to_bf16(w.x, e), a1 = e4m3x4_to_bf16(w.y, e);
-        const uint2 a2 = e4m3x4_to_bf16(w.z, e), a3 = e4m3x4_to_bf16(w.w, e);
-        o[i][0] = make_uint4(a0.x, a0.y, a1.x, a1.y);
-        o[i][1] = make_uint4(a2.x, a2.y, a3.x, a3.y);
+  for (int i = 0; i < kItems; ++i) {
+    const unsigned long long item = first + (unsigned long long)i * blockDim.x;
+    o[i][0] = o[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    e[i][0] = e[i][1] = 127;
+    if (item >= items) continue;
+    const uint32_t row = (uint32_t)(item / kPieces);
+    const int d = (int)(item - (unsigned long long)row * kPieces) * 8;
+    const uint32_t bh = fast_div(row, div_n);
+    const int pos = (int)(row - bh * (uint32_t)N);
+    const uint32_t b = fast_div(bh, div_h);
+    if (pos >= __ldg(c.lens + b)) continue;
+    const long long src = cache_row(c, (int)b, (int)(bh - b * (uint32_t)c.Hkv), pos);
+    if (src < 0) continue;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (kF8) {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(j ? c.v : c.k) + src * D + d));
+        o[i][j].x = w.x;
+        o[i][j].y = w.y;
+        e[i][j] = (j ? c.vs : c.ks)[src];
+      } else {
+        o[i][j] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(j ? c.v : c.k) + src * D + d));
       }
-    } else {
-      const uint4* kp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.k) + src * D + d);
-      const uint4* vp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.v) + src * D + d);
-      o[0][0] = __ldcs(kp);
-      o[0][1] = __ldcs(kp + 1);
-      o[1][0] = __ldcs(vp);
-      o[1][1] = __ldcs(vp + 1);
     }
   }
-  uint4* ko = reinterpret_cast<uint4*>(k_out + (size_t)row * D + d);
-  uint4* vo = reinterpret_cast<uint4*>(v_out + (size_t)row * D + d);
-  ko[0] = o[0][0];
-  ko[1] = o[0][1];
-  vo[0] = o[1][0];
-  vo[1] = o[1][1];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const unsigned long long item = first + (unsigned long long)i * blockDim.x;
+    if (item >= items) return;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (kF8) {
+        const uint2 a = e4m3x4_to_bf16(o[i][j].x, e[i][j]), b = e4m3x4_to_bf16(o[i][j].y, e[i][j]);
+        o[i][j] = make_uint4(a.x, a.y, b.x, b.y);
+      }
+      __stcs(reinterpret_cast<uint4*>(j ? v_out : k_out) + item, o[i][j]);
+    }
+  }
 }
 
 // Products of bf16 pairs (nearest even; subnormal operands and results count).

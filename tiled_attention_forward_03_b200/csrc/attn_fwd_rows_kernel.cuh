@@ -12,9 +12,10 @@
 //  * Keys, bf16: contiguous, or in pages, by TMA boxes of the largest of 128, 64, 32, 16 rows that
 //    divides a page.  Each batch row has its own count of them; the MMA warp overwrites the last
 //    value tile's rows behind it with zeros (its probabilities are 0, and 0 * NaN would not be).
-//  * Keys, E4M3 (kF8): codes and exponents go by TMA to a raw ring; a fourth warpgroup converts them
-//    to bf16, exactly (a power-of-two scale rounds nothing), and stores them as TMA would, 128-byte
-//    swizzled.  One conversion serves 128 rows and is hidden behind their exponentials.
+//  * Keys, E4M3 (kF8): codes and exponents go by TMA to a raw ring; two more warpgroups convert them,
+//    every other tile each, to bf16, exactly (a power-of-two scale rounds nothing), and store them as
+//    TMA would, 128-byte swizzled.  One conversion serves 128 rows and is hidden behind their
+//    exponentials (with one warpgroup it was not: 4100 clocks a block instead of 2100).
 //  * Work: as in the decode kernel, the 128-key blocks of all units stand in one line and each CTA
 //    takes an equal, contiguous range of it, whatever the lengths; a range holds whole units and at
 //    most two parts of units, which go unnormalised, in fp32, to the CTA's two slots of the workspace
@@ -25,7 +26,7 @@
 //    the time).
 //
 //   warps 0-3, 4-7  softmax warpgroups     warp 8   TMA producer     warp 9  MMA issuer
-//   warp 10  output store (cross)          warp 11  scheduler        warps 12-15 (kF8) converters
+//   warp 10  output store (cross)          warp 11  scheduler        warps 12-19 (kF8) converters
 //
 // Every mbarrier wait is bounded; named barriers are only reached by all their participants.
 #pragma once
@@ -46,16 +47,16 @@ enum : unsigned {
   kSiteRowsSchedule = 47,
 };
 
-// Register split.  bf16: the forward kernel's (384 threads at 168).  kF8: 512 threads at 128;
-// 2 * 128 * 168 + 128 * 56 + 128 * 120 == 512 * 128.
+// Register split.  bf16: the forward kernel's (384 threads at 168).  kF8: 640 threads at 96;
+// 2 * 128 * 152 + 128 * 48 + 2 * 128 * 64 == 640 * 96.
 template <bool kF8>
 struct RowsCfg {
-  static constexpr int kThreads = kF8 ? 512 : 384;
-  static constexpr int kRegsLaunch = kF8 ? 128 : kRegsAtLaunch;
-  static constexpr int kSoftmax = kF8 ? 168 : kRegsSoftmax;
-  static constexpr int kControl = kRegsControl;
-  static constexpr int kConvert = 120;
-  static_assert(2 * 128 * kSoftmax + 128 * kControl + (kF8 ? 128 * kConvert : 0) <= kThreads * kRegsLaunch,
+  static constexpr int kThreads = kF8 ? 640 : 384;
+  static constexpr int kRegsLaunch = kF8 ? 96 : kRegsAtLaunch;
+  static constexpr int kSoftmax = kF8 ? 152 : kRegsSoftmax;
+  static constexpr int kControl = kF8 ? 48 : kRegsControl;
+  static constexpr int kConvert = 64;
+  static_assert(2 * 128 * kSoftmax + 128 * kControl + (kF8 ? 256 * kConvert : 0) <= kThreads * kRegsLaunch,
                 "register split exceeds the launch allocation");
 };
 
@@ -69,13 +70,16 @@ struct RowsSmem {
   static constexpr int kChunkBytes = kBlockM * 128;
   static constexpr int kTileBytes = kChunks * kChunkBytes;
   static constexpr int kStages = kF8 ? (kChunks == 2 ? 3 : 6) : (kChunks == 2 ? 4 : 8);   // K/V ring (bf16 tiles)
-  static constexpr int kRaw = kF8 ? 3 : 0;                // raw ring (E4M3 tiles and their exponents)
+  // raw ring (E4M3 tiles and their exponents): with three a block took 3500 clocks, the tiles' latency
+  static constexpr int kRaw = kF8 ? 5 : 0;
   static constexpr int kRawBytes = kBlockN * D;
   static constexpr int kOChunks = D / 32;                 // 32-column output chunks (64-byte rows)
   static constexpr int kStageBytes = kBlockM * 64;        // one staged output chunk: 8 KB
   static_assert(kOChunks * kStageBytes <= kTileBytes, "staged O must fit in a Q buffer");
-  static constexpr int kQOff = 0;                         // two Q buffers (O staging after their last use)
-  static constexpr int kKVOff = 2 * kTileBytes;
+  // Q buffers: two (O staging after their last use); one for kF8, whose units are long
+  static constexpr int kQBufs = kF8 ? 1 : 2;
+  static constexpr int kQOff = 0;
+  static constexpr int kKVOff = kQBufs * kTileBytes;
   static constexpr int kRawOff = kKVOff + kStages * kTileBytes;
   static constexpr int kExpOff = kRawOff + kRaw * kRawBytes;
   static constexpr int kXOff = kExpOff + kRaw * kBlockN;  // (m, l) exchange [unit parity][warpgroup][row]
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
     for (int i = 0; i < kRowsQueue; ++i) {
       mbar_init(&u_full[i], 1);
       // softmax warps, producer, MMA warp, store warp, converter warps
-      mbar_init(&u_empty[i], 8 + 1 + 1 + (p.prefix ? 0 : 1) + (kF8 ? 4 : 0));
+      mbar_init(&u_empty[i], 8 + 1 + 1 + (p.prefix ? 0 : 1) + (kF8 ? 8 : 0));
     }
     for (int i = 0; i < R; ++i) {
       mbar_init(&raw_full[i], 1);
@@ -485,7 +489,7 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
         for (int half = 0; half < 2 && ok; ++half) {   // V(i-2), then K(i)
           if ((half == 0 && i < 2) || !__all_sync(0xffffffffu, half ? sc.valid : pc.valid)) continue;
           if (half && sc.j == sc.w.jb) {   // the unit's Q tile
-            const int qb = (int)(sc.ord - 1u) & 1;
+            const int qb = (int)(sc.ord - 1u) % Plan::kQBufs;
             if (!(ok = wait_all(&q_empty[qb], (q_par >> qb) & 1u))) break;
             q_par ^= 1u << qb;
             if (lane == 0) {
@@ -585,7 +589,7 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
           if (++pc.j >= pc.w.je) next_unit(pc, true, true, kSiteRowsMma);
         }
         if (__all_sync(0xffffffffu, sc.valid)) {
-          const int qb = (int)(sc.ord - 1u) & 1;
+          const int qb = (int)(sc.ord - 1u) % Plan::kQBufs;
           const bool last = sc.j == sc.w.je - 1;
           if (sc.j == sc.w.jb) {
             if (!(ok = wait_all(&q_full[qb], (q_par >> qb) & 1u))) break;
@@ -835,61 +839,66 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
     __syncwarp();
   } else if constexpr (kF8) {
     // ------------------------------------------------------------ converters: E4M3 -> bf16 tiles
-    // A 128-row tile takes kPasses passes; in each, kLanes lanes share a row (16 codes each).
+    // Warpgroup c (0, 1) takes the tiles of its parity in the order of the ring.  A 128-row tile takes
+    // kPasses passes; in each, kLanes lanes share a row (16 codes each).
     regs_decrease<Cfg::kConvert>();
     constexpr int kLanes = D / 16;                    // 2, 4, 6, 8
     constexpr int kRows = 128 / kLanes / 16 * 16;     // 64, 32, 16 (96 of the 128 threads), 16
     constexpr int kPasses = kBlockN / kRows;
-    const int tid = threadIdx.x - 384;
+    constexpr int kBatch = kPasses < 4 ? kPasses : 4;   // passes at a time (registers)
+    const uint32_t group = (uint32_t)(warp - 12) >> 2;
+    const int tid = (threadIdx.x - 384) & 127;
     const int pr = tid / kLanes, col = (tid - pr * kLanes) * 16;
     const bool mine = pr < kRows;
     const uint32_t at = (uint32_t)((col >> 6) * Plan::kChunkBytes), q = (uint32_t)(col & 63) >> 3;
     Ring ring, raw;
+    uint32_t tile = 0u;
     bool ok = true;
     auto convert = [&](int len, int j) -> bool {
       if (!wait_phase(&raw_full[raw.stage], raw.phase, abort_flag, kSiteRowsConvert)) return false;
+      if (!wait_phase(&kv_empty[ring.stage], ring.phase ^ 1u, abort_flag, kSiteRowsConvert)) return false;
       const uint8_t* codes = sRaw + raw.stage * Plan::kRawBytes;
       const uint8_t* exps = sExp + raw.stage * kBlockN;
-      uint4 x[kPasses];
-      uint32_t e[kPasses];
-      uint32_t top = 0u;
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int r = i * kRows + pr;
-        const bool live = mine && j * kBlockN + r < len;
-        x[i] = live ? *reinterpret_cast<const uint4*>(codes + r * D + col) : make_uint4(0u, 0u, 0u, 0u);
-        e[i] = live ? exps[r] : 127u;
-        top = max(top, e[i]);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&raw_empty[raw.stage]);
-      raw.advance<R == 0 ? 1 : R>();
-      if (!wait_phase(&kv_empty[ring.stage], ring.phase ^ 1u, abort_flag, kSiteRowsConvert)) return false;
       const uint32_t base = smem_u32(sKV) + ring.stage * Plan::kTileBytes + at;
-      // bits -> value * 2^-120, times 2^(e - 7) in one multiplication while that is a bf16 number,
-      // else (exponents above 2^7, and rows marked NaN) times 2^120 and the scale
-      const bool far = __any_sync(0xffffffffu, top > 134u);
+#pragma unroll 1
+      for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
+        uint4 x[kBatch];
+        uint32_t e[kBatch], top = 0u;
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const int r = i * kRows + pr;
-        const uint32_t f = far ? 0x7b807b80u : (e[i] + 120u) * 0x00800080u;
-        uint2 y[4] = {e4m3x4_scaled(x[i].x, f), e4m3x4_scaled(x[i].y, f), e4m3x4_scaled(x[i].z, f),
-                      e4m3x4_scaled(x[i].w, f)};
-        if (far) {
-          const uint32_t f2 = e8_bf16x2((int)e[i]);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = make_uint2(mul_bf16x2(y[k].x, f2), mul_bf16x2(y[k].y, f2));
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = (p0 + i) * kRows + pr;
+          const bool live = mine && j * kBlockN + r < len;
+          x[i] = live ? *reinterpret_cast<const uint4*>(codes + r * D + col) : make_uint4(0u, 0u, 0u, 0u);
+          e[i] = live ? exps[r] : 127u;
+          top = max(top, e[i]);
         }
-        if (mine) {
-          const uint32_t row = base + r * 128;
-          st_shared_v4(row + ((q ^ (r & 7)) << 4), y[0].x, y[0].y, y[1].x, y[1].y);
-          st_shared_v4(row + (((q + 1) ^ (r & 7)) << 4), y[2].x, y[2].y, y[3].x, y[3].y);
+        // bits -> value * 2^-120, times 2^(e - 7) in one multiplication while that is a bf16 number,
+        // else (exponents above 2^7, and rows marked NaN) times 2^120 and the scale
+        const bool far = __any_sync(0xffffffffu, top > 134u);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = (p0 + i) * kRows + pr;
+          const uint32_t f = far ? 0x7b807b80u : (e[i] + 120u) * 0x00800080u;
+          uint2 y[4] = {e4m3x4_scaled(x[i].x, f), e4m3x4_scaled(x[i].y, f), e4m3x4_scaled(x[i].z, f),
+                        e4m3x4_scaled(x[i].w, f)};
+          if (far) {
+            const uint32_t f2 = e8_bf16x2((int)e[i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = make_uint2(mul_bf16x2(y[k].x, f2), mul_bf16x2(y[k].y, f2));
+          }
+          if (mine) {
+            const uint32_t row = base + r * 128;
+            st_shared_v4(row + ((q ^ (r & 7)) << 4), y[0].x, y[0].y, y[1].x, y[1].y);
+            st_shared_v4(row + (((q + 1) ^ (r & 7)) << 4), y[2].x, y[2].y, y[3].x, y[3].y);
+          }
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&kv_full[ring.stage]);
-      ring.advance<S>();
+      if (lane == 0) {
+        mbar_arrive(&raw_empty[raw.stage]);
+        mbar_arrive(&kv_full[ring.stage]);
+      }
       return true;
     };
     Cursor sc, pc;
@@ -900,7 +909,11 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
 #pragma unroll 1
       for (int half = 0; half < 2 && ok; ++half) {
         if ((half == 0 && i < 2) || !__all_sync(0xffffffffu, half ? sc.valid : pc.valid)) continue;
-        ok = __all_sync(0xffffffffu, convert(half ? sc.w.len : pc.w.len, half ? sc.j : pc.j));
+        if ((tile & 1u) == group)
+          ok = __all_sync(0xffffffffu, convert(half ? sc.w.len : pc.w.len, half ? sc.j : pc.j));
+        ++tile;
+        raw.advance<R == 0 ? 1 : R>();
+        ring.advance<S>();
         if (!ok) break;
         if (half) {
           if (++sc.j >= sc.w.je) next_unit(sc, false, true, kSiteRowsConvert);

@@ -126,7 +126,7 @@ constexpr int kDecCtasPerSm = 3;    // resident CTAs (the kernel's launch bounds
 // the file's head comment, and E4M3 Hkv8 D128, all lengths at the limit: see the table of the notes.
 constexpr int kDecShortBlocks = 16, kDecTinyBlocks = 2;
 // Else a CTA takes whole units where no sequence has more than this many blocks: a launch less.
-constexpr int kDecWholeBlocks = 8;
+constexpr int kDecWholeBlocks = 4;
 
 // `cap`: keys a sequence can have at most.  `shared`: a prefix of `prefix_len` keys comes first;
 // `prefix_here`: this kernel computes it too.
@@ -489,19 +489,28 @@ int attn_cache_append(const void* k, const void* v, void* k_cache, void* v_cache
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(new_lens, 4)) return ATTN_ERR_MISALIGNED;
   const uint32_t rows = (uint32_t)((long long)B * Hkv * T);
   const int lanes = D / 8 <= 4 ? 4 : D / 8 <= 8 ? 8 : 16;
-  const unsigned grid = (unsigned)(((unsigned long long)rows * lanes + 255) / 256);
+  // four rows a group where that still leaves blocks for every SM several times over
+  const bool many = (unsigned long long)rows * lanes >= (1u << 20);
+  const unsigned long long groups = many ? ((unsigned long long)rows + 3) / 4 : rows;
+  const unsigned grid = (unsigned)((groups * lanes + 255) / 256);
   const attn::CacheView c = cache_view(a);
   const auto kb = reinterpret_cast<const __nv_bfloat16*>(k);
   const auto vb = reinterpret_cast<const __nv_bfloat16*>(v);
   const attn::FastDiv dt = attn::make_fast_div((uint32_t)T), dh = attn::make_fast_div((uint32_t)Hkv);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool f8 = k_scale != nullptr;
   auto go = [&](auto kern) { kern<<<grid, 256, 0, s>>>(kb, vb, c, new_lens, T, dt, dh, rows); };
+  auto pick = [&](auto dim) {
+    constexpr int D_ = decltype(dim)::value;
+    if (k_scale != nullptr)
+      many ? go(attn::attn_cache_append_kernel<D_, true, 4>) : go(attn::attn_cache_append_kernel<D_, true, 1>);
+    else
+      many ? go(attn::attn_cache_append_kernel<D_, false, 4>) : go(attn::attn_cache_append_kernel<D_, false, 1>);
+  };
   switch (D) {
-    case 32: f8 ? go(attn::attn_cache_append_kernel<32, true>) : go(attn::attn_cache_append_kernel<32, false>); break;
-    case 64: f8 ? go(attn::attn_cache_append_kernel<64, true>) : go(attn::attn_cache_append_kernel<64, false>); break;
-    case 96: f8 ? go(attn::attn_cache_append_kernel<96, true>) : go(attn::attn_cache_append_kernel<96, false>); break;
-    default: f8 ? go(attn::attn_cache_append_kernel<128, true>) : go(attn::attn_cache_append_kernel<128, false>); break;
+    case 32: pick(std::integral_constant<int, 32>()); break;
+    case 64: pick(std::integral_constant<int, 64>()); break;
+    case 96: pick(std::integral_constant<int, 96>()); break;
+    default: pick(std::integral_constant<int, 128>()); break;
   }
   return launch_status("cache append kernel launch");
 }
@@ -518,20 +527,27 @@ int attn_cache_read(const void* k_cache, const void* v_cache, const void* k_scal
   if (!k || !v) return ATTN_ERR_INVALID_ARG;
   if ((st = cache_pointer_checks(a)) != ATTN_OK) return st;
   if (!aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_MISALIGNED;
-  const unsigned long long items = (unsigned long long)B * Hkv * N * (D / 16);
-  const unsigned grid = (unsigned)((items + 255) / 256);
+  const unsigned long long items = (unsigned long long)B * Hkv * N * (D / 8);
+  const bool many = items >= (1u << 20);   // two items a thread where that still fills the GPU
+  const unsigned grid = (unsigned)((items + (many ? 511 : 255)) / (many ? 512 : 256));
   const attn::CacheView c = cache_view(a);
   const auto kb = reinterpret_cast<__nv_bfloat16*>(k);
   const auto vb = reinterpret_cast<__nv_bfloat16*>(v);
   const attn::FastDiv dn = attn::make_fast_div((uint32_t)N), dh = attn::make_fast_div((uint32_t)Hkv);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool f8 = k_scale != nullptr;
   auto go = [&](auto kern) { kern<<<grid, 256, 0, s>>>(c, kb, vb, N, dn, dh, items); };
+  auto pick = [&](auto dim) {
+    constexpr int D_ = decltype(dim)::value;
+    if (k_scale != nullptr)
+      many ? go(attn::attn_cache_read_kernel<D_, true, 2>) : go(attn::attn_cache_read_kernel<D_, true, 1>);
+    else
+      many ? go(attn::attn_cache_read_kernel<D_, false, 2>) : go(attn::attn_cache_read_kernel<D_, false, 1>);
+  };
   switch (D) {
-    case 32: f8 ? go(attn::attn_cache_read_kernel<32, true>) : go(attn::attn_cache_read_kernel<32, false>); break;
-    case 64: f8 ? go(attn::attn_cache_read_kernel<64, true>) : go(attn::attn_cache_read_kernel<64, false>); break;
-    case 96: f8 ? go(attn::attn_cache_read_kernel<96, true>) : go(attn::attn_cache_read_kernel<96, false>); break;
-    default: f8 ? go(attn::attn_cache_read_kernel<128, true>) : go(attn::attn_cache_read_kernel<128, false>); break;
+    case 32: pick(std::integral_constant<int, 32>()); break;
+    case 64: pick(std::integral_constant<int, 64>()); break;
+    case 96: pick(std::integral_constant<int, 96>()); break;
+    default: pick(std::integral_constant<int, 128>()); break;
   }
   return launch_status("cache read kernel launch");
 }
