@@ -463,9 +463,13 @@ int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cac
                            int page_size, int max_pages, float scale, void* workspace, size_t workspace_bytes,
                            void* stream);
 
-/* Workspace attn_fwd_shared_prefix needs on the current device; -1 on rejected sizes or a CUDA error. */
+/*
+ * Workspace attn_fwd_shared_prefix needs on the current device (e4m3: 1 for an E4M3 cache, whose prefix
+ * is converted to bf16 in the workspace, up to 256 MB, when many rows read it); -1 on rejected sizes
+ * or a CUDA error.
+ */
 long long attn_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int page_size, int max_pages,
-                                                 int prefix_len);
+                                                 int prefix_len, int e4m3);
 
 /*
  * attn_fwd_cross -- attention to keys of another length (a decoder's to an encoder's states).

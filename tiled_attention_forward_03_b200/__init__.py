@@ -113,7 +113,7 @@ def _load() -> ctypes.CDLL:
     L.attn_fwd_decode_workspace_bytes.restype = ctypes.c_longlong
     L.attn_fwd_shared_prefix.argtypes = [vp] * 6 + [i] + [vp] * 4 + [i] * 8 + [f, vp, ctypes.c_size_t, vp]
     L.attn_fwd_shared_prefix.restype = i
-    L.attn_fwd_shared_prefix_workspace_bytes.argtypes = [i] * 8
+    L.attn_fwd_shared_prefix_workspace_bytes.argtypes = [i] * 9
     L.attn_fwd_shared_prefix_workspace_bytes.restype = ctypes.c_longlong
     L.attn_fwd_cross.argtypes = [vp] * 6 + [i] * 6 + [f, vp, ctypes.c_size_t, vp]
     L.attn_fwd_cross.restype = i
@@ -268,8 +268,9 @@ def attn_fwd_shared_prefix(q, k_cache, v_cache, k_scale, v_scale, prefix_table, 
 
 
 def attn_fwd_shared_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, D: int, page_size: int, max_pages: int,
-                                           prefix_len: int) -> int:
-    return lib.attn_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, T, D, page_size, max_pages, prefix_len)
+                                           prefix_len: int, e4m3: bool) -> int:
+    return lib.attn_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, T, D, page_size, max_pages, prefix_len,
+                                                      int(bool(e4m3)))
 
 
 def attn_fwd_cross(q, k, v, k_lens, o, lse, B, Hq, Hkv, Nq, Nk, D, scale, workspace, workspace_bytes, stream) -> int:
@@ -1013,7 +1014,7 @@ def forward_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len: int, bl
     s = _raw_stream(stream, dev)
     with _On(dev):
         nbytes = _workspace_bytes("attn_fwd_shared_prefix_workspace_bytes", dev.index, B, Hq, Hkv, T, D, page, max_pages,
-                                  prefix_len)
+                                  prefix_len, int(k_scale is not None))
         ws = _scratch(nbytes, dev, stream) if nbytes > 0 else None
         st = lib.attn_fwd_shared_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
                                         _ptr(v_scale), prefix_table.data_ptr(), prefix_len, block_table.data_ptr(),

@@ -40,7 +40,8 @@ struct CacheView {
   uint8_t* ks;        // E8M0 bytes, null for a bf16 cache
   uint8_t* vs;
   const int* table;   // [B][max_pages]
-  const int* lens;    // [B]
+  const int* lens;    // [B], or null (reading): len_all
+  int len_all;
   int max_pages, num_pages, page, Hkv;
   FastDiv div_page;
 };
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(256) attn_cache_read_kernel(CacheView c, __nv_
     const uint32_t bh = fast_div(row, div_n);
     const int pos = (int)(row - bh * (uint32_t)N);
     const uint32_t b = fast_div(bh, div_h);
-    if (pos >= __ldg(c.lens + b)) continue;
+    if (pos >= (c.lens != nullptr ? __ldg(c.lens + b) : c.len_all)) continue;
     const long long src = cache_row(c, (int)b, (int)(bh - b * (uint32_t)c.Hkv), pos);
     if (src < 0) continue;
 #pragma unroll

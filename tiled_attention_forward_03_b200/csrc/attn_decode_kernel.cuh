@@ -62,7 +62,9 @@ namespace attn {
 
 constexpr int kDecThreads = 128;
 constexpr int kDecBlock = 64;       // keys per block of the schedule
-constexpr int kDecStages = 8;       // of all the CTA's rings together
+// Stages of all the CTA's rings together: eight, with three CTAs an SM; the warp form, which has fewer
+// warps with work, twelve and two CTAs.
+__host__ __device__ constexpr int dec_stages(bool warps) { return warps ? 12 : 8; }
 constexpr int kDecStageBytes = 8192;
 
 enum : unsigned {
@@ -279,12 +281,14 @@ struct DecCfg {
   static constexpr int kVWords = D * kElem / 32;            // of a value row (1/8 of it)
   static constexpr int kRowStride = D + 4;                  // floats, of a row of the join
   static constexpr int kJoinBytes = 4 * 16 * kRowStride * 4;
-  static_assert(kJoinBytes <= kDecStages * kDecStageBytes, "the join takes the rings' place");
+  static_assert(kJoinBytes <= dec_stages(false) * kDecStageBytes, "the join takes the rings' place");
 };
 // E4M3: a stage's exponents, K's then V's (32 keys at most), behind all the stages; slack for
 // 1024-byte alignment
 constexpr int kDecExpBytes = 64;
-constexpr int kDecSmem = kDecStages * (kDecStageBytes + kDecExpBytes) + 1024;
+__host__ __device__ constexpr int dec_smem(bool warps) {
+  return dec_stages(warps) * (kDecStageBytes + kDecExpBytes) + 1024;
+}
 
 // Byte `b` of row `r` in a tile of 128-byte rows as TMA swizzles it.
 __device__ __forceinline__ uint32_t dec_sw(uint32_t r, uint32_t b) { return r * 128 + (b ^ ((r & 7) << 4)); }
@@ -380,12 +384,13 @@ __device__ __forceinline__ uint32_t dec_pair(const uint32_t* r0, const uint32_t*
 
 // kN: tiles of 8 rows a warp takes (1: units of at most 8 rows; else 2).
 template <int D, bool kF8, int kN, bool kWarp>
-__global__ void __launch_bounds__(kDecThreads, 3)
+__global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
     attn_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                        const DecParams p) {
   using Cfg = DecCfg<D, kF8>;
   constexpr int G = Cfg::kGroups, KW = Cfg::kKWords, VW = Cfg::kVWords;
   constexpr int kTile = 8 * kN;   // rows of a warp
+  constexpr int kDecStages = dec_stages(kWarp);
   extern __shared__ uint8_t smem_raw[];
   __shared__ float2 sml[4][16];
   __shared__ long long scratch[16];
@@ -881,21 +886,39 @@ __global__ void __launch_bounds__(kDecThreads, 3)
             acc[2 * c + 1] = o[nt][c][2 + e];
           }
           if (p.many.tiles > 0) {
+            // the prefix's parts, four at a time: their sums, then their rows, all loads before any use
+            constexpr int kAhead = 4;
             const DecParts pt = dec_prefix_parts(p, seq, h, i);
-            for (int k = 0; k < pt.n; ++k) {
-              const long long at = pt.at(k);
-              const float2 ml = p.many.ml[at];
-              const float mn = fmaxf(mt, ml.x);
-              const float a = dec_weight(make_float2(mt, lt), mn), w = dec_weight(ml, mn);
-              mt = mn;
-              lt = fmaf(ml.y, w, lt * a);
+            for (int k0 = 0; k0 < pt.n; k0 += kAhead) {
+              float2 ml[kAhead];
+              float4 v[kAhead][D / 32];
 #pragma unroll
-              for (int ct = 0; ct < D / 8; ct += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(p.many.o + at * D + dec_col<D, kF8>(ct, g));
-                acc[ct] = fmaf(v.x, w, acc[ct] * a);
-                acc[ct + 1] = fmaf(v.y, w, acc[ct + 1] * a);
-                acc[ct + 2] = fmaf(v.z, w, acc[ct + 2] * a);
-                acc[ct + 3] = fmaf(v.w, w, acc[ct + 3] * a);
+              for (int k = 0; k < kAhead; ++k) {
+                const long long at = pt.at(min(k0 + k, pt.n - 1));
+                ml[k] = p.many.ml[at];
+#pragma unroll
+                for (int ct = 0; ct < D / 8; ct += 4)
+                  v[k][ct / 4] = *reinterpret_cast<const float4*>(p.many.o + at * D + dec_col<D, kF8>(ct, g));
+              }
+              float mn = mt;
+#pragma unroll
+              for (int k = 0; k < kAhead; ++k) mn = fmaxf(mn, ml[k].x);
+              const float a = dec_weight(make_float2(mt, lt), mn);
+              mt = mn;
+              lt *= a;
+#pragma unroll
+              for (int ct = 0; ct < D / 8; ++ct) acc[ct] *= a;
+#pragma unroll
+              for (int k = 0; k < kAhead; ++k) {
+                const float w = k0 + k < pt.n ? dec_weight(ml[k], mn) : 0.f;
+                lt = fmaf(ml[k].y, w, lt);
+#pragma unroll
+                for (int ct = 0; ct < D / 8; ct += 4) {
+                  acc[ct] = fmaf(v[k][ct / 4].x, w, acc[ct]);
+                  acc[ct + 1] = fmaf(v[k][ct / 4].y, w, acc[ct + 1]);
+                  acc[ct + 2] = fmaf(v[k][ct / 4].z, w, acc[ct + 2]);
+                  acc[ct + 3] = fmaf(v[k][ct / 4].w, w, acc[ct + 3]);
+                }
               }
             }
           }

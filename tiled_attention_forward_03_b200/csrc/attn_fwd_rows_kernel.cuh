@@ -103,6 +103,7 @@ struct RowsParams {
   int B, Hkv, GT;
   int tiles;                 // of a key group: (b, h), or for a prefix h
   int prefix;                // 1: a tile has rows of all sequences
+  int behind;                // 1: the keys are written by the kernel before
   int seqs;                  // sequences in a tile (prefix; else 1)
   int seq_tiles;             // tiles of a sequence (prefix with GT > 128; else 1)
   int q_box_rows;            // rows a Q tile load fills
@@ -480,6 +481,7 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
         return true;
       };
       // Tiles in the order the MMA warp reads them: K(0), K(1), then V(g), K(g+2) for g = 0, 1, ...
+      if (p.behind) wait_for_previous();
       Cursor sc, pc;
       next_unit(sc, false, true, kSiteRowsProducer);
       next_unit(pc, true, true, kSiteRowsProducer);
@@ -848,7 +850,17 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
     constexpr int kBatch = kPasses < 4 ? kPasses : 4;   // passes at a time (registers)
     const uint32_t group = (uint32_t)(warp - 12) >> 2;
     const int tid = (threadIdx.x - 384) & 127;
-    const int pr = tid / kLanes, col = (tid - pr * kLanes) * 16;
+    // This thread's row of a pass and its columns.  D = 128, where shared memory's bandwidth bounds the
+    // block (S reads 64 KB, P V 32, the conversion 96, all at 128 bytes a clock): the raw rows are
+    // 128-byte swizzled too, and the eight lanes of a 128-byte access take one 64-column chunk of rows r
+    // and r ^ 5, whose swizzles send their pieces to different banks in both layouts.
+    constexpr bool kPairs = D == 128;
+    int pr = tid / kLanes, col = (tid - pr * kLanes) * 16;
+    if constexpr (kPairs) {
+      const int pair = tid >> 3;   // 16: eight row pairs, two chunks
+      pr = ((pair >> 1 & 3) | (pair >> 1 & 4) << 1) ^ ((tid >> 2 & 1) ? 5 : 0);
+      col = (pair & 1) * 64 + (tid & 3) * 16;
+    }
     const bool mine = pr < kRows;
     const uint32_t at = (uint32_t)((col >> 6) * Plan::kChunkBytes), q = (uint32_t)(col & 63) >> 3;
     Ring ring, raw;
@@ -868,7 +880,8 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
         for (int i = 0; i < kBatch; ++i) {
           const int r = (p0 + i) * kRows + pr;
           const bool live = mine && j * kBlockN + r < len;
-          x[i] = live ? *reinterpret_cast<const uint4*>(codes + r * D + col) : make_uint4(0u, 0u, 0u, 0u);
+          x[i] = live ? *reinterpret_cast<const uint4*>(codes + r * D + (kPairs ? col ^ ((r & 7) << 4) : col))
+                      : make_uint4(0u, 0u, 0u, 0u);
           e[i] = live ? exps[r] : 127u;
           top = max(top, e[i]);
         }

@@ -44,6 +44,7 @@ attn::CacheView cache_view(const CacheArgs& a) {
   c.vs = static_cast<uint8_t*>(const_cast<void*>(a.vs));
   c.table = a.table;
   c.lens = a.lens;
+  c.len_all = 0;
   c.max_pages = a.max_pages;
   c.num_pages = a.num_pages;
   c.page = a.page;
@@ -80,6 +81,30 @@ int encode_rows_map(CUtensorMap* map, const void* base, int rank, const cuuint64
   if (r == CUDA_SUCCESS) return ATTN_OK;
   record_driver_error("cuTensorMapEncodeTiled", (int)r);
   return ATTN_ERR_CUDA;
+}
+
+// Positions [0, N) of B sequences into k, v [B][Hkv][N][D].
+void launch_cache_read(const attn::CacheView& c, bool f8, void* k, void* v, int B, int N, int D, cudaStream_t s) {
+  const unsigned long long items = (unsigned long long)B * c.Hkv * N * (D / 8);
+  const bool many = items >= (1u << 20);   // two items a thread where that still fills the GPU
+  const unsigned grid = (unsigned)((items + (many ? 511 : 255)) / (many ? 512 : 256));
+  const auto kb = reinterpret_cast<__nv_bfloat16*>(k);
+  const auto vb = reinterpret_cast<__nv_bfloat16*>(v);
+  const attn::FastDiv dn = attn::make_fast_div((uint32_t)N), dh = attn::make_fast_div((uint32_t)c.Hkv);
+  auto go = [&](auto kern) { kern<<<grid, 256, 0, s>>>(c, kb, vb, N, dn, dh, items); };
+  auto pick = [&](auto dim) {
+    constexpr int D_ = decltype(dim)::value;
+    if (f8)
+      many ? go(attn::attn_cache_read_kernel<D_, true, 2>) : go(attn::attn_cache_read_kernel<D_, true, 1>);
+    else
+      many ? go(attn::attn_cache_read_kernel<D_, false, 2>) : go(attn::attn_cache_read_kernel<D_, false, 1>);
+  };
+  switch (D) {
+    case 32: pick(std::integral_constant<int, 32>()); break;
+    case 64: pick(std::integral_constant<int, 64>()); break;
+    case 96: pick(std::integral_constant<int, 96>()); break;
+    default: pick(std::integral_constant<int, 128>()); break;
+  }
 }
 
 // ---------------------------------------------------------------- decode schedule
@@ -120,7 +145,7 @@ struct DecPlan {
 };
 
 constexpr int kDecMinShare = 2;     // blocks of 64 keys
-constexpr int kDecCtasPerSm = 3;    // resident CTAs (the kernel's launch bounds)
+constexpr int kDecCtasPerSm = 3, kDecWarpCtasPerSm = 2;   // resident CTAs (the kernel's launch bounds)
 // Warps take whole units where no sequence has more than this many blocks, and there are units for
 // all CTAs (or sequences are so short that there is nothing to share).  Measured on B200: at the end of
 // the file's head comment, and E4M3 Hkv8 D128, all lengths at the limit: see the table of the notes.
@@ -152,12 +177,13 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
     blocks += (double)Hkv * pl.prefix_row_blocks * (double)pre_blocks;
   }
   const double most = pl.warps ? (double)((units + 3) / 4) : pl.whole_units ? (double)units : blocks / kDecMinShare + 1;
-  pl.grid = (unsigned)(most < (double)ctas ? (long long)most : ctas);
+  const long long resident = pl.warps ? (long long)kDecWarpCtasPerSm * num_sms : ctas;
+  pl.grid = (unsigned)(most < (double)resident ? (long long)most : resident);
   if (pl.grid < 1) pl.grid = 1;
   pl.join = !pl.whole_units;
   const size_t slots = pl.whole_units ? 0 : 2 * (size_t)pl.grid * pl.unit_rows;
   pl.slot_o = slots * D * sizeof(float);
-  pl.slot_ml = slots * sizeof(float2);
+  pl.slot_ml = (slots * sizeof(float2) + 255) / 256 * 256;
   const size_t rows = shared && !pl.whole_units ? ((size_t)B * Hkv * (size_t)GT + 63) / 64 * 64 : 0;
   pl.area_o = rows * D * sizeof(float);
   pl.area_ml = rows * sizeof(float2);
@@ -174,7 +200,7 @@ int launch_decode_dim(attn::DecParams& p, const DecPlan& pl, const void* k, cons
   if (e == cudaSuccess) {
     std::call_once(info[dev].once, [&] {
       info[dev].err = cudaFuncSetAttribute(reinterpret_cast<const void*>(attn::attn_decode_kernel<D, kF8, kN, kWarp>),
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, attn::kDecSmem);
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, attn::dec_smem(kWarp));
     });
     e = info[dev].err;
   }
@@ -198,9 +224,9 @@ int launch_decode_dim(attn::DecParams& p, const DecPlan& pl, const void* k, cons
   // behind the many-row kernel of a shared prefix it may start early
   auto kern = attn::attn_decode_kernel<D, kF8, kN, kWarp>;
   if (p.many.tiles > 0)
-    e = launch_behind(kern, dim3(pl.grid), attn::kDecThreads, attn::kDecSmem, s, mk, mv, p);
+    e = launch_behind(kern, dim3(pl.grid), attn::kDecThreads, attn::dec_smem(kWarp), s, mk, mv, p);
   else
-    kern<<<pl.grid, attn::kDecThreads, attn::kDecSmem, s>>>(mk, mv, p);
+    kern<<<pl.grid, attn::kDecThreads, attn::dec_smem(kWarp), s>>>(mk, mv, p);
   if (e == cudaSuccess && pl.join)
     e = launch_behind(attn::attn_decode_join_kernel<D>,
                       dim3((unsigned)((long long)p.B * p.Hkv * p.row_blocks), (unsigned)((pl.unit_rows + 3) / 4)),
@@ -355,6 +381,9 @@ void launch_rows_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   if (f8)
     attn::attn_fwd_rows_sm100<D, true>
         <<<grid, attn::RowsCfg<true>::kThreads, attn::RowsSmem<D, true>::kAlloc, s>>>(mq, mk, mv, mo, p);
+  else if (p.behind)
+    launch_behind(attn::attn_fwd_rows_sm100<D, false>, dim3(grid), attn::RowsCfg<false>::kThreads,
+                  attn::RowsSmem<D, false>::kAlloc, s, mq, mk, mv, mo, p);
   else
     attn::attn_fwd_rows_sm100<D, false>
         <<<grid, attn::RowsCfg<false>::kThreads, attn::RowsSmem<D, false>::kAlloc, s>>>(mq, mk, mv, mo, p);
@@ -424,8 +453,9 @@ int launch_rows(attn::RowsParams& p, const RowsPlan& pl, const void* q, const vo
     while (p.page % p.box != 0) p.box /= 2;
   const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)p.page, (cuuint64_t)p.num_pages * (cuuint64_t)p.Hkv};
   const cuuint32_t kb[3] = {(cuuint32_t)(f8 ? D : 64), (cuuint32_t)p.box, 1};
-  if ((st = encode_rows_map(&mk, k, 3, kd, kb, f8 ? 1 : 2, !f8)) != ATTN_OK) return st;
-  if ((st = encode_rows_map(&mv, v, 3, kd, kb, f8 ? 1 : 2, !f8)) != ATTN_OK) return st;
+  const bool swizzle = !f8 || D == 128;   // (raw E4M3 tiles: as the converters read them)
+  if ((st = encode_rows_map(&mk, k, 3, kd, kb, f8 ? 1 : 2, swizzle)) != ATTN_OK) return st;
+  if ((st = encode_rows_map(&mv, v, 3, kd, kb, f8 ? 1 : 2, swizzle)) != ATTN_OK) return st;
   if (!prefix && (st = encode_map_o(&mo, o, (long long)p.B * p.Hkv, p.GT, D)) != ATTN_OK) return st;
   const bool join = !prefix && pl.grid > 1;
   switch (D) {
@@ -443,17 +473,25 @@ constexpr int kFewRows = 32;
 // Shared prefix: the plans of its two kernels, and the workspace's layout (decode's part first).
 struct PrefixPlan {
   bool here;        // the decode kernel computes the prefix too
+  size_t wide;      // bytes of the prefix's keys, and of its values, as bf16 (0: converted in the kernel)
   DecPlan dec;
   RowsPlan rows;
-  size_t bytes() const { return dec.bytes() + rows.bytes(); }
+  size_t bytes() const { return dec.bytes() + rows.bytes() + 2 * wide; }
 };
 
+// An E4M3 prefix is converted to bf16 once, ahead, where at least this many 128-row tiles of each head
+// would convert it themselves and the copy is no larger than this.
+constexpr int kWideTiles = 4;
+constexpr size_t kWideBytes = (size_t)256 << 20;
+
 PrefixPlan prefix_plan(int B, int Hkv, long long GT, int D, int page, int max_pages, long long prefix_len,
-                       int num_sms) {
+                       int num_sms, bool f8) {
   PrefixPlan pl;
   pl.here = prefix_len > 0 && (long long)B * GT <= kFewRows;
   pl.dec = dec_plan(B, Hkv, GT, D, cache_cap(page, max_pages), num_sms, true, pl.here, prefix_len);
   if (prefix_len > 0 && !pl.here) pl.rows = rows_plan(B, Hkv, GT, D, prefix_len, num_sms, true);
+  const size_t wide = ((size_t)Hkv * (size_t)prefix_len * D * 2 + 255) / 256 * 256;
+  pl.wide = f8 && !pl.here && pl.rows.tiles >= kWideTiles && 2 * wide <= kWideBytes ? wide : 0;
   return pl;
 }
 
@@ -527,28 +565,7 @@ int attn_cache_read(const void* k_cache, const void* v_cache, const void* k_scal
   if (!k || !v) return ATTN_ERR_INVALID_ARG;
   if ((st = cache_pointer_checks(a)) != ATTN_OK) return st;
   if (!aligned(k, 16) || !aligned(v, 16)) return ATTN_ERR_MISALIGNED;
-  const unsigned long long items = (unsigned long long)B * Hkv * N * (D / 8);
-  const bool many = items >= (1u << 20);   // two items a thread where that still fills the GPU
-  const unsigned grid = (unsigned)((items + (many ? 511 : 255)) / (many ? 512 : 256));
-  const attn::CacheView c = cache_view(a);
-  const auto kb = reinterpret_cast<__nv_bfloat16*>(k);
-  const auto vb = reinterpret_cast<__nv_bfloat16*>(v);
-  const attn::FastDiv dn = attn::make_fast_div((uint32_t)N), dh = attn::make_fast_div((uint32_t)Hkv);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto go = [&](auto kern) { kern<<<grid, 256, 0, s>>>(c, kb, vb, N, dn, dh, items); };
-  auto pick = [&](auto dim) {
-    constexpr int D_ = decltype(dim)::value;
-    if (k_scale != nullptr)
-      many ? go(attn::attn_cache_read_kernel<D_, true, 2>) : go(attn::attn_cache_read_kernel<D_, true, 1>);
-    else
-      many ? go(attn::attn_cache_read_kernel<D_, false, 2>) : go(attn::attn_cache_read_kernel<D_, false, 1>);
-  };
-  switch (D) {
-    case 32: pick(std::integral_constant<int, 32>()); break;
-    case 64: pick(std::integral_constant<int, 64>()); break;
-    case 96: pick(std::integral_constant<int, 96>()); break;
-    default: pick(std::integral_constant<int, 128>()); break;
-  }
+  launch_cache_read(cache_view(a), k_scale != nullptr, k, v, B, N, D, reinterpret_cast<cudaStream_t>(stream));
   return launch_status("cache read kernel launch");
 }
 
@@ -584,14 +601,14 @@ int attn_fwd_decode(const void* q, const void* k_cache, const void* v_cache, con
 }
 
 long long attn_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int T, int D, int page_size, int max_pages,
-                                                 int prefix_len) {
+                                                 int prefix_len, int e4m3) {
   const CacheArgs a{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, B, Hkv, D, 1, page_size, max_pages};
   long long GT = 0;
   if (prefix_len < 0 || decode_size_checks(a, Hq, T, 1.f, &GT) != ATTN_OK) return -1;
   if (B == 0 || T == 0) return 0;
   int num_sms = 0;
   if (sm_count(&num_sms) != ATTN_OK) return -1;
-  return (long long)prefix_plan(B, Hkv, GT, D, page_size, max_pages, prefix_len, num_sms).bytes();
+  return (long long)prefix_plan(B, Hkv, GT, D, page_size, max_pages, prefix_len, num_sms, e4m3 != 0).bytes();
 }
 
 int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
@@ -611,7 +628,7 @@ int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cac
     return ATTN_ERR_MISALIGNED;
   int num_sms = 0;
   if ((st = sm_count(&num_sms)) != ATTN_OK) return st;
-  const PrefixPlan pl = prefix_plan(B, Hkv, GT, D, page_size, max_pages, prefix_len, num_sms);
+  const PrefixPlan pl = prefix_plan(B, Hkv, GT, D, page_size, max_pages, prefix_len, num_sms, k_scale != nullptr);
   if (pl.bytes() > workspace_bytes || (pl.bytes() > 0 && !workspace)) return ATTN_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   attn::DecParams p;
@@ -632,8 +649,27 @@ int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cac
     r.num_pages = num_pages;
     r.ks = p.ks;
     r.vs = p.vs;
+    // (every part of the workspace is a multiple of 256 bytes)
     char* w = static_cast<char*>(workspace) + pl.dec.bytes();
-    if ((st = launch_rows(r, pl.rows, q, k_cache, v_cache, o, D, true, scale, w, s)) != ATTN_OK) return st;
+    const void *kp = k_cache, *vp = v_cache;
+    if (pl.wide) {
+      char* wide = w + pl.rows.bytes();
+      attn::CacheView c = cache_view(a);
+      c.table = prefix_table;
+      c.lens = nullptr;
+      c.len_all = prefix_len;
+      c.max_pages = (prefix_len + page_size - 1) / page_size;
+      launch_cache_read(c, true, wide, wide + pl.wide, 1, prefix_len, D, s);
+      if ((st = launch_status("prefix conversion launch")) != ATTN_OK) return st;
+      kp = wide;
+      vp = wide + pl.wide;
+      r.behind = 1;
+      r.table = nullptr;
+      r.page = prefix_len;
+      r.num_pages = 1;
+      r.ks = r.vs = nullptr;
+    }
+    if ((st = launch_rows(r, pl.rows, q, kp, vp, o, D, true, scale, w, s)) != ATTN_OK) return st;
     p.many.o = r.slot_o;
     p.many.ml = r.slot_ml;
     p.many.tiles = r.tiles;
