@@ -37,7 +37,7 @@
 //    usual step needs one vote and no shuffle, and O is rarely rescaled.
 //
 // Schedule.  The work is counted in blocks of 64 keys of one (sequence, KV head, row block) unit,
-// all units in one line.  Each of the grid's CTAs takes an equal, contiguous range of that line,
+// and two more for each unit, all in one line.  Each of the grid's CTAs takes an equal, contiguous range of that line,
 // found from the lengths on the device, so uneven batches stay balanced and a captured launch serves
 // any lengths.  A range covers whole units (written out directly) and at most two partial ones
 // (written as unnormalised O, maximum and sum in fp32 to the CTA's two slots of the workspace); a
@@ -91,7 +91,7 @@ struct DecParams {
   const int* prefix_table;
   int prefix_len, prefix_row_blocks;
   int whole_units;           // 1: units are not split (each stands in the line as one block)
-  int min_share;             // blocks a CTA takes at least
+  int min_share;             // places a CTA takes at least
   float c;                   // scale * log2(e)
   __nv_bfloat16* o;          // [B][Hkv][GT][D]
   float* lse;                // [B][Hkv][GT]
@@ -102,11 +102,12 @@ struct DecParams {
   float* area_o[2];
   float2* area_ml[2];
   // the prefix's results from the many-row kernel (tiles > 0): slots of 128 rows, two a CTA for parts of
-  // units and then a unit's own; a unit is a tile of a head, of `blocks` blocks
+  // units and then a unit's own; a unit is a tile of a head, of `places` places in that kernel's line, the
+  // first `over` of them without blocks
   struct {
     const float* o;
     const float2* ml;
-    int tiles, seqs, seq_tiles, blocks;
+    int tiles, seqs, seq_tiles, places, over;
     long long share, ctas;
   } many;
 };
@@ -156,21 +157,27 @@ __device__ __forceinline__ DecParts dec_prefix_parts(const DecParams& p, int b, 
   DecParts r;
   const int tile = p.many.seq_tiles > 1 ? b * p.many.seq_tiles + i / 128 : b / p.many.seqs;
   r.row = p.many.seq_tiles > 1 ? i % 128 : b % p.many.seqs * p.GT + i;
-  const long long unit = (long long)h * p.many.tiles + tile, u0 = unit * p.many.blocks;
-  r.f = u0 / p.many.share;
-  const long long e = (u0 + p.many.blocks - 1) / p.many.share;
+  const long long unit = (long long)h * p.many.tiles + tile, u0 = unit * p.many.places;
+  r.f = (u0 + p.many.over) / p.many.share;
+  const long long e = (u0 + p.many.places - 1) / p.many.share;
   r.n = (int)(e - r.f) + 1;
   r.whole = r.n == 1 ? 2 * p.many.ctas + unit : -1;
-  r.first_slot = 2 * r.f + (u0 != r.f * p.many.share ? 1 : 0);
+  r.first_slot = 2 * r.f + (u0 > r.f * p.many.share ? 1 : 0);
   return r;
 }
 
-// The line of blocks: the prefix's first, then sequence by sequence; within a sequence KV head by
-// KV head, row block by row block.
+// The line of work: the prefix's units first, then sequence by sequence; within a sequence KV head by
+// KV head, row block by row block.  A unit takes kDecOver places for its start and end (about 4 us of
+// a CTA, a block 1.3 us at full load), then one for each of its blocks.
+constexpr int kDecOver = 2;
+__device__ __forceinline__ int dec_places(int blocks) { return blocks + kDecOver; }
+// Blocks of a unit before place `p` of it.
+__device__ __forceinline__ int dec_block_at(int p) { return p > kDecOver ? p - kDecOver : 0; }
+
 struct DecLine {
-  long long prefix;   // blocks of the prefix's units together
+  long long prefix;   // places of the prefix's units together
   long long total;
-  long long share;    // blocks of a CTA
+  long long share;    // places of a CTA
 };
 
 // Whole block (kDecThreads threads): the line's length, and the sequence that holds position `x`
@@ -183,7 +190,7 @@ __device__ __forceinline__ DecLine dec_locate(const DecParams& p, unsigned ctas,
   const int per = (p.B + kDecThreads - 1) / kDecThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += dec_blocks(p, dec_len(p, b));
+  for (int b = b0; b < b1; ++b) mine += dec_places(dec_blocks(p, dec_len(p, b)));
   mine *= per_seq;
   long long incl = mine;
 #pragma unroll
@@ -194,7 +201,8 @@ __device__ __forceinline__ DecLine dec_locate(const DecParams& p, unsigned ctas,
   if (lane == 31) sh[warp] = incl;
   __syncthreads();
   DecLine ln;
-  ln.prefix = p.prefix_len > 0 ? (long long)p.Hkv * p.prefix_row_blocks * ((p.prefix_len + kDecBlock - 1) / kDecBlock) : 0;
+  ln.prefix = p.prefix_len > 0 ? (long long)p.Hkv * p.prefix_row_blocks * dec_places((p.prefix_len + kDecBlock - 1) / kDecBlock)
+                               : 0;
   long long before = ln.prefix, total = ln.prefix;
 #pragma unroll
   for (int w = 0; w < kDecThreads / 32; ++w) {
@@ -208,7 +216,7 @@ __device__ __forceinline__ DecLine dec_locate(const DecParams& p, unsigned ctas,
   if (find_seq >= 0 ? (find_seq >= b0 && find_seq < b1) : (x >= at && x < at + mine)) {
     int b = b0;
     for (; b < b1; ++b) {
-      const long long n = per_seq * dec_blocks(p, dec_len(p, b));
+      const long long n = per_seq * dec_places(dec_blocks(p, dec_len(p, b)));
       if (find_seq >= 0 ? b == find_seq : x < at + n) break;
       at += n;
     }
@@ -447,9 +455,24 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
     const int nblk = kWarp ? 1 : prefix ? (len + kDecBlock - 1) / kDecBlock : dec_blocks(p, len);
     const int row_blocks = prefix ? p.prefix_row_blocks : p.row_blocks;
     const int rows = prefix ? p.B * p.GT : p.GT;
-    const int unit = kWarp ? 0 : (int)((x - first) / nblk);
-    const int blk0 = kWarp ? 0 : (int)((x - first) - (long long)unit * nblk);
-    const int blk1 = kWarp ? 1 : (int)min((long long)nblk, blk0 + (end - x));
+    const int places = dec_places(nblk);
+    const int unit = kWarp ? 0 : (int)((x - first) / places);
+    const int p0 = kWarp ? 0 : (int)((x - first) - (long long)unit * places);
+    const int p1 = kWarp ? 1 : (int)min((long long)places, p0 + (end - x));
+    const int blk0 = kWarp ? 0 : dec_block_at(p0), blk1 = kWarp ? 1 : dec_block_at(p1);
+    // the next unit of the line
+    auto move_on = [&](int row_blocks_) {
+      x += p1 - p0;
+      const long long seq_places = (long long)p.Hkv * row_blocks_ * places;
+      if (x >= first + seq_places) {
+        first += seq_places;
+        ++seq;
+      }
+    };
+    if (!kWarp && blk0 == blk1) {   // only places of its start: the next CTA has the unit
+      move_on(row_blocks);
+      continue;
+    }
     const int h = kWarp ? (int)(x - (long long)seq * p.Hkv) : unit / row_blocks, rb = kWarp ? 0 : unit - h * row_blocks;
     const int* table = prefix ? p.prefix_table : (p.table ? p.table + (size_t)seq * p.max_pages : nullptr);
     const int i0 = (rb * row_tiles + rt) * kTile;   // first row of this warp's tile
@@ -611,28 +634,45 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       if (active) {
         const uint32_t tile_k = ring + stage * kDecStageBytes, tile_v = tile_k + Cfg::kVOff;
-        // S^T = K Q^T: keys g and g + 8 of each group, rows 2t and 2t + 1 of each tile
+        // S^T = K Q^T: keys g and g + 8 of each group, rows 2t and 2t + 1 of each tile.  Even and odd K
+        // steps add to sums of their own and the groups alternate: a lone chain of D / 16 products is
+        // most of a step's latency.
         float s[G][kN][4];
+        {
+          float odd[G][kN][4];
+          uint32_t ka[G][KW], kb[G][KW];
 #pragma unroll
-        for (int gr = 0; gr < G; ++gr) {
-          uint32_t ka[KW], kb[KW];
-          dec_load_k<D, kF8>(ka, tile_k, 16 * gr + g, t4);
-          dec_load_k<D, kF8>(kb, tile_k, 16 * gr + 8 + g, t4);
+          for (int gr = 0; gr < G; ++gr) {
+            dec_load_k<D, kF8>(ka[gr], tile_k, 16 * gr + g, t4);
+            dec_load_k<D, kF8>(kb[gr], tile_k, 16 * gr + 8 + g, t4);
 #pragma unroll
-          for (int nt = 0; nt < kN; ++nt) s[gr][nt][0] = s[gr][nt][1] = s[gr][nt][2] = s[gr][nt][3] = 0.f;
+            for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
-          for (int q = 0; q < D / 16; ++q) {
-            if constexpr (kF8) {
-              const uint32_t a[4] = {e4m3_lo_to_f16(ka[q]), e4m3_lo_to_f16(kb[q]), e4m3_hi_to_f16(ka[q]),
-                                     e4m3_hi_to_f16(kb[q])};
-#pragma unroll
-              for (int nt = 0; nt < kN; ++nt) mma_16816_f16(s[gr][nt], a, qw[nt][2 * q], qw[nt][2 * q + 1]);
-            } else {
-              const uint32_t a[4] = {ka[2 * q], kb[2 * q], ka[2 * q + 1], kb[2 * q + 1]};
-#pragma unroll
-              for (int nt = 0; nt < kN; ++nt) mma_16816(s[gr][nt], a, qw[nt][2 * q], qw[nt][2 * q + 1]);
-            }
+              for (int e = 0; e < 4; ++e) s[gr][nt][e] = odd[gr][nt][e] = 0.f;
           }
+#pragma unroll
+          for (int q = 0; q < D / 16; ++q)
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr) {
+              if constexpr (kF8) {
+                const uint32_t a[4] = {e4m3_lo_to_f16(ka[gr][q]), e4m3_lo_to_f16(kb[gr][q]), e4m3_hi_to_f16(ka[gr][q]),
+                                       e4m3_hi_to_f16(kb[gr][q])};
+#pragma unroll
+                for (int nt = 0; nt < kN; ++nt)
+                  mma_16816_f16(q & 1 ? odd[gr][nt] : s[gr][nt], a, qw[nt][2 * q], qw[nt][2 * q + 1]);
+              } else {
+                const uint32_t a[4] = {ka[gr][2 * q], kb[gr][2 * q], ka[gr][2 * q + 1], kb[gr][2 * q + 1]};
+#pragma unroll
+                for (int nt = 0; nt < kN; ++nt)
+                  mma_16816(q & 1 ? odd[gr][nt] : s[gr][nt], a, qw[nt][2 * q], qw[nt][2 * q + 1]);
+              }
+            }
+#pragma unroll
+          for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+            for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[gr][nt][e] += odd[gr][nt][e];
         }
         int ev[G][2];   // E4M3: V exponents of keys g, g + 8
 #pragma unroll
@@ -989,13 +1029,7 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
     fence_proxy_async_smem();   // the next unit's copies follow these accesses
     __syncthreads();
 
-    // ---- the next unit
-    x += blk1 - blk0;
-    const long long seq_blocks = (long long)p.Hkv * row_blocks * nblk;
-    if (x >= first + seq_blocks) {
-      first += seq_blocks;
-      ++seq;
-    }
+    move_on(row_blocks);
   }
   if (!kWarp && p.many.tiles > 0) wait_for_previous();   // the joining kernel relies on the one before, too
   // Drain after a wait gave up: every issued copy lands before the CTA exits.
@@ -1024,10 +1058,10 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
   int seq;
   long long first;
   const DecLine ln = dec_locate(p, ctas, 0, b, scratch, seq, first);
-  const int nblk = dec_blocks(p, dec_len(p, b));
-  const long long u0 = first + (long long)hr * nblk, u1 = u0 + nblk;
+  const int places = dec_places(dec_blocks(p, dec_len(p, b)));
+  const long long u0 = first + (long long)hr * places, u1 = u0 + places;
   const bool shared = p.area_o[0] != nullptr;
-  if (!shared && u0 / ln.share == (u1 - 1) / ln.share) return;   // written by the one CTA that had it
+  if (!shared && (u0 + kDecOver) / ln.share == (u1 - 1) / ln.share) return;   // written by the one CTA that had it
   const int r = (int)blockIdx.y * 4 + warp, i = rb * p.unit_rows + r;
   if (r >= p.unit_rows || i >= p.GT) return;
   const long long row = ((long long)b * p.Hkv + h) * p.GT + i;
@@ -1067,19 +1101,19 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
   };
   // the parts [a0, a1) of the line, of a unit whose rows start at `slot_row`'s of a slot; whole: an area's row
   auto add_unit = [&](long long a0, long long a1, int part, int slot_row) {
-    const long long f = a0 / ln.share, e = (a1 - 1) / ln.share;
+    const long long f = (a0 + kDecOver) / ln.share, e = (a1 - 1) / ln.share;
     if (f == e)
       add(1, p.area_o[part], p.area_ml[part], [&](int) { return row; });
     else
       add((int)(e - f) + 1, p.slot_o, p.slot_ml, [&](int k) {
-        return (2 * (f + k) + ((k == 0 && a0 != f * ln.share) ? 1 : 0)) * p.unit_rows + slot_row;
+        return (2 * (f + k) + ((k == 0 && a0 > f * ln.share) ? 1 : 0)) * p.unit_rows + slot_row;
       });
   };
   if (p.prefix_len > 0) {   // few rows: computed by the same kernel
-    const int pre_nblk = (p.prefix_len + kDecBlock - 1) / kDecBlock;
+    const int pre = dec_places((p.prefix_len + kDecBlock - 1) / kDecBlock);
     const int pr = b * p.GT + i;
-    const long long a0 = ((long long)h * p.prefix_row_blocks + pr / p.unit_rows) * pre_nblk;
-    add_unit(a0, a0 + pre_nblk, 1, pr % p.unit_rows);
+    const long long a0 = ((long long)h * p.prefix_row_blocks + pr / p.unit_rows) * pre;
+    add_unit(a0, a0 + pre, 1, pr % p.unit_rows);
   }
   if (p.many.tiles > 0) {
     const DecParts pt = dec_prefix_parts(p, b, h, i);

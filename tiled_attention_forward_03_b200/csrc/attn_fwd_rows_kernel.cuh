@@ -16,7 +16,7 @@
 //    every other tile each, to bf16, exactly (a power-of-two scale rounds nothing), and store them as
 //    TMA would, 128-byte swizzled.  One conversion serves 128 rows and is hidden behind their
 //    exponentials (with one warpgroup it was not: 4100 clocks a block instead of 2100).
-//  * Work: as in the decode kernel, the 128-key blocks of all units stand in one line and each CTA
+//  * Work: as in the decode kernel, the units' 128-key blocks stand in one line and each CTA
 //    takes an equal, contiguous range of it, whatever the lengths; a range holds whole units and at
 //    most two parts of units, which go unnormalised, in fp32, to the CTA's two slots of the workspace
 //    and are joined by a second kernel.  (Dealing whole units out left the GPU a third idle for the
@@ -107,7 +107,7 @@ struct RowsParams {
   int seqs;                  // sequences in a tile (prefix; else 1)
   int seq_tiles;             // tiles of a sequence (prefix with GT > 128; else 1)
   int q_box_rows;            // rows a Q tile load fills
-  int min_share;             // blocks a CTA takes at least
+  int min_share;             // places a CTA takes at least
   const int* k_lens;         // [B] or null
   int len_all;               // keys where k_lens is null; no batch row has more
   // paged keys
@@ -133,11 +133,16 @@ static_assert(sizeof(RowsUnit) == 32, "queue entry");
 __device__ __forceinline__ int rows_len(const RowsParams& p, int b) {
   return p.k_lens != nullptr ? max(0, min(__ldg(p.k_lens + b), p.len_all)) : p.len_all;
 }
-__device__ __forceinline__ int rows_blocks(int len) {
-  return max(1, (int)(((long long)len + kBlockN - 1) / kBlockN));
-}
+__device__ __forceinline__ int rows_blocks(int len) { return (int)(((long long)len + kBlockN - 1) / kBlockN); }
 
-// The line of blocks: key group by key group (sequences and heads; heads for a prefix), tile by tile.
+// The line of work: key group by key group (sequences and heads; heads for a prefix), tile by tile; a
+// unit takes kRowsOver places for its start and end (2000 clocks, a block 1700 to 2000), then one for
+// each of its blocks.  Batch rows without keys have no place.
+constexpr int kRowsOver = 1;
+__host__ __device__ __forceinline__ int rows_places(int blocks) { return blocks > 0 ? blocks + kRowsOver : 0; }
+// Blocks of a unit before place `p` of it.
+__host__ __device__ __forceinline__ int rows_block_at(int p) { return p > kRowsOver ? p - kRowsOver : 0; }
+
 struct RowsLine {
   long long total, share;
 };
@@ -151,7 +156,7 @@ __device__ __forceinline__ RowsLine rows_locate(const RowsParams& p, unsigned ct
   RowsLine ln;
   const int n = p.prefix ? 1 : p.B;
   long long total = 0;
-  for (int c = 0; c < n; c += 32) total += c + lane < n ? rows_blocks(rows_len(p, c + lane)) : 0;
+  for (int c = 0; c < n; c += 32) total += c + lane < n ? rows_places(rows_blocks(rows_len(p, c + lane))) : 0;
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
   ln.total = total * per_seq;
@@ -161,7 +166,7 @@ __device__ __forceinline__ RowsLine rows_locate(const RowsParams& p, unsigned ct
   first = ln.total;
   long long at = 0;
   for (int c = 0; c < n; c += 32) {
-    const long long mine = c + lane < n ? per_seq * rows_blocks(rows_len(p, c + lane)) : 0;
+    const long long mine = c + lane < n ? per_seq * rows_places(rows_blocks(rows_len(p, c + lane))) : 0;
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -370,46 +375,52 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
       mbar_arrive(&u_full[q]);
       ++ord;
     };
-    // Twice over the range: the units with keys to the ring (one lane), then zeros for those without
-    // (the whole warp, while the last units are computed).
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      int seq = b;
-      long long at = first;
+    // The units of the range to the ring (one lane).
+    if (lane == 0) {
       for (long long x = begin; x < end && ok;) {
         RowsUnit w;
-        w.len = rows_len(p, seq);
-        const int nblk = rows_blocks(w.len);
-        const int unit = (int)((x - at) / nblk);
-        const int blk0 = (int)((x - at) - (long long)unit * nblk);
-        const int blk1 = (int)min((long long)nblk, blk0 + (end - x));
-        const int h = unit / p.tiles;
-        rows_tile(p, seq, h, unit - h * p.tiles, w);
-        if (pass == 0 && w.len > 0 && lane == 0) {
-          const bool whole = blk0 == 0 && blk1 == nblk;
-          w.jb = blk0;
-          w.je = blk1;
-          w.slot = !whole ? 2 * (int)blockIdx.x + (x == begin ? 0 : 1) : p.prefix ? 2 * (int)gridDim.x + unit : -1;
-          put(w);
+        w.len = rows_len(p, b);
+        const int nblk = rows_blocks(w.len), n = rows_places(nblk);
+        if (n == 0) {
+          ++b;
+          continue;
         }
-        if (pass == 1 && w.len == 0) {
-          const int n = min(kBlockM, p.GT - w.i0);   // (cross attention: a tile's rows are contiguous)
-          const long long row = ((long long)seq * p.Hkv + h) * p.GT + w.i0;
+        const int unit = (int)((x - first) / n);
+        const int p0 = (int)((x - first) - (long long)unit * n);
+        const int p1 = (int)min((long long)n, p0 + (end - x));
+        const int h = unit / p.tiles;
+        rows_tile(p, b, h, unit - h * p.tiles, w);
+        w.jb = rows_block_at(p0);
+        w.je = rows_block_at(p1);
+        const bool whole = w.jb == 0 && w.je == nblk;
+        w.slot = !whole ? 2 * (int)blockIdx.x + (x == begin ? 0 : 1) : p.prefix ? 2 * (int)gridDim.x + unit : -1;
+        if (w.jb < w.je) put(w);
+        x += p1 - p0;
+        if (x >= first + per_seq * n) {
+          first += per_seq * n;
+          ++b;
+        }
+      }
+      if (ok) {
+        RowsUnit w{};
+        w.je = -1;
+        put(w);
+      }
+    }
+    __syncwarp();
+    // Zeros for the tiles of batch rows without keys (the whole warp, while the last units are
+    // computed), dealt out to all CTAs.
+    if (!p.prefix) {
+      for (int seq = 0; seq < p.B; ++seq) {
+        if (rows_len(p, seq) > 0) continue;
+        for (long long u = blockIdx.x; u < per_seq; u += gridDim.x) {
+          const int h = (int)(u / p.tiles), i0 = (int)(u - (long long)h * p.tiles) * kBlockM;
+          const int n = min(kBlockM, p.GT - i0);
+          const long long row = ((long long)seq * p.Hkv + h) * p.GT + i0;
           for (int i = lane; i < n * (D / 8); i += 32)
             reinterpret_cast<uint4*>(p.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
           for (int i = lane; i < n; i += 32) p.lse[row + i] = -INFINITY;
         }
-        x += blk1 - blk0;
-        if (x >= at + per_seq * nblk) {
-          at += per_seq * nblk;
-          ++seq;
-        }
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      if (pass == 0 && ok && lane == 0) {
-        RowsUnit w{};
-        w.je = -1;
-        put(w);
       }
     }
     __syncwarp();
@@ -963,18 +974,19 @@ __global__ void __launch_bounds__(256) attn_rows_join_kernel(const RowsParams p,
     RowsUnit w{};
     long long u0 = 0;
     if (x < ln.total) {
-      const int nblk = rows_blocks(rows_len(p, b));
-      const int unit = (int)((x - first) / nblk);
-      u0 = first + (long long)unit * nblk;
-      if (u0 != x && u0 / ln.share == c) {   // split here, and not before
-        n = (int)((u0 + nblk - 1) / ln.share - c) + 1;
+      const int places = rows_places(rows_blocks(rows_len(p, b)));
+      const int unit = (int)((x - first) / places);
+      u0 = first + (long long)unit * places;
+      // split here (the unit's first block is before x, in range c), and not before
+      if (u0 + kRowsOver < x && (u0 + kRowsOver) / ln.share == c) {
+        n = (int)((u0 + places - 1) / ln.share - c) + 1;
         const int h = unit / p.tiles;
         rows_tile(p, b, h, unit - h * p.tiles, w);
       }
     }
     if (lane == 0) {
       unit_s[0] = make_int4(w.b0, w.i0, w.h, n);
-      place_s[0] = 2 * c + (u0 != c * ln.share ? 1 : 0);
+      place_s[0] = 2 * c + (u0 > c * ln.share ? 1 : 0);
     }
   }
   __syncthreads();

@@ -144,7 +144,7 @@ struct DecPlan {
   size_t bytes() const { return slot_o + slot_ml + 2 * (area_o + area_ml); }
 };
 
-constexpr int kDecMinShare = 2;     // blocks of 64 keys
+constexpr int kDecMinShare = 4;     // places of the line: a unit's two, and 64-key blocks
 constexpr int kDecCtasPerSm = 3, kDecWarpCtasPerSm = 2;   // resident CTAs (the kernel's launch bounds)
 // Warps take whole units where no sequence has more than this many blocks, and there are units for
 // all CTAs (or sequences are so short that there is nothing to share).  Measured on B200: at the end of
@@ -170,11 +170,11 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   pl.warps = !prefix_here && pl.row_tiles == 1 &&
              (cap_blocks <= kDecTinyBlocks || (cap_blocks <= kDecShortBlocks && units >= ctas));
   pl.whole_units = pl.warps || (!shared && cap_blocks <= kDecWholeBlocks) ? 1 : 0;
-  double blocks = (double)units * (double)cap_blocks;
+  double blocks = (double)units * (double)(cap_blocks + 2);   // places of the line, at most
   if (prefix_here) {
     const long long rows = (long long)B * GT;
     pl.prefix_row_blocks = (int)((rows + pl.unit_rows - 1) / pl.unit_rows);
-    blocks += (double)Hkv * pl.prefix_row_blocks * (double)pre_blocks;
+    blocks += (double)Hkv * pl.prefix_row_blocks * (double)(pre_blocks + 2);
   }
   const double most = pl.warps ? (double)((units + 3) / 4) : pl.whole_units ? (double)units : blocks / kDecMinShare + 1;
   const long long resident = pl.warps ? (long long)kDecWarpCtasPerSm * num_sms : ctas;
@@ -246,7 +246,7 @@ int launch_decode(attn::DecParams& p, const DecPlan& pl, const void* k, const vo
   p.row_blocks = pl.row_blocks;
   p.prefix_row_blocks = pl.prefix_row_blocks;
   p.whole_units = pl.whole_units;
-  p.min_share = pl.whole_units ? 1 : kDecMinShare;
+  p.min_share = pl.whole_units ? 3 : kDecMinShare;
   p.unit_rows = pl.unit_rows;
   char* w = static_cast<char*>(workspace);
   p.slot_o = reinterpret_cast<float*>(w);
@@ -390,7 +390,7 @@ void launch_rows_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtenso
   if (join) launch_behind(attn::attn_rows_join_kernel<D>, dim3(grid - 1, attn::kBlockM / 32), 256, 0, s, p, grid);
 }
 
-constexpr int kRowsMinShare = 2;   // blocks of 128 keys
+constexpr int kRowsMinShare = 3;   // places of the line: a unit's one, and 128-key blocks
 
 // The tiles of a problem, the grid and the workspace.
 struct RowsPlan {
@@ -415,7 +415,7 @@ RowsPlan rows_plan(int B, int Hkv, long long GT, int D, long long max_len, int n
     pl.tiles = (int)(B * per_seq);
   }
   const long long units = (long long)(prefix ? Hkv : (long long)B * Hkv) * pl.tiles;
-  const double most = (double)units * (double)pl.blocks / kRowsMinShare + 1;
+  const double most = (double)units * (double)(pl.blocks + 1) / kRowsMinShare + 1;
   pl.grid = most < (double)num_sms ? (unsigned)most : (unsigned)num_sms;
   const size_t slots = 2 * (size_t)pl.grid + (prefix ? (size_t)units : 0);
   pl.slot_o = slots * attn::kBlockM * D * sizeof(float);
@@ -675,9 +675,10 @@ int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cac
     p.many.tiles = r.tiles;
     p.many.seqs = r.seqs;
     p.many.seq_tiles = r.seq_tiles;
-    p.many.blocks = (int)pl.rows.blocks;
+    p.many.places = attn::rows_places((int)pl.rows.blocks);
+    p.many.over = attn::kRowsOver;
     p.many.ctas = pl.rows.grid;
-    const long long total = (long long)Hkv * r.tiles * pl.rows.blocks;
+    const long long total = (long long)Hkv * r.tiles * p.many.places;
     p.many.share = (total + p.many.ctas - 1) / p.many.ctas;
     if (p.many.share < kRowsMinShare) p.many.share = kRowsMinShare;
   }
