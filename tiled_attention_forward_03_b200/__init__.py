@@ -844,7 +844,7 @@ class _On:
     def __enter__(self):
         import torch
 
-        self.before = torch.cuda.current_device()
+        self.before = torch._C._cuda_getDevice()   # (a tensor of the device exists: CUDA is initialised)
         if self.before != self.index:
             torch.cuda.set_device(self.index)
 
@@ -877,7 +877,8 @@ def _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, device):
     if not k_cache.is_cuda:
         raise ValueError("k_cache must be a CUDA tensor")
     shape = k_cache.shape
-    _expect(k_cache, "k_cache", k_cache.dtype, shape, device)
+    if k_cache.device != device or not k_cache.is_contiguous():
+        _expect(k_cache, "k_cache", k_cache.dtype, shape, device)
     _expect(v_cache, "v_cache", k_cache.dtype, shape, device)
     if f8:
         _expect(k_scale, "k_scale", torch.float8_e8m0fnu, shape[:3], device)
@@ -932,11 +933,11 @@ def cache_read(k_cache, v_cache, block_table, lens, N: int, k_scale=None, v_scal
     s = _raw_stream(stream, dev)
     shape = (B, Hkv, N, D)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        k_out = torch.empty(*shape, dtype=torch.bfloat16, device=dev)
     else:
         _expect(k_out, "k_out", torch.bfloat16, shape, dev)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        v_out = torch.empty(*shape, dtype=torch.bfloat16, device=dev)
     else:
         _expect(v_out, "v_out", torch.bfloat16, shape, dev)
     with _On(dev):
@@ -961,7 +962,7 @@ def _decode_outputs(q, Hkv, B, D, out, lse):
     else:
         _expect(out, "out", torch.bfloat16, shape, dev)
     if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+        lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev)
     else:
         _expect(lse, "lse", torch.float32, (B, Hq, T), dev)
     return Hq, T, out, lse
@@ -1054,7 +1055,7 @@ def forward_cross(q, k, v, k_lens=None, scale: float | None = None, out=None, ls
     else:
         _expect(out, "out", torch.bfloat16, (B, Hq, Nq, D), dev)
     if lse is None:
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=dev)
+        lse = torch.empty(B, Hq, Nq, dtype=torch.float32, device=dev)
     else:
         _expect(lse, "lse", torch.float32, (B, Hq, Nq), dev)
     if scale is None:

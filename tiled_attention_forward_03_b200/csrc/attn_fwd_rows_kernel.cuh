@@ -957,12 +957,13 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
 }
 
 // Cross attention: joins the parts of every unit that was split, in key order, into O and LSE.  Block
-// (c, y): the unit at the end of CTA c's range, where its first part is in that range; a warp a row,
-// 32 rows a block, in turns of eight.
+// (c, y): the unit at the end of CTA c's range, where its first part is in that range; 32 rows a block,
+// four a warp, whose loads stand side by side (one row after another, most of the kernel's 13 us for
+// 9 MB was the chain of their latencies).
 template <int D>
 __global__ void __launch_bounds__(256) attn_rows_join_kernel(const RowsParams p, unsigned ctas) {
-  __shared__ int4 unit_s[2];
-  __shared__ long long place_s[2];
+  __shared__ int4 unit_s;
+  __shared__ long long place_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     int b;
@@ -985,52 +986,70 @@ __global__ void __launch_bounds__(256) attn_rows_join_kernel(const RowsParams p,
       }
     }
     if (lane == 0) {
-      unit_s[0] = make_int4(w.b0, w.i0, w.h, n);
-      place_s[0] = 2 * c + (u0 > c * ln.share ? 1 : 0);
+      unit_s = make_int4(w.b0, w.i0, w.h, n);
+      place_s = 2 * c + (u0 > c * ln.share ? 1 : 0);
     }
   }
   __syncthreads();
-  const int4 unit = unit_s[0];
-  const long long first_slot = place_s[0], c0 = blockIdx.x;
+  const int4 unit = unit_s;
+  const long long first_slot = place_s, c0 = blockIdx.x;
   const int n = unit.w;
   if (n == 0) return;
+  // rows r0 + 8 i of the unit (those that are none come last); lane (i, k): part k of row i
+  const int r0 = blockIdx.y * 32 + warp, part = lane & 7;
+  long long row[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) row[i] = rows_index(p, unit.x, unit.y, unit.z, r0 + 8 * i);
+  if (row[0] < 0) return;
   wait_for_previous();
-  for (int r = blockIdx.y * 32 + warp; r < (int)blockIdx.y * 32 + 32; r += 8) {
-    const long long row = rows_index(p, unit.x, unit.y, unit.z, r);
-    if (row < 0) return;   // (rows that are none come last)
-    float m = -INFINITY, l = 0.f;
-    float acc[D / 32];
+  float m = -INFINITY, l = 0.f;   // of row lane / 8
+  float acc[4][D / 32];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      const bool mine = k0 + lane < n;
-      const long long place = (k0 + lane == 0 ? first_slot : 2 * (c0 + k0 + lane)) * kBlockM + r;
-      const float2 ml = mine ? p.slot_ml[place] : make_float2(-INFINITY, 0.f);
-      float mn = ml.x;
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
-      mn = fmaxf(m, mn);
-      const float a = dec_weight(make_float2(m, l), mn), w = dec_weight(ml, mn);
-      float sum = ml.y * w;
+    for (int e = 0; e < D / 32; ++e) acc[i][e] = 0.f;
+  auto slot_row = [&](int k) { return (k == 0 ? first_slot : 2 * (c0 + k)) * kBlockM + r0; };   // of row 0
+  for (int k0 = 0; k0 < n; k0 += 8) {
+    const float2 ml = k0 + part < n ? p.slot_ml[slot_row(k0 + part) + 8 * (lane >> 3)] : make_float2(-INFINITY, 0.f);
+    float mn = ml.x;
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      m = mn;
-      l = fmaf(l, a, sum);
+    for (int d = 4; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+    mn = fmaxf(m, mn);
+    const float a = dec_weight(make_float2(m, l), mn), w = dec_weight(ml, mn);
+    float sum = ml.y * w;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) acc[i] *= a;
-      const int here = min(32, n - k0);
-#pragma unroll 4
-      for (int k = 0; k < here; ++k) {
-        const float wk = __shfl_sync(0xffffffffu, w, k);
-        const long long pk = __shfl_sync(0xffffffffu, place, k);
+    for (int d = 4; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    m = mn;
+    l = fmaf(l, a, sum);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(p.slot_o[pk * D + 32 * i + lane], wk, acc[i]);
+    for (int i = 0; i < 4; ++i) {
+      const float ai = __shfl_sync(0xffffffffu, a, 8 * i);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[i][e] *= ai;
+    }
+    const int here = min(8, n - k0);
+#pragma unroll 2
+    for (int k = 0; k < here; ++k) {
+      const float* o = p.slot_o + slot_row(k0 + k) * D + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float wk = __shfl_sync(0xffffffffu, w, 8 * i + k);
+        if (row[i] >= 0)
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) acc[i][e] = fmaf(o[8 * i * D + 32 * e], wk, acc[i][e]);
       }
     }
-    const float inv = 1.f / l;
+  }
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) p.o[row * D + 32 * i + lane] = __float2bfloat16_rn(acc[i] * inv);
-    if (lane == 0) p.lse[row] = dec_lse(m, l);
+  for (int i = 0; i < 4; ++i) {
+    const float inv = 1.f / __shfl_sync(0xffffffffu, l, 8 * i);
+    if (row[i] < 0) continue;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) p.o[row[i] * D + 32 * e + lane] = __float2bfloat16_rn(acc[i][e] * inv);
+  }
+  if (part == 0) {
+    const long long mine = rows_index(p, unit.x, unit.y, unit.z, r0 + 8 * (lane >> 3));
+    if (mine >= 0) p.lse[mine] = dec_lse(m, l);
   }
 }
 
