@@ -390,7 +390,8 @@ int attn_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* ls
  *   num_pages >= 1, max_pages >= 0, num_pages * Hkv <= 2^31-1.
  * Tables and lengths are read on the device when the kernels run, so captured calls see their
  * values at replay.  A table entry outside [0, num_pages) is no page: nothing is written there, and
- * it reads as zeros.  Host checks and errors as in attn_fwd: ATTN_ERR_INVALID_ARG (null pointers,
+ * it reads as zeros.  E4M3 caches: what attn_cache_append never writes (NaN codes; exponent bytes below
+ * 7 or in 248..254) may count as any value in the results of the rows that see it.  Host checks and errors as in attn_fwd: ATTN_ERR_INVALID_ARG (null pointers,
  * negative sizes, one scale without the other), ATTN_ERR_MISALIGNED, ATTN_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------------------------ */
 
@@ -435,9 +436,13 @@ int attn_cache_read(const void* k_cache, const void* v_cache, const void* k_scal
  * Any T >= 0 (T == 0 or B == 0: ATTN_OK, nothing launched), made for few rows: a KV head's keys are
  * read once for each 64 of its T * Hq / Hkv rows.  Further limits (ATTN_ERR_UNSUPPORTED): fewer than
  * 2^31 rows a KV head over the batch, and as many 16-row tiles.
- * Numerics as attn_fwd (probabilities times the value's scale rounded to bf16).  E4M3 NaN codes,
- * which attn_cache_append never writes, count as +-480.  Deterministic; the split of a sequence
- * over the GPU, and with it the fp32 order of its sums, depends on all the batch's lengths.
+ * Numerics: scores, maxima and sums in fp32.  bf16: probabilities rounded to bf16.  E4M3: the codes
+ * are exact in f16; each query row is scaled by a power of two and rounded to f16 (nothing is lost
+ * down to 2^-27 of its largest element), and probabilities times 2^(their value's exponent) are
+ * rounded to f16.  Deterministic; the split of a sequence over the GPU, and with it the fp32 order of
+ * its sums, depends on all the batch's lengths.  Positions at and past lens[b] may hold anything.
+ * Those that a token of the call does not see but a later one does must hold finite values (their
+ * probability is 0, and 0 * infinity is NaN), as with attn_fwd's causal form.
  */
 int attn_fwd_decode(const void* q, const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
                     const int* block_table, const int* lens, void* o, float* lse, int B, int Hq, int Hkv, int T,
@@ -453,9 +458,11 @@ long long attn_fwd_decode_workspace_bytes(int B, int Hq, int Hkv, int T, int D, 
  *   prefix_len    positions of the prefix, >= 0; every row sees all of them.
  *   block_table, lens   each sequence's own positions, behind the prefix; seen as in attn_fwd_decode.
  * o and lse are those of the softmax over the prefix's and the row's own positions together.  The
- * prefix is read once for up to 128 rows of a KV head (B * T * Hq / Hkv of them).  All other
- * arguments, limits, errors and numerics as attn_fwd_decode; workspace of at least
- * attn_fwd_shared_prefix_workspace_bytes() bytes.
+ * prefix's keys of a KV head are read once for each 128 of the B * T * Hq / Hkv rows that see them, or
+ * once for all where those are few; an E4M3 prefix that many rows read is converted to bf16 in the
+ * workspace first, once.  All other arguments, limits, errors and numerics as attn_fwd_decode (where
+ * more than 32 rows see the prefix, its keys, values and probabilities are products of bf16);
+ * workspace of at least attn_fwd_shared_prefix_workspace_bytes() bytes.
  */
 int attn_fwd_shared_prefix(const void* q, const void* k_cache, const void* v_cache, const void* k_scale,
                            const void* v_scale, const int* prefix_table, int prefix_len, const int* block_table,
@@ -481,7 +488,8 @@ long long attn_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int T, 
  *   o, lse     bf16 [B, Hq, Nq, D] and fp32 [B, Hq, Nq]; rows without a key have o = 0 and
  *              lse = -infinity.                                          written (every element)
  *   Nq, Nk >= 0; D is 32, 64, 96 or 128.  B == 0 or Nq == 0: ATTN_OK, nothing launched.  Limits
- *   (ATTN_ERR_UNSUPPORTED): Nq * Hq / Hkv <= 2^30 and fewer than 2^31 16-row tiles.
+ *   (ATTN_ERR_UNSUPPORTED): Nq * Hq / Hkv <= 2^30, fewer than 2^31 16-row tiles, and
+ *   B * Hkv * (Nk / 128 + 1) <= 2^30.
  *   workspace  device pointer, 256-byte aligned, of at least attn_fwd_cross_workspace_bytes() bytes.
  * Errors and numerics as attn_fwd; deterministic.
  */
@@ -500,9 +508,8 @@ long long attn_fwd_cross_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk,
  *   dq         bf16 [B, Hq,  Nq, D]; zero in batch rows without a key      written (every element)
  *   dk, dv     bf16 [B, Hkv, Nk, D]; zero at the padding                   written (every element)
  *   workspace  device pointer, 256-byte aligned, of at least attn_bwd_cross_workspace_bytes() bytes.
- * Sizes, limits and errors as attn_fwd_cross; additionally B * Hkv * ceil(Nk / 128) <= 2^30.  With
- * Nq == 0 dk and dv are zero-filled, with Nk == 0 dq is.  The padding's keys and values are not used.  Numerics and
- * determinism as attn_bwd.
+ * Sizes, limits and errors as attn_fwd_cross.  With Nq == 0 dk and dv are zero-filled, with Nk == 0 dq
+ * is.  The padding's keys and values are not used.  Numerics and determinism as attn_bwd.
  */
 int attn_bwd_cross(const void* q, const void* k, const void* v, const int* k_lens, const void* o, const float* lse,
                    const void* dout, void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Nq, int Nk, int D,
@@ -529,7 +536,8 @@ const char* attn_last_cuda_error(void);
  * If `site` is non-null it receives the code of the first wait that gave up (0 if
  * none): 1-9 the forward kernel's roles (producer, MMA issuer, softmax, drain),
  * 10 the wait self-test, 11 the forward's split-tail merge, 12-19 the backward
- * kernels' roles.
+ * kernels' roles, 21-35 those of the forward's other forms, 41-47 the many-row
+ * kernel's (cross attention, shared prefix), 51-52 the decode kernel's.
  */
 int attn_device_status(void* stream, int* site);
 

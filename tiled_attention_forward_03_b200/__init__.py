@@ -974,6 +974,7 @@ def forward_decode(q, k_cache, v_cache, block_table, lens, k_scale=None, v_scale
     paged cache (see cache_append), which holds their keys and values already: lens[b] counts them, token t stands at
     position lens[b] - T + t and sees the positions up to its own.  Returns (o bf16, lse fp32 [B, Hq, T]); a row that
     sees nothing has o = 0 and lse = -inf.  Table entries that are no page read as zero keys and values.
+    Positions past lens[b] may hold anything; those that only later tokens of the call see must hold finite values.
 
     Made for few rows: the cache is read once for each 64 rows (T times the query heads of a KV head)."""
     import torch
@@ -1033,6 +1034,8 @@ def _cross_checks(q, k, v, k_lens):
         raise ValueError("q and k must be 4-D [B, H, N, D]")
     B, Hq, Nq, D = q.shape
     Hkv, Nk = k.shape[1], k.shape[2]
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
     dev = q.device
     _expect(q, "q", torch.bfloat16, (B, Hq, Nq, D), dev)
     _expect(k, "k", torch.bfloat16, (B, Hkv, Nk, D), dev)

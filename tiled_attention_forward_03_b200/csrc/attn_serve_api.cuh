@@ -783,9 +783,8 @@ template <int D>
 void launch_cross_bwd_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
                           const attn::BwdParams& pkv, const attn::BwdParams& pq, int num_sms, cudaStream_t s) {
   auto grid = [&](int items) { return (unsigned)(items > num_sms ? num_sms : items); };
-  if (pkv.num_items > 0)
-    attn::attn_bwd_sm100<D, true, true>
-        <<<grid(pkv.num_items), attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, true>::kAlloc, s>>>(mk, mv, mq, mdo, pkv);
+  attn::attn_bwd_sm100<D, true, true>
+      <<<grid(pkv.num_items), attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, true>::kAlloc, s>>>(mk, mv, mq, mdo, pkv);
   attn::attn_bwd_sm100<D, false, true>
       <<<grid(pq.num_items), attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, false>::kAlloc, s>>>(mq, mdo, mk, mv, pq);
 }
