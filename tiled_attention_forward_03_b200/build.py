@@ -32,7 +32,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-shared", "-Xcompiler", "-fPIC,-O2",
     "-Xptxas", "-v",
-    "--expt-relaxed-constexpr", "-split-compile=0",
+    "--expt-relaxed-constexpr",
 ]
 
 

@@ -180,13 +180,14 @@ __global__ void attn_bwd_prep(const __nv_bfloat16* __restrict__ o, const __nv_bf
   const long long row0 = ((long long)blockIdx.x * (blockDim.x >> 4) + (threadIdx.x >> 4)) * kPrepRows;
   const int l16 = threadIdx.x & 15;
   if (row0 >= rows) return;  // whole 16-lane groups leave together (rows is a multiple of 128)
+  // (Npad is a multiple of 128: the group's rows have one head)
+  const long long bh = row0 / Npad;
+  const int q0 = (int)(row0 - bh * Npad);
   uint4 a[kPrepRows], b[kPrepRows];
   bool live[kPrepRows];
 #pragma unroll
   for (int k = 0; k < kPrepRows; ++k) {
-    const long long row = row0 + k;
-    const long long bh = row / Npad;
-    const int qi = (int)(row - bh * Npad);
+    const int qi = q0 + k;
     live[k] = qi < N && l16 * 8 < D;
     a[k] = b[k] = make_uint4(0u, 0u, 0u, 0u);
     if (live[k]) {
@@ -214,8 +215,7 @@ __global__ void attn_bwd_prep(const __nv_bfloat16* __restrict__ o, const __nv_bf
     acc += __shfl_xor_sync(mask, acc, 1, 16);
     if (l16 == k) {
       const long long row = row0 + k;
-      const long long bh = row / Npad;
-      const int qi = (int)(row - bh * Npad);
+      const int qi = q0 + k;
       ndelta[row] = -acc;
       nlse2[row] = qi < N ? -lse[(size_t)bh * N + qi] * kLog2e : 0.f;
     }
@@ -379,6 +379,10 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  if constexpr (kX && kKV) {
+    wait_for_previous();   // the row sums
+    launch_dependents();   // the Q pass needs them, and nothing of this one
+  }
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
@@ -819,6 +823,8 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
+  // what follows in the stream waits for both passes
+  if (kX && !kKV && blockIdx.x == gridDim.x - 1) wait_for_previous();
 }
 
 }  // namespace attn

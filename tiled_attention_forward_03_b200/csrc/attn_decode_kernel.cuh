@@ -139,11 +139,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Programmatic dependent launch: the next kernel of the stream may start (it waits for this one's
-// end before it reads its results), and the wait for the end of the kernel before.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // The many-row kernel's results for row i of sequence b and head h: n of them, rows `at(k)` of
 // p.many.o and p.many.ml.
 struct DecParts {

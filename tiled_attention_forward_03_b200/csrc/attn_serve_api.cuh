@@ -3,6 +3,7 @@
 // translation unit: it uses that file's device set-up, error records and tensor-map encoders.
 #pragma once
 
+#include <algorithm>
 #include <type_traits>
 
 #include "attn_cache_kernel.cuh"
@@ -779,14 +780,21 @@ bool cross_bwd_device_setup(int dev) {
   return false;
 }
 
+// The Q pass starts as the KV pass's CTAs end: its work is what fills the SMs that the KV pass leaves early (units of
+// batch rows without keys at their block are empty), so it is cut into up to kCrossCtas CTAs an SM, of kCrossTiles
+// column tiles at least, which the hardware deals out.  B4 Hq32 Hkv8 Nq2048 Nk<=4096 D128: one CTA an SM 1158 us for
+// both passes, two 1088, four 1062, eight 1029; one after the other's end, 1187.  With four tiles an item
+// (Nk 512) eight CTAs an SM took 147 us instead of 138.  The KV pass gains nothing from more CTAs than SMs.
+constexpr int kCrossTiles = 8, kCrossCtas = 8;
 template <int D>
 void launch_cross_bwd_dim(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
                           const attn::BwdParams& pkv, const attn::BwdParams& pq, int num_sms, cudaStream_t s) {
-  auto grid = [&](int items) { return (unsigned)(items > num_sms ? num_sms : items); };
-  attn::attn_bwd_sm100<D, true, true>
-      <<<grid(pkv.num_items), attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, true>::kAlloc, s>>>(mk, mv, mq, mdo, pkv);
-  attn::attn_bwd_sm100<D, false, true>
-      <<<grid(pq.num_items), attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, false>::kAlloc, s>>>(mq, mdo, mk, mv, pq);
+  launch_behind(attn::attn_bwd_sm100<D, true, true>, dim3((unsigned)std::min(pkv.num_items, num_sms)),
+                attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, true>::kAlloc, s, mk, mv, mq, mdo, pkv);
+  const int each = (kCrossTiles + pkv.num_blocks - 1) / pkv.num_blocks;
+  const int ctas = std::max(num_sms, std::min((pq.num_items + each - 1) / each, kCrossCtas * num_sms));
+  launch_behind(attn::attn_bwd_sm100<D, false, true>, dim3((unsigned)std::min(pq.num_items, ctas)),
+                attn::BwdCfg<D>::kThreads, attn::BwdPlan<D, false>::kAlloc, s, mq, mdo, mk, mv, pq);
 }
 
 }  // namespace

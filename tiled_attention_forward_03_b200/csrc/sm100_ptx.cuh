@@ -432,4 +432,9 @@ ATTN_DEV uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// Programmatic dependent launch: the next kernel of the stream may start (it waits for this one's
+// end before it reads its results), and the wait for the end of the kernel before.
+ATTN_DEV void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+ATTN_DEV void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace attn
