@@ -147,12 +147,16 @@ struct DecPlan {
 
 constexpr int kDecMinShare = 4;     // places of the line: a unit's two, and 64-key blocks
 constexpr int kDecCtasPerSm = 3, kDecWarpCtasPerSm = 2;   // resident CTAs (the kernel's launch bounds)
-// Warps take whole units where no sequence has more than this many blocks, and there are units for
-// all CTAs (or sequences are so short that there is nothing to share).  Measured on B200: at the end of
-// the file's head comment, and E4M3 Hkv8 D128, all lengths at the limit: see the table of the notes.
-constexpr int kDecShortBlocks = 16, kDecTinyBlocks = 2;
-// Else a CTA takes whole units where no sequence has more than this many blocks: a launch less.
-constexpr int kDecWholeBlocks = 4;
+// A warp takes whole units where no sequence has more than kDecShortBlocks blocks and there are units for
+// all CTAs, or, behind a shared prefix (where it saves the joining kernel), kDecTinyBlocks.  Measured with
+// Hq32 Hkv8 D128 E4M3, in us, warps against the CTA form: B64 N<=250 18.4 / 20.5, B256 N<=250 35 / 47, B256
+// N<=500 55 / 68, B64 N<=500 both 28.7, B64 N<=1000 49 / 33; behind a prefix of 16384, B128 N<=500 98 / 106, B32
+// N<=120 47 / 55; without one, B4 N128 14 / 10.
+constexpr int kDecShortBlocks = 8, kDecTinyBlocks = 2;
+// Else a CTA takes whole units where no sequence has more than this many blocks: a launch less.  Whole
+// units against split ones, bf16 D128: B12 Hkv8 N500 16 / 18 us, B1 N280 12 / 14, B1 N500 16 / 14, B4 N1000
+// 25 / 16; B16 Hkv16 N<=500 D64 14 / 18.
+constexpr int kDecWholeBlocks = 8;
 
 // `cap`: keys a sequence can have at most.  `shared`: a prefix of `prefix_len` keys comes first;
 // `prefix_here`: this kernel computes it too.
@@ -169,7 +173,7 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   const long long ctas = (long long)kDecCtasPerSm * num_sms;
   const long long units = (long long)B * Hkv * pl.row_blocks;
   pl.warps = !prefix_here && pl.row_tiles == 1 &&
-             (cap_blocks <= kDecTinyBlocks || (cap_blocks <= kDecShortBlocks && units >= ctas));
+             ((shared && cap_blocks <= kDecTinyBlocks) || (cap_blocks <= kDecShortBlocks && units >= ctas));
   pl.whole_units = pl.warps || (!shared && cap_blocks <= kDecWholeBlocks) ? 1 : 0;
   double blocks = (double)units * (double)(cap_blocks + 2);   // places of the line, at most
   if (prefix_here) {
@@ -468,8 +472,11 @@ int launch_rows(attn::RowsParams& p, const RowsPlan& pl, const void* q, const vo
   return launch_status("many-row kernel launch");
 }
 
-// At most this many rows go through the decode kernel; more, through the tensor-core kernel.
-constexpr int kFewRows = 32;
+// At most this many rows of a KV head go through the decode kernel; more, through the tensor-core
+// kernel.  Measured, in us, decode kernel against the other: cross attention, B8 Hkv16 N<=1500 D64, 16 rows 20.5 /
+// 23.6, 20 to 32 rows 24.6 / 22.5 (B2 N<=8000 32.8 / 26.6); a prefix of 8000 bf16 keys (Hkv16 D64), 32 rows
+// 34 / 38 (the other is two more kernels there), 48 rows 50 / 38.
+constexpr int kFewRows = 16, kFewPrefixRows = 32;
 
 // Shared prefix: the plans of its two kernels, and the workspace's layout (decode's part first).
 struct PrefixPlan {
@@ -481,14 +488,16 @@ struct PrefixPlan {
 };
 
 // An E4M3 prefix is converted to bf16 once, ahead, where at least this many 128-row tiles of each head
-// would convert it themselves and the copy is no larger than this.
+// would convert it themselves and the copy is no larger than this.  Prefix of 16384, Hq32 Hkv8 D128, in us,
+// converted ahead against in the kernel: one tile (B32) 80 / 65, two (B64) 81 / 75, three (B96) 89 / 89, four (B128)
+// 101 / 108, eight (B256) 153 / 187.
 constexpr int kWideTiles = 4;
 constexpr size_t kWideBytes = (size_t)256 << 20;
 
 PrefixPlan prefix_plan(int B, int Hkv, long long GT, int D, int page, int max_pages, long long prefix_len,
                        int num_sms, bool f8) {
   PrefixPlan pl;
-  pl.here = prefix_len > 0 && (long long)B * GT <= kFewRows;
+  pl.here = prefix_len > 0 && (long long)B * GT <= kFewPrefixRows;
   pl.dec = dec_plan(B, Hkv, GT, D, cache_cap(page, max_pages), num_sms, true, pl.here, prefix_len);
   if (prefix_len > 0 && !pl.here) pl.rows = rows_plan(B, Hkv, GT, D, prefix_len, num_sms, true);
   const size_t wide = ((size_t)Hkv * (size_t)prefix_len * D * 2 + 255) / 256 * 256;
