@@ -73,7 +73,8 @@
 // and its gradients are stored as zeros.  Padding keys may hold anything, NaN included: their columns
 // of P and dP are replaced by zeros in registers, and the MMA warp overwrites their rows of the K tile with
 // zeros before dS K reads it (0 * NaN would not vanish in the sum); as rows of the KV pass's own tile they reach
-// only their own lanes of tensor memory, which are stored as zeros.
+// only their own lanes of tensor memory, which are stored as zeros.  The Q pass needs nothing of the KV
+// pass: it is launched to start as that one's CTAs end.
 #pragma once
 
 #include <cuda_bf16.h>

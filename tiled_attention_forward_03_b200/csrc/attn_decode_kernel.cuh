@@ -49,6 +49,12 @@
 // kernel) is joined in registers as the unit is written.  Sharing such units among a CTA's warps took
 // three times as long (B128 Hkv8 N<=256 behind a prefix: 37 us), most of it between units.
 //
+// Measured (B200; L2 flushed before each call): B64 Hq32 Hkv8 N<=8192 D128 E4M3 (550 MB) 114 us,
+// 4.8 TB/s; B3 T4 N<=100001 bf16 (820 MB) 167 us, 4.9 TB/s: three quarters of a copy's rate.  What is
+// left is the steps' own latency (conversion, products and exponentials in turn, three warps a
+// scheduler) and the ends of the units; short calls are launches, the look-up of the schedule and one
+// step's latency after another (B1 N500: 14 us).
+//
 // A CTA's four warps take `row_tiles` tiles of 16 rows (1, 2 or 4; or one of 8) and share the keys 4 / row_tiles
 // ways; the warps of one way share its ring (a stage is refilled once all of them have left it).
 // Their results are joined in shared memory, in the ring's place.  Every wait is bounded.
@@ -1039,8 +1045,7 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
 // Joins the parts of every split unit in key order, and, behind a shared prefix (area_o set), the
 // prefix's results with each row's own.  Block (unit, y): a warp for each of four rows of the unit.
 // Lane k takes part k's maximum, sum and place (32 at a time), then the warp adds the parts' rows.
-// Bound by launch and three dependent reads (lengths, sums, rows; the parts are in L2): started by the
-// first kernel's end, it takes about 3 us.
+// Bound by launch and three dependent reads (lengths, sums, rows; the parts are in L2).
 template <int D>
 __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const DecParams p, unsigned ctas) {
   __shared__ long long scratch[16];
@@ -1085,7 +1090,7 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) acc[c] *= a;
       const int here = min(32, n - k0);
-#pragma unroll 4
+#pragma unroll 8
       for (int k = 0; k < here; ++k) {
         const float wk = __shfl_sync(0xffffffffu, w, k);
         const long long pk = __shfl_sync(0xffffffffu, place, k);

@@ -87,18 +87,14 @@ int encode_rows_map(CUtensorMap* map, const void* base, int rank, const cuuint64
 // Positions [0, N) of B sequences into k, v [B][Hkv][N][D].
 void launch_cache_read(const attn::CacheView& c, bool f8, void* k, void* v, int B, int N, int D, cudaStream_t s) {
   const unsigned long long items = (unsigned long long)B * c.Hkv * N * (D / 8);
-  const bool many = items >= (1u << 20);   // two items a thread where that still fills the GPU
-  const unsigned grid = (unsigned)((items + (many ? 511 : 255)) / (many ? 512 : 256));
+  const unsigned grid = (unsigned)((items + 255) / 256);
   const auto kb = reinterpret_cast<__nv_bfloat16*>(k);
   const auto vb = reinterpret_cast<__nv_bfloat16*>(v);
   const attn::FastDiv dn = attn::make_fast_div((uint32_t)N), dh = attn::make_fast_div((uint32_t)c.Hkv);
   auto go = [&](auto kern) { kern<<<grid, 256, 0, s>>>(c, kb, vb, N, dn, dh, items); };
   auto pick = [&](auto dim) {
     constexpr int D_ = decltype(dim)::value;
-    if (f8)
-      many ? go(attn::attn_cache_read_kernel<D_, true, 2>) : go(attn::attn_cache_read_kernel<D_, true, 1>);
-    else
-      many ? go(attn::attn_cache_read_kernel<D_, false, 2>) : go(attn::attn_cache_read_kernel<D_, false, 1>);
+    f8 ? go(attn::attn_cache_read_kernel<D_, true>) : go(attn::attn_cache_read_kernel<D_, false>);
   };
   switch (D) {
     case 32: pick(std::integral_constant<int, 32>()); break;
