@@ -1,4 +1,4 @@
-"""bf16 attention on B200 (sm_100a) -- forward, backward, RoPE: Python binding of the C ABI in include/attn.h.
+"""bf16 attention on B200 (sm_100a) -- forward, backward, RoPE, paged key/value cache and decoding, cross attention: Python binding of the C ABI in include/attn.h.
 
 The binding only marshals arguments: every step of the computation runs in the
 CUDA kernel inside ``libattn_fwd.so``.  There is no CPU fallback; if the library
@@ -10,6 +10,10 @@ cannot be loaded, importing this package raises.
     cos_t, sin_t = attn.rope_tables(N, D, device="cuda")
     o, lse = attn.forward_rope(q, k, v, cos_t, sin_t, causal=True)   # attention of RoPE(q), RoPE(k)
     dq, dk, dv = attn.backward_rope(q, k, v, cos_t, sin_t, o, lse, do, causal=True)
+    attn.cache_append(k, v, k_cache, v_cache, block_table, lens, new_lens)    # pages [num_pages, Hkv, page, D]
+    o, lse = attn.forward_decode(q, k_cache, v_cache, block_table, lens)      # the last tokens of each sequence
+    o, lse = attn.forward_cross(q, k, v, k_lens=k_lens)                       # keys of another length
+    dq, dk, dv = attn.backward_cross(q, k, v, o, lse, do, k_lens=k_lens)
 """
 from __future__ import annotations
 
