@@ -70,12 +70,13 @@ def check(o, lse, want, d, scale, n):
     otherwise work in fp32 (2^-24 a step):
       scores   the sum of D products: at most (D + 4) steps of sum |q k| * scale, which shifts every exponent; an
                exponential turns that into a relative error of p, once in the numerator and once in the sum;
-      exp      2 * 7.5e-5 where the polynomial is used, its largest relative error, numerator and sum;
+      exp      2 * 2.4e-7, the largest relative error of the hardware's 2^x (2^-22) and of the polynomial that
+               stands in for part of it, numerator and sum;
       sums     n + 64 additions at most, numerator and sum.
     """
     o_ref, lse_ref, a, top = want
     half = 2.0 ** -8
-    rel = 2 * ((d + 4) * 2.0 ** -24 * abs(scale) * top + 7.5e-5 + (n + 64) * 2.0 ** -24)
+    rel = 2 * ((d + 4) * 2.0 ** -24 * abs(scale) * top + 2.4e-7 + (n + 64) * 2.0 ** -24)
     tol = (half * (1 + half) + rel[..., None]) * a + half * (np.abs(o_ref) + half * a) + 1e-30
     live = np.isfinite(lse_ref)
     assert np.array_equal(np.isneginf(lse), ~live), "rows without keys"

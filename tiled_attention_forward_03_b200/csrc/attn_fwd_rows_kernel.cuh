@@ -415,15 +415,18 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
     // Zeros for the tiles of batch rows without keys (the whole warp, while the last units are
     // computed), dealt out to all CTAs.
     if (!p.prefix) {
-      for (int seq = 0; seq < p.B; ++seq) {
-        if (rows_len(p, seq) > 0) continue;
-        for (long long u = blockIdx.x; u < per_seq; u += gridDim.x) {
-          const int h = (int)(u / p.tiles), i0 = (int)(u - (long long)h * p.tiles) * kBlockM;
-          const int n = min(kBlockM, p.GT - i0);
-          const long long row = ((long long)seq * p.Hkv + h) * p.GT + i0;
-          for (int i = lane; i < n * (D / 8); i += 32)
-            reinterpret_cast<uint4*>(p.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-          for (int i = lane; i < n; i += 32) p.lse[row + i] = -INFINITY;
+      for (int c = 0; c < p.B; c += 32) {
+        unsigned none = __ballot_sync(0xffffffffu, c + lane < p.B && rows_len(p, c + lane) == 0);
+        for (; none != 0u; none &= none - 1u) {
+          const int seq = c + __ffs(none) - 1;
+          for (long long u = blockIdx.x; u < per_seq; u += gridDim.x) {
+            const int h = (int)(u / p.tiles), i0 = (int)(u - (long long)h * p.tiles) * kBlockM;
+            const int n = min(kBlockM, p.GT - i0);
+            const long long row = ((long long)seq * p.Hkv + h) * p.GT + i0;
+            for (int i = lane; i < n * (D / 8); i += 32)
+              reinterpret_cast<uint4*>(p.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = lane; i < n; i += 32) p.lse[row + i] = -INFINITY;
+          }
         }
       }
     }
