@@ -168,6 +168,22 @@ def test_many_short_sequences(attn):
 
 
 @pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("B,hkv,top,d", [(80, 2, 1200, 64), (50, 4, 900, 128), (230, 2, 400, 96), (3, 2, 500, 32)])
+def test_whole_units(attn, f8, B, hkv, top, d):
+    """Batches whose units are not split: one to a CTA, one to a warp, and a few short ones."""
+    r = np.random.default_rng(12)
+    lens = [int(x) for x in r.integers(0, top + 1, B)]
+    lens[0], lens[1], lens[-1] = top, 0, top - 1
+    c = Cache(56, lens, hkv, d, 32, f8)
+    q = bf16(gen(13), B, 4 * hkv, 2, d)
+    k, v, table, n, sc = c.on_gpu()
+    o, lse = attn.forward_decode(q.cuda(), k, v, table, n, **sc)
+    settled(attn)
+    for b in (0, 1, 2, B // 2, B - 2, B - 1):
+        check(f64(o[b]), f64(lse[b]), decode_want(c, f64(q[b]), b, d ** -0.5), d, d ** -0.5, lens[b])
+
+
+@pytest.mark.parametrize("f8", [False, True])
 def test_many_tokens_at_once(attn, f8):
     """2,400 rows a KV head through the decode, most of which see nothing."""
     c = Cache(53, [40, 700], 1, 64, 16, f8)

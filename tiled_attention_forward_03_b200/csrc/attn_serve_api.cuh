@@ -149,10 +149,14 @@ constexpr int kDecCtasPerSm = 3, kDecWarpCtasPerSm = 2;   // resident CTAs (the 
 // N<=500 55 / 68, B64 N<=500 both 28.7, B64 N<=1000 49 / 33; behind a prefix of 16384, B128 N<=500 98 / 106, B32
 // N<=120 47 / 55; without one, B4 N128 14 / 10.
 constexpr int kDecShortBlocks = 8, kDecTinyBlocks = 2;
-// Else a CTA takes whole units where no sequence has more than this many blocks: a launch less.  Whole
-// units against split ones, bf16 D128: B12 Hkv8 N500 16 / 18 us, B1 N280 12 / 14, B1 N500 16 / 14, B4 N1000
-// 25 / 16; B16 Hkv16 N<=500 D64 14 / 18.
-constexpr int kDecWholeBlocks = 8;
+// Else a CTA takes whole units where no sequence has more than kDecWholeBlocks blocks, or, with a unit (of
+// up to 8 rows) for each SM and no more than there are CTAs, kDecEvenBlocks (kDecEvenNarrow at D <= 64,
+// where a step has more keys): a launch less, and nothing to join.  Whole units against split ones, in us:
+// bf16 Hkv8 D128 B12 N500 16 / 18, B1 N280 12 / 14, B1 N500 16 / 14, B4 N1000 25 / 16; a unit for each SM, D64 Hkv16
+// B10 N<=1000 16 / 21, B16 N<=1500 22.5 / 25.6, all 1500 27 / 32, N<=3000 35 / 34, D32 Hkv8 B30 N2000 33 / 29;
+// D128, E4M3 Hkv8 B48 N<=1000 27 / 34, bf16 Hkv16 B12 N<=1500 33 / 30, Hkv8 B20 N<=2000 39 / 32; 16 rows, E4M3 B20
+// N<=2000 74 / 46; more units than CTAs, B64 N<=1000 42 / 36.
+constexpr int kDecWholeBlocks = 8, kDecEvenBlocks = 16, kDecEvenNarrow = 24;
 
 // `cap`: keys a sequence can have at most.  `shared`: a prefix of `prefix_len` keys comes first;
 // `prefix_here`: this kernel computes it too.
@@ -170,7 +174,9 @@ DecPlan dec_plan(int B, int Hkv, long long GT, int D, long long cap, int num_sms
   const long long units = (long long)B * Hkv * pl.row_blocks;
   pl.warps = !prefix_here && pl.row_tiles == 1 &&
              ((shared && cap_blocks <= kDecTinyBlocks) || (cap_blocks <= kDecShortBlocks && units >= ctas));
-  pl.whole_units = pl.warps || (!shared && cap_blocks <= kDecWholeBlocks) ? 1 : 0;
+  const bool even = pl.tile_rows == 8 && units >= num_sms && units <= ctas;
+  const int whole_blocks = !even ? kDecWholeBlocks : D <= 64 ? kDecEvenNarrow : kDecEvenBlocks;
+  pl.whole_units = pl.warps || (!shared && cap_blocks <= whole_blocks) ? 1 : 0;
   double blocks = (double)units * (double)(cap_blocks + 2);   // places of the line, at most
   if (prefix_here) {
     const long long rows = (long long)B * GT;
