@@ -183,6 +183,29 @@ def test_whole_units(attn, f8, B, hkv, top, d):
         check(f64(o[b]), f64(lse[b]), decode_want(c, f64(q[b]), b, d ** -0.5), d, d ** -0.5, lens[b])
 
 
+def test_what_follows_waits_for_unsplit_units(attn):
+    """No unit is split, so the joining kernels have nothing to do: a copy of the result behind the call still gets it
+    whole."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    g = torch.Generator(device="cuda").manual_seed(14)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    # decode: as many equal units as CTAs (three an SM)
+    B, hkv, d, page, n = 3 * sms // 4, 4, 128, 64, 2560
+    k, v, q = rand(B * n // page, hkv, page, d), rand(B * n // page, hkv, page, d), rand(B, 8, 1, d)
+    table = torch.arange(B * n // page, dtype=torch.int32, device="cuda").view(B, n // page)
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    # cross: a unit for each SM
+    qc, kc, vc = rand(sms, 1, 128, d), rand(sms, 1, 8192, d), rand(sms, 1, 8192, d)
+    for _ in range(5):
+        for call, shape in ((lambda out: attn.forward_decode(q, k, v, table, lens, out=out), q.shape),
+                            (lambda out: attn.forward_cross(qc, kc, vc, out=out), qc.shape)):
+            out = torch.full(shape, 7.0, dtype=torch.bfloat16, device="cuda")
+            call(out)
+            behind = out.clone()
+            settled(attn)
+            assert not (out == 7).all(-1).any() and same([behind], [out])
+
+
 @pytest.mark.parametrize("f8", [False, True])
 def test_many_tokens_at_once(attn, f8):
     """2,400 rows a KV head through the decode, most of which see nothing."""

@@ -1058,6 +1058,8 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
   int seq;
   long long first;
   const DecLine ln = dec_locate(p, ctas, 0, b, scratch, seq, first);
+  // what follows in the stream waits for this kernel alone, so some block always waits for the one before
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) wait_for_previous();
   const int places = dec_places(dec_blocks(p, dec_len(p, b)));
   const long long u0 = first + (long long)hr * places, u1 = u0 + places;
   const bool shared = p.area_o[0] != nullptr;

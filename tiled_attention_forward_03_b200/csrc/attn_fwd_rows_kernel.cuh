@@ -1001,6 +1001,8 @@ __global__ void __launch_bounds__(256) attn_rows_join_kernel(const RowsParams p,
   const int4 unit = unit_s;
   const long long first_slot = place_s, c0 = blockIdx.x;
   const int n = unit.w;
+  // what follows in the stream waits for this kernel alone, so some block always waits for the one before
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1) wait_for_previous();
   if (n == 0) return;
   // rows r0 + 8 i of the unit (those that are none come last); lane (i, k): part k of row i
   const int r0 = blockIdx.y * 32 + warp, part = lane & 7;
