@@ -318,6 +318,18 @@ def test_shared_prefix_of_nothing_is_decode(attn):
 
 
 @pytest.mark.parametrize("B", [3, 60])
+@pytest.mark.parametrize("page", [16, 48, 32])
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+def test_shared_prefix_without_pages_of_its_own(attn, d, f8, page, B):
+    """A table of no pages (its pointer is null): the prefix's pages are pages all the same, of fewer rows than a step
+    of the kernel or not a multiple of it."""
+    c = Cache(34, [0] * B, 2, d, page, f8, prefix=100)
+    c.table = c.table[:, :0].contiguous()
+    check_decode(attn, c, 4, 2, which=[0, B - 1])
+
+
+@pytest.mark.parametrize("B", [3, 60])
 @pytest.mark.parametrize("f8", [False, True])
 def test_shared_prefix_bad_page_reads_as_zeros(attn, f8, B):
     c = Cache(33, [10] * B, 1, 64, 16, f8, prefix=100)

@@ -215,8 +215,10 @@ int launch_decode_dim(attn::DecParams& p, const DecPlan& pl, const void* k, cons
     record_cuda_error("decode device setup", e);
     return ATTN_ERR_CUDA;
   }
-  // boxes of a whole step where pages hold whole steps (contiguous keys are one page), else of 16 keys
-  p.box = (p.table == nullptr || p.page % Cfg::kStep == 0) ? Cfg::kStep : 16;
+  // boxes of a whole step where pages hold whole steps (contiguous keys are one page), else of 16 keys; a call
+  // may have a table for its prefix alone (max_pages == 0)
+  const bool paged = p.table != nullptr || p.prefix_table != nullptr;
+  p.box = (!paged || p.page % Cfg::kStep == 0) ? Cfg::kStep : 16;
   CUtensorMap mk, mv;
   int st;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.page, (cuuint64_t)p.num_pages * (cuuint64_t)p.Hkv};
