@@ -110,6 +110,35 @@ def test_forward_large_scores_move_the_maximum(attn):
     check(f64(o[0]), f64(lse[0]), attend(f64(q[0]), f64(k[0]), f64(v[0]), [700] * 140, 1 / 8), 64, 1 / 8, 700)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,nk", [(1, 150), (200, 150), (200, 16), (130, 1200), (2000, 700)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_forward_keys_that_are_not_finite(attn, bad, nq, nk, d):
+    """A key that is NaN or infinite, at each position mod 16 (one a batch row): NaN wherever the score is NaN or plus
+    infinity, the key's weight 0 where it is minus infinity; the other batch rows bit for bit as without it."""
+    B, s = 18, d ** -0.5
+    q, k, v, _ = case(8, B, 2, 1, nq, nk, d, None)
+    clean = attn.forward_cross(q.cuda(), k.cuda(), v.cuda())
+    at = [nk // 2 // 16 * 16 + b for b in range(16)]
+    for b, p in enumerate(at):
+        k[b, 0, p, 3] = bad
+    o, lse = attn.forward_cross(q.cuda(), k.cuda(), v.cuda())
+    settled(attn)
+    for got, want in zip((o, lse), clean):
+        assert torch.equal(got[16:], want[16:])
+    for b, p in enumerate(at):
+        nan = torch.isnan(q[b, ..., 3].float() * bad) | (q[b, ..., 3].float() * bad > 0)   # [Hq, Nq]
+        assert torch.equal(lse[b].isnan().cpu(), nan) and torch.equal(o[b].isnan().all(-1).cpu(), nan)
+        rows = (~nan).any(0).nonzero().flatten()[:40]
+        if len(rows):
+            keep = [j for j in range(nk) if j != p]
+            want = attend(f64(q[b][:, rows]), f64(k[b, :, keep]), f64(v[b, :, keep]), [nk - 1] * len(rows), s)
+            live = f64(~nan[:, rows].unsqueeze(-1)) > 0
+            w = (*(np.where(live if x.ndim == 3 else live[..., 0], x, -np.inf if i == 1 else 0.0) for i, x in enumerate(want)),)
+            go, gl = f64(o[b][:, rows]), f64(lse[b][:, rows])
+            check(np.where(live, go, 0.0), np.where(live[..., 0], gl, -np.inf), w, d, s, nk)
+
+
 def backward_bounds(q, k, v, do, n, scale, o, lse):
     """Element-wise tolerances of dq, dk, dv for one batch row, from the roundings of the kernel: P and dS to bf16 (half
     a step, 2^-8, of each), the gradients to bf16, and the given o (bf16) in delta; scores, dP and exponentials in fp32

@@ -337,6 +337,30 @@ def test_shared_prefix_bad_page_reads_as_zeros(attn, f8, B):
     check_decode(attn, c, 4, 1, which=[0, B - 1])
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("B", [4, 25, 150])   # 16 rows a KV head: the decode kernel; 100: one tile; 600: E4M3 converted ahead
+def test_shared_prefix_keys_that_are_not_finite(attn, B, f8):
+    """A prefix key that is NaN (E4M3: marked), at each position mod 16: every row of its head is NaN in o and lse, the
+    other head's rows are bit for bit as without it."""
+    c = Cache(35, [(7 * b) % 40 for b in range(B)], 2, 64, 16, f8, prefix=300)
+    q = bf16(gen(6), B, 8, 1, 64)
+    clean = run_decode(attn, c, q)
+    for p in range(130, 146):
+        i, row = page_row(c.prefix_table.tolist(), 16, c.k.shape[0], p)
+        keep = c.k[i, 0, row].clone(), None if c.ks is None else c.ks.view(torch.uint8)[i, 0, row].clone()
+        if f8:
+            c.k[i, 0, row] = 0
+            c.ks.view(torch.uint8)[i, 0, row] = 255
+        else:
+            c.k[i, 0, row, 5] = math.nan
+        o, lse = run_decode(attn, c, q)
+        assert o[:, :4].isnan().all() and lse[:, :4].isnan().all(), p
+        assert torch.equal(o[:, 4:], clean[0][:, 4:]) and torch.equal(lse[:, 4:], clean[1][:, 4:]), p
+        c.k[i, 0, row] = keep[0]
+        if f8:
+            c.ks.view(torch.uint8)[i, 0, row] = keep[1]
+
+
 # ---------------------------------------------------------------- together, as a server uses them
 
 @pytest.mark.parametrize("f8", [False, True])

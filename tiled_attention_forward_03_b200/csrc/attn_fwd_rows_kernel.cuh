@@ -222,9 +222,21 @@ ATTN_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int 
       : "memory");
 }
 
+// Maxima that keep a NaN (max.f32 and fmaxf drop it).
+ATTN_DEV float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+ATTN_DEV float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // 2^x for a pair on the FMA pipe, as exp2_poly2 but with a degree-5 polynomial (csrc/fit_exp2_poly.py
 // 5: largest relative error 2.4e-7 in fp32).  The degree-3 one is 7e-5 low at the row's maximum,
-// which shows in the LSE of rows with few keys.
+// which shows in the LSE of rows with few keys.  (The clamp drops a NaN: the row maximum carries it.)
 ATTN_DEV float2 exp2_poly5(float2 x) {
   constexpr float kRound = 12582912.0f;
   x.x = fmaxf(x.x, -125.0f);
@@ -694,24 +706,27 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
           for (int i = 0; i < 64; ++i)
             if (k0 + i > key_lim) s[i] = -INFINITY;
         }
+        // The maximum keeps a NaN score (a key that is NaN): through m the row's sum, O and LSE are NaN
+        // then, also where the polynomial, which takes it for a small probability, has its column.  (An
+        // infinite score makes them NaN at the end of the unit, as infinity - infinity.)
         float mx[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = max3f(s[e], s[4 + e], s[8 + e]);
+        for (int e = 0; e < 4; ++e) mx[e] = max3_nan(s[e], s[4 + e], s[8 + e]);
 #pragma unroll
         for (int i = 12; i < 60; i += 8) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3f(mx[e], s[i + e], s[i + 4 + e]);
+          for (int e = 0; e < 4; ++e) mx[e] = max3_nan(mx[e], s[i + e], s[i + 4 + e]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[60 + e]);
-        const float m_new = fmaxf(m, fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]) * c);
+        for (int e = 0; e < 4; ++e) mx[e] = max_nan(mx[e], s[60 + e]);
+        const float m_new = max_nan(m, max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]) * c);
         // Lazy correction, as in the column-split kernel.
         bool any_rescale = false;
         float alpha = 1.f;
         if (j == w.jb) {
           m = m_new;
         } else {
-          const bool need = m_new > m + kRescaleLog2;
+          const bool need = !(m_new <= m + kRescaleLog2) && m == m;   // (once for a NaN: O and l stay NaN)
           any_rescale = __any_sync(0xffffffffu, need);
           if (need) {
             alpha = ex2_approx(m - m_new);  // 0 while m is still -inf (no key of this half seen yet)
