@@ -234,6 +234,23 @@ def test_step_against_differences(attn):
         assert abs(terms.sum() - slope) <= 6 * 2.0 ** -6 * math.sqrt((terms ** 2).sum()) + 1e-6
 
 
+@pytest.mark.parametrize("d,nq,nk", [(32, 40, 30), (64, 300, 130), (96, 128, 500), (128, 700, 900)])
+def test_backward_row_sums_are_this_calls(attn, d, nq, nk):
+    """Calls in turn whose row sums differ in every row and lie in the same workspace, without a pause between them:
+    the dQ pass, which starts before the dK/dV pass has ended, reads those of its own call."""
+    q, k, v, do = (t.cuda() for t in case(18, 2, 4, 2, nq, nk, d, None))
+    o, lse = attn.forward_cross(q, k, v)
+    dos = [do, (-3 * do).contiguous(), (do * do).contiguous()]
+    want = []
+    for x in dos:
+        want.append(attn.backward_cross(q, k, v, o, lse, x))
+        torch.cuda.synchronize()
+    got = [attn.backward_cross(q, k, v, o, lse, dos[i % 3]) for i in range(30)]
+    settled(attn)
+    for i, grads in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(grads, want[i % 3])), i
+
+
 def test_backward_captured_beside_an_eager_one(attn):
     B, hq, hkv, nq, nk, d, lens = 2, 2, 1, 100, 150, 64, [150, 33]
     q, k, v, do = (t.cuda() for t in case(16, B, hq, hkv, nq, nk, d, lens))

@@ -380,9 +380,14 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  // The row sums reach the Q pass past this one.  A wait makes the kernel before visible to the grid that
+  // executes it, and the Q pass's own would be for the whole KV pass; so here every thread waits for the row
+  // sums, releases what it then sees at device scope, and only then lets the Q pass start; the threads there that
+  // read them acquire at device scope first and read past L1, where alone an older copy could lie.
   if constexpr (kX && kKV) {
-    wait_for_previous();   // the row sums
-    launch_dependents();   // the Q pass needs them, and nothing of this one
+    wait_for_previous();
+    fence_acq_rel_gpu();
+    launch_dependents();   // the Q pass needs nothing of this one
   }
 
   if (warp == 8) {
@@ -631,12 +636,13 @@ __global__ void __launch_bounds__(BwdCfg<D>::kThreads, 1)
       }
     }
     const int keys = kX ? w.len : p.N;          // positions that are keys
+    if constexpr (kX && !kKV) fence_acq_rel_gpu();   // the row sums' (see the KV pass's release)
     // Q pass: the row's -lse2 and -delta are fixed for the whole unit.
     float row_nlse2 = 0.f, row_ndelta = 0.f;
     if (!kKV) {
       const size_t off = (size_t)w.row_head * p.Npad + row;
-      row_nlse2 = p.nlse2[off];
-      row_ndelta = p.ndelta[off];
+      row_nlse2 = kX ? __ldcg(p.nlse2 + off) : p.nlse2[off];
+      row_ndelta = kX ? __ldcg(p.ndelta + off) : p.ndelta[off];
     }
     int cb = w.c0;                              // column block of the current tile
     for (int it0 = 0; it0 < w.n && ok; ++it0) {

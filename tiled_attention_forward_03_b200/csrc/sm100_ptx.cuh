@@ -436,5 +436,7 @@ ATTN_DEV uint32_t pack_bf16x2(float lo, float hi) {
 // end before it reads its results), and the wait for the end of the kernel before.
 ATTN_DEV void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 ATTN_DEV void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Release and acquire of all of a thread's memory accesses at device scope.
+ATTN_DEV void fence_acq_rel_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 
 }  // namespace attn
