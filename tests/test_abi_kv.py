@@ -96,6 +96,19 @@ def test_workspace_queries_refuse_what_the_calls_refuse():
     assert attn.attn_bwd_cross_workspace_bytes(2, 4, 2, 5) > 0
 
 
+def test_a_failed_workspace_query_is_asked_again(monkeypatch):
+    """A CUDA error during the query does not stay: the next call of those sizes gets its workspace, and that is kept."""
+    answers = [-1, -1, 4096]
+
+    class Lib:
+        def attn_fwd_decode_workspace_bytes(self, *sizes):
+            return answers.pop(0)
+
+    monkeypatch.setattr(attn, "lib", Lib())
+    sizes = ("attn_fwd_decode_workspace_bytes", 77, 2, 4, 2, 1, 64, 16, 4)
+    assert [attn._workspace_bytes(*sizes) for _ in range(4)] == [-1, -1, 4096, 4096]
+
+
 def test_host_tensors_are_refused():
     import torch
 

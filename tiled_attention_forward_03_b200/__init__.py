@@ -859,10 +859,25 @@ class _On:
             torch.cuda.set_device(self.before)
 
 
+class _NoBytes(Exception):
+    pass
+
+
 @functools.lru_cache(maxsize=4096)
+def _known_workspace_bytes(what: str, device_index: int, *sizes) -> int:
+    n = getattr(lib, what)(*sizes)
+    if n < 0:
+        raise _NoBytes   # refused sizes or a CUDA error: the cache keeps neither
+    return n
+
+
 def _workspace_bytes(what: str, device_index: int, *sizes) -> int:
-    """lib.<what>(*sizes) for the current device (device_index), a function of the sizes alone; -1 where refused."""
-    return getattr(lib, what)(*sizes)
+    """lib.<what>(*sizes) for the current device (device_index), a function of the sizes alone, asked once; -1, each
+    time asked anew, where it refuses them or a CUDA call failed."""
+    try:
+        return _known_workspace_bytes(what, device_index, *sizes)
+    except _NoBytes:
+        return -1
 
 
 def _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, device):
