@@ -14,6 +14,10 @@ cannot be loaded, importing this package raises.
     o, lse = attn.forward_decode(q, k_cache, v_cache, block_table, lens)      # the last tokens of each sequence
     o, lse = attn.forward_cross(q, k, v, k_lens=k_lens)                       # keys of another length
     dq, dk, dv = attn.backward_cross(q, k, v, o, lse, do, k_lens=k_lens)
+
+Each call runs on ``stream`` (default: torch's current stream), and on that alone: with another stream than the current
+one, the caller orders the two and keeps the inputs alive as for any work of that stream (Tensor.record_stream); outputs
+that the call allocates may be used on, and freed behind, either.
 """
 from __future__ import annotations
 
@@ -357,6 +361,22 @@ def _check(t, name, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _new(shape, dtype, device, stream):
+    """An output for a call on `stream` (None: the current one).  On another stream than the current its memory comes from
+    that stream's pool, so that whatever held it before has ended there, and it returns to the pool only after the work
+    that the current stream has when it is freed."""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    if here != stream:
+        t.record_stream(here)
+    return t
+
+
 _workspaces: dict = {}
 
 
@@ -374,7 +394,7 @@ def _workspace(device, nbytes: int, purpose: str, stream):
     key = (device.type, device.index, purpose, stream.cuda_stream)
     buf = _workspaces.get(key)
     if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        buf = _new((nbytes,), torch.uint8, device, stream)
         _workspaces[key] = buf
     buf.record_stream(stream)
     return buf
@@ -401,9 +421,9 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None,
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device)
+        lse = _new((B, Hq, N), torch.float32, q.device, stream)
     _check(out, "out", torch.bfloat16, (B, Hq, N, D))
     _check(lse, "lse", torch.float32, (B, Hq, N))
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -572,9 +592,9 @@ def backward(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
     _check(dout, "dout", torch.bfloat16, (B, Hq, N, D))
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _new(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _new(k.shape, k.dtype, k.device, stream) if dk is None else dk
+    dv = _new(v.shape, v.dtype, v.device, stream) if dv is None else dv
     _check(dq, "dq", torch.bfloat16, (B, Hq, N, D))
     _check(dk, "dk", torch.bfloat16, (B, Hkv, N, D))
     _check(dv, "dv", torch.bfloat16, (B, Hkv, N, D))
@@ -648,8 +668,8 @@ def forward_fp8(q, k, v, q_descale: float, k_descale: float, v_descale: float, c
     _check(v, "v", f8, (B, Hkv, N, D))
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    out = torch.empty((B, Hq, N, D), dtype=torch.bfloat16, device=q.device) if out is None else out
-    lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device) if lse is None else lse
+    out = _new((B, Hq, N, D), torch.bfloat16, q.device, stream) if out is None else out
+    lse = _new((B, Hq, N), torch.float32, q.device, stream) if lse is None else lse
     _check(out, "out", torch.bfloat16, (B, Hq, N, D))
     _check(lse, "lse", torch.float32, (B, Hq, N))
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -675,8 +695,8 @@ def rope_tables(N: int, D: int, base: float = 10000.0, device=None, stream=None)
     dev = torch.device(device if device is not None else "cuda")
     with torch.cuda.device(dev):
         s = stream if stream is not None else torch.cuda.current_stream(dev)
-        cos_t = torch.empty((N, D // 2), dtype=torch.float32, device=dev)
-        sin_t = torch.empty((N, D // 2), dtype=torch.float32, device=dev)
+        cos_t = _new((N, D // 2), torch.float32, dev, stream)
+        sin_t = _new((N, D // 2), torch.float32, dev, stream)
         st = attn_rope_tables(cos_t.data_ptr(), sin_t.data_ptr(), N, D, base, s.cuda_stream)
     if st != ATTN_OK:
         raise AttnError(st, "attn_rope_tables")
@@ -694,8 +714,8 @@ def rope(q, k, cos_t, sin_t, q_out=None, k_out=None, stream=None):
     _check(k, "k", torch.bfloat16, (B, Hkv, N, D))
     _check(cos_t, "cos_t", torch.float32, (N, D // 2))
     _check(sin_t, "sin_t", torch.float32, (N, D // 2))
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    k_out = torch.empty_like(k) if k_out is None else k_out
+    q_out = _new(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
+    k_out = _new(k.shape, k.dtype, k.device, stream) if k_out is None else k_out
     _check(q_out, "q_out", torch.bfloat16, (B, Hq, N, D))
     _check(k_out, "k_out", torch.bfloat16, (B, Hkv, N, D))
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -719,8 +739,8 @@ def rope_inverse(dq_rot, dk_rot, cos_t, sin_t, dq=None, dk=None, stream=None):
     _check(dk_rot, "dk_rot", torch.bfloat16, (B, Hkv, N, D))
     _check(cos_t, "cos_t", torch.float32, (N, D // 2))
     _check(sin_t, "sin_t", torch.float32, (N, D // 2))
-    dq = torch.empty_like(dq_rot) if dq is None else dq
-    dk = torch.empty_like(dk_rot) if dk is None else dk
+    dq = _new(dq_rot.shape, dq_rot.dtype, dq_rot.device, stream) if dq is None else dq
+    dk = _new(dk_rot.shape, dk_rot.dtype, dk_rot.device, stream) if dk is None else dk
     _check(dq, "dq", torch.bfloat16, (B, Hq, N, D))
     _check(dk, "dk", torch.bfloat16, (B, Hkv, N, D))
     s = stream if stream is not None else torch.cuda.current_stream(dq_rot.device)
@@ -753,9 +773,9 @@ def backward_rope(q, k, v, cos_t, sin_t, o, lse, dout, causal: bool = False, sca
     _check(dout, "dout", torch.bfloat16, (B, Hq, N, D))
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _new(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _new(k.shape, k.dtype, k.device, stream) if dk is None else dk
+    dv = _new(v.shape, v.dtype, v.device, stream) if dv is None else dv
     _check(dq, "dq", torch.bfloat16, (B, Hq, N, D))
     _check(dk, "dk", torch.bfloat16, (B, Hkv, N, D))
     _check(dv, "dv", torch.bfloat16, (B, Hkv, N, D))
@@ -788,8 +808,8 @@ def forward_rope(q, k, v, cos_t, sin_t, causal: bool = False, scale: float | Non
     _check(sin_t, "sin_t", torch.float32, (N, D // 2))
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device) if lse is None else lse
+    out = _new(q.shape, q.dtype, q.device, stream) if out is None else out
+    lse = _new((B, Hq, N), torch.float32, q.device, stream) if lse is None else lse
     _check(out, "out", torch.bfloat16, (B, Hq, N, D))
     _check(lse, "lse", torch.float32, (B, Hq, N))
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -952,11 +972,11 @@ def cache_read(k_cache, v_cache, block_table, lens, N: int, k_scale=None, v_scal
     s = _raw_stream(stream, dev)
     shape = (B, Hkv, N, D)
     if k_out is None:
-        k_out = torch.empty(*shape, dtype=torch.bfloat16, device=dev)
+        k_out = _new(shape, torch.bfloat16, dev, stream)
     else:
         _expect(k_out, "k_out", torch.bfloat16, shape, dev)
     if v_out is None:
-        v_out = torch.empty(*shape, dtype=torch.bfloat16, device=dev)
+        v_out = _new(shape, torch.bfloat16, dev, stream)
     else:
         _expect(v_out, "v_out", torch.bfloat16, shape, dev)
     with _On(dev):
@@ -968,7 +988,7 @@ def cache_read(k_cache, v_cache, block_table, lens, N: int, k_scale=None, v_scal
     return k_out, v_out
 
 
-def _decode_outputs(q, Hkv, B, D, out, lse):
+def _decode_outputs(q, B, D, out, lse, stream):
     import torch
 
     if q.dim() != 4:
@@ -977,11 +997,11 @@ def _decode_outputs(q, Hkv, B, D, out, lse):
     dev = q.device
     _expect(q, "q", torch.bfloat16, (B, Hq, T, D), dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(shape, torch.bfloat16, dev, stream)
     else:
         _expect(out, "out", torch.bfloat16, shape, dev)
     if lse is None:
-        lse = torch.empty(B, Hq, T, dtype=torch.float32, device=dev)
+        lse = _new((B, Hq, T), torch.float32, dev, stream)
     else:
         _expect(lse, "lse", torch.float32, (B, Hq, T), dev)
     return Hq, T, out, lse
@@ -1000,7 +1020,7 @@ def forward_decode(q, k_cache, v_cache, block_table, lens, k_scale=None, v_scale
 
     dev = q.device
     B, Hkv, D, num_pages, page, max_pages = _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, dev)
-    Hq, T, out, lse = _decode_outputs(q, Hkv, B, D, out, lse)
+    Hq, T, out, lse = _decode_outputs(q, B, D, out, lse, stream)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     s = _raw_stream(stream, dev)
@@ -1026,7 +1046,7 @@ def forward_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len: int, bl
 
     dev = q.device
     B, Hkv, D, num_pages, page, max_pages = _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, dev)
-    Hq, T, out, lse = _decode_outputs(q, Hkv, B, D, out, lse)
+    Hq, T, out, lse = _decode_outputs(q, B, D, out, lse, stream)
     _expect(prefix_table, "prefix_table", torch.int32, (prefix_table.numel(),), dev)
     if prefix_len < 0 or prefix_len > prefix_table.numel() * page:
         raise ValueError(f"prefix_len {prefix_len} does not fit prefix_table's {prefix_table.numel()} pages of {page}")
@@ -1073,11 +1093,11 @@ def forward_cross(q, k, v, k_lens=None, scale: float | None = None, out=None, ls
 
     B, Hq, Hkv, Nq, Nk, D, dev = _cross_checks(q, k, v, k_lens)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(q.shape, torch.bfloat16, dev, stream)
     else:
         _expect(out, "out", torch.bfloat16, (B, Hq, Nq, D), dev)
     if lse is None:
-        lse = torch.empty(B, Hq, Nq, dtype=torch.float32, device=dev)
+        lse = _new((B, Hq, Nq), torch.float32, dev, stream)
     else:
         _expect(lse, "lse", torch.float32, (B, Hq, Nq), dev)
     if scale is None:
@@ -1106,9 +1126,9 @@ def backward_cross(q, k, v, o, lse, dout, k_lens=None, scale: float | None = Non
     _expect(o, "o", torch.bfloat16, q_shape, dev)
     _expect(lse, "lse", torch.float32, (B, Hq, Nq), dev)
     _expect(dout, "dout", torch.bfloat16, q_shape, dev)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _new(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _new(k.shape, k.dtype, k.device, stream) if dk is None else dk
+    dv = _new(v.shape, v.dtype, v.device, stream) if dv is None else dv
     _expect(dq, "dq", torch.bfloat16, q_shape, dev)
     _expect(dk, "dk", torch.bfloat16, k_shape, dev)
     _expect(dv, "dv", torch.bfloat16, k_shape, dev)
