@@ -22,7 +22,6 @@ that the call allocates may be used on, and freed behind, either.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 
@@ -362,19 +361,24 @@ def _check(t, name, dtype, shape):
 
 
 def _new(shape, dtype, device, stream):
-    """An output for a call on `stream` (None: the current one).  On another stream than the current its memory comes from
-    that stream's pool, so that whatever held it before has ended there, and it returns to the pool only after the work
-    that the current stream has when it is freed."""
+    """An output for a call on a `stream` that was named.  On another stream than the current its memory comes from that
+    stream's pool, so that whatever held it before has ended there, and it returns to the pool only after the work that
+    the current stream has when it is freed.  (Without a name, torch.empty does this in a fifth of the time.)"""
     import torch
 
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     here = torch.cuda.current_stream(device)
     if here != stream:
         t.record_stream(here)
     return t
+
+
+def _new_like(t, stream):
+    """An output like t, for a call on `stream` (None: the current one)."""
+    import torch
+
+    return torch.empty_like(t) if stream is None else _new(t.shape, t.dtype, t.device, stream)
 
 
 _workspaces: dict = {}
@@ -421,9 +425,10 @@ def forward(q, k, v, causal: bool = False, scale: float | None = None, out=None,
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if out is None:
-        out = _new(q.shape, q.dtype, q.device, stream)
+        out = torch.empty_like(q) if stream is None else _new(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = _new((B, Hq, N), torch.float32, q.device, stream)
+        lse = (torch.empty((B, Hq, N), dtype=torch.float32, device=q.device) if stream is None
+               else _new((B, Hq, N), torch.float32, q.device, stream))
     _check(out, "out", torch.bfloat16, (B, Hq, N, D))
     _check(lse, "lse", torch.float32, (B, Hq, N))
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -592,9 +597,9 @@ def backward(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = 
     _check(dout, "dout", torch.bfloat16, (B, Hq, N, D))
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    dq = _new(q.shape, q.dtype, q.device, stream) if dq is None else dq
-    dk = _new(k.shape, k.dtype, k.device, stream) if dk is None else dk
-    dv = _new(v.shape, v.dtype, v.device, stream) if dv is None else dv
+    dq = _new_like(q, stream) if dq is None else dq
+    dk = _new_like(k, stream) if dk is None else dk
+    dv = _new_like(v, stream) if dv is None else dv
     _check(dq, "dq", torch.bfloat16, (B, Hq, N, D))
     _check(dk, "dk", torch.bfloat16, (B, Hkv, N, D))
     _check(dv, "dv", torch.bfloat16, (B, Hkv, N, D))
@@ -668,8 +673,12 @@ def forward_fp8(q, k, v, q_descale: float, k_descale: float, v_descale: float, c
     _check(v, "v", f8, (B, Hkv, N, D))
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    out = _new((B, Hq, N, D), torch.bfloat16, q.device, stream) if out is None else out
-    lse = _new((B, Hq, N), torch.float32, q.device, stream) if lse is None else lse
+    if out is None:
+        out = (torch.empty((B, Hq, N, D), dtype=torch.bfloat16, device=q.device) if stream is None
+               else _new((B, Hq, N, D), torch.bfloat16, q.device, stream))
+    if lse is None:
+        lse = (torch.empty((B, Hq, N), dtype=torch.float32, device=q.device) if stream is None
+               else _new((B, Hq, N), torch.float32, q.device, stream))
     _check(out, "out", torch.bfloat16, (B, Hq, N, D))
     _check(lse, "lse", torch.float32, (B, Hq, N))
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -695,8 +704,10 @@ def rope_tables(N: int, D: int, base: float = 10000.0, device=None, stream=None)
     dev = torch.device(device if device is not None else "cuda")
     with torch.cuda.device(dev):
         s = stream if stream is not None else torch.cuda.current_stream(dev)
-        cos_t = _new((N, D // 2), torch.float32, dev, stream)
-        sin_t = _new((N, D // 2), torch.float32, dev, stream)
+        cos_t = (torch.empty((N, D // 2), dtype=torch.float32, device=dev) if stream is None
+                 else _new((N, D // 2), torch.float32, dev, stream))
+        sin_t = (torch.empty((N, D // 2), dtype=torch.float32, device=dev) if stream is None
+                 else _new((N, D // 2), torch.float32, dev, stream))
         st = attn_rope_tables(cos_t.data_ptr(), sin_t.data_ptr(), N, D, base, s.cuda_stream)
     if st != ATTN_OK:
         raise AttnError(st, "attn_rope_tables")
@@ -714,8 +725,8 @@ def rope(q, k, cos_t, sin_t, q_out=None, k_out=None, stream=None):
     _check(k, "k", torch.bfloat16, (B, Hkv, N, D))
     _check(cos_t, "cos_t", torch.float32, (N, D // 2))
     _check(sin_t, "sin_t", torch.float32, (N, D // 2))
-    q_out = _new(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
-    k_out = _new(k.shape, k.dtype, k.device, stream) if k_out is None else k_out
+    q_out = _new_like(q, stream) if q_out is None else q_out
+    k_out = _new_like(k, stream) if k_out is None else k_out
     _check(q_out, "q_out", torch.bfloat16, (B, Hq, N, D))
     _check(k_out, "k_out", torch.bfloat16, (B, Hkv, N, D))
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -739,8 +750,8 @@ def rope_inverse(dq_rot, dk_rot, cos_t, sin_t, dq=None, dk=None, stream=None):
     _check(dk_rot, "dk_rot", torch.bfloat16, (B, Hkv, N, D))
     _check(cos_t, "cos_t", torch.float32, (N, D // 2))
     _check(sin_t, "sin_t", torch.float32, (N, D // 2))
-    dq = _new(dq_rot.shape, dq_rot.dtype, dq_rot.device, stream) if dq is None else dq
-    dk = _new(dk_rot.shape, dk_rot.dtype, dk_rot.device, stream) if dk is None else dk
+    dq = _new_like(dq_rot, stream) if dq is None else dq
+    dk = _new_like(dk_rot, stream) if dk is None else dk
     _check(dq, "dq", torch.bfloat16, (B, Hq, N, D))
     _check(dk, "dk", torch.bfloat16, (B, Hkv, N, D))
     s = stream if stream is not None else torch.cuda.current_stream(dq_rot.device)
@@ -773,9 +784,9 @@ def backward_rope(q, k, v, cos_t, sin_t, o, lse, dout, causal: bool = False, sca
     _check(dout, "dout", torch.bfloat16, (B, Hq, N, D))
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    dq = _new(q.shape, q.dtype, q.device, stream) if dq is None else dq
-    dk = _new(k.shape, k.dtype, k.device, stream) if dk is None else dk
-    dv = _new(v.shape, v.dtype, v.device, stream) if dv is None else dv
+    dq = _new_like(q, stream) if dq is None else dq
+    dk = _new_like(k, stream) if dk is None else dk
+    dv = _new_like(v, stream) if dv is None else dv
     _check(dq, "dq", torch.bfloat16, (B, Hq, N, D))
     _check(dk, "dk", torch.bfloat16, (B, Hkv, N, D))
     _check(dv, "dv", torch.bfloat16, (B, Hkv, N, D))
@@ -808,8 +819,10 @@ def forward_rope(q, k, v, cos_t, sin_t, causal: bool = False, scale: float | Non
     _check(sin_t, "sin_t", torch.float32, (N, D // 2))
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    out = _new(q.shape, q.dtype, q.device, stream) if out is None else out
-    lse = _new((B, Hq, N), torch.float32, q.device, stream) if lse is None else lse
+    out = _new_like(q, stream) if out is None else out
+    if lse is None:
+        lse = (torch.empty((B, Hq, N), dtype=torch.float32, device=q.device) if stream is None
+               else _new((B, Hq, N), torch.float32, q.device, stream))
     _check(out, "out", torch.bfloat16, (B, Hq, N, D))
     _check(lse, "lse", torch.float32, (B, Hq, N))
     s = stream if stream is not None else torch.cuda.current_stream(q.device)
@@ -879,25 +892,20 @@ class _On:
             torch.cuda.set_device(self.before)
 
 
-class _NoBytes(Exception):
-    pass
+_known_bytes: dict = {}
 
 
-@functools.lru_cache(maxsize=4096)
-def _known_workspace_bytes(what: str, device_index: int, *sizes) -> int:
-    n = getattr(lib, what)(*sizes)
-    if n < 0:
-        raise _NoBytes   # refused sizes or a CUDA error: the cache keeps neither
+def _workspace_bytes(*key) -> int:
+    """lib.<what>(*sizes) for key = (what, device index, *sizes) on that device, the current one: a function of the sizes
+    alone, asked once; -1, asked anew each time, where it refuses them or a CUDA call failed."""
+    n = _known_bytes.get(key)
+    if n is None:
+        n = getattr(lib, key[0])(*key[2:])
+        if n >= 0:
+            if len(_known_bytes) >= 4096:
+                _known_bytes.clear()
+            _known_bytes[key] = n
     return n
-
-
-def _workspace_bytes(what: str, device_index: int, *sizes) -> int:
-    """lib.<what>(*sizes) for the current device (device_index), a function of the sizes alone, asked once; -1, each
-    time asked anew, where it refuses them or a CUDA call failed."""
-    try:
-        return _known_workspace_bytes(what, device_index, *sizes)
-    except _NoBytes:
-        return -1
 
 
 def _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, device):
@@ -972,11 +980,13 @@ def cache_read(k_cache, v_cache, block_table, lens, N: int, k_scale=None, v_scal
     s = _raw_stream(stream, dev)
     shape = (B, Hkv, N, D)
     if k_out is None:
-        k_out = _new(shape, torch.bfloat16, dev, stream)
+        k_out = (torch.empty(*shape, dtype=torch.bfloat16, device=dev) if stream is None
+                 else _new(shape, torch.bfloat16, dev, stream))
     else:
         _expect(k_out, "k_out", torch.bfloat16, shape, dev)
     if v_out is None:
-        v_out = _new(shape, torch.bfloat16, dev, stream)
+        v_out = (torch.empty(*shape, dtype=torch.bfloat16, device=dev) if stream is None
+                 else _new(shape, torch.bfloat16, dev, stream))
     else:
         _expect(v_out, "v_out", torch.bfloat16, shape, dev)
     with _On(dev):
@@ -997,11 +1007,12 @@ def _decode_outputs(q, B, D, out, lse, stream):
     dev = q.device
     _expect(q, "q", torch.bfloat16, (B, Hq, T, D), dev)
     if out is None:
-        out = _new(shape, torch.bfloat16, dev, stream)
+        out = torch.empty_like(q) if stream is None else _new(shape, torch.bfloat16, dev, stream)
     else:
         _expect(out, "out", torch.bfloat16, shape, dev)
     if lse is None:
-        lse = _new((B, Hq, T), torch.float32, dev, stream)
+        lse = (torch.empty(B, Hq, T, dtype=torch.float32, device=dev) if stream is None
+               else _new((B, Hq, T), torch.float32, dev, stream))
     else:
         _expect(lse, "lse", torch.float32, (B, Hq, T), dev)
     return Hq, T, out, lse
@@ -1093,11 +1104,12 @@ def forward_cross(q, k, v, k_lens=None, scale: float | None = None, out=None, ls
 
     B, Hq, Hkv, Nq, Nk, D, dev = _cross_checks(q, k, v, k_lens)
     if out is None:
-        out = _new(q.shape, torch.bfloat16, dev, stream)
+        out = torch.empty_like(q) if stream is None else _new(q.shape, torch.bfloat16, dev, stream)
     else:
         _expect(out, "out", torch.bfloat16, (B, Hq, Nq, D), dev)
     if lse is None:
-        lse = _new((B, Hq, Nq), torch.float32, dev, stream)
+        lse = (torch.empty(B, Hq, Nq, dtype=torch.float32, device=dev) if stream is None
+               else _new((B, Hq, Nq), torch.float32, dev, stream))
     else:
         _expect(lse, "lse", torch.float32, (B, Hq, Nq), dev)
     if scale is None:
@@ -1126,9 +1138,9 @@ def backward_cross(q, k, v, o, lse, dout, k_lens=None, scale: float | None = Non
     _expect(o, "o", torch.bfloat16, q_shape, dev)
     _expect(lse, "lse", torch.float32, (B, Hq, Nq), dev)
     _expect(dout, "dout", torch.bfloat16, q_shape, dev)
-    dq = _new(q.shape, q.dtype, q.device, stream) if dq is None else dq
-    dk = _new(k.shape, k.dtype, k.device, stream) if dk is None else dk
-    dv = _new(v.shape, v.dtype, v.device, stream) if dv is None else dv
+    dq = _new_like(q, stream) if dq is None else dq
+    dk = _new_like(k, stream) if dk is None else dk
+    dv = _new_like(v, stream) if dv is None else dv
     _expect(dq, "dq", torch.bfloat16, q_shape, dev)
     _expect(dk, "dk", torch.bfloat16, k_shape, dev)
     _expect(dv, "dv", torch.bfloat16, k_shape, dev)
