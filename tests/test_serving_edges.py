@@ -236,6 +236,38 @@ def test_a_table_far_longer_than_the_sequences(attn, f8):
 
 
 @pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("prefix", [False, True])
+@pytest.mark.parametrize("short", [0, 1, 40, 70])
+def test_the_longest_sequence(attn, f8, prefix, short):
+    """2^31 - 1 positions (less a few), all on one page but for the last, whose position 2^31 - 1 is no key and whose key
+    there would outweigh all others.  Keys are 0 and values 0 or 1: every sum of a part is exact, the joining adds fewer
+    than 1000 of them, and o is the values' mean, rounded to bf16."""
+    page, d, n = 1024, 64, (1 << 31) - 1 - short
+    g = gen(15)
+    k = torch.zeros(2, 1, page, d)
+    v = torch.randint(0, 2, (1, 1, page, d), generator=g).float().repeat(2, 1, 1, 1)
+    k[1, 0, -1] = 16.0
+    counts = ((1 << 21) * v[0, 0].double().sum(0) - v[0, 0, page - 1 - short :].double().sum(0)) / n
+    if short:
+        k[1, 0, -1 - short :] = 16.0
+    dt = torch.float8_e4m3fn if f8 else torch.bfloat16
+    k, v = k.to(dt).cuda(), v.to(dt).cuda()
+    sc = {x: torch.full((2, 1, page), 127, dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu)
+          for x in ("k_scale", "v_scale")} if f8 else {}
+    table = torch.zeros(1 << 21, dtype=torch.int32, device="cuda")
+    table[-1] = 1
+    q = torch.ones(1, 2, 1, d, dtype=torch.bfloat16, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    if prefix:
+        o, lse = attn.forward_shared_prefix(q, k, v, table, n, table[:1].view(1, 1), lens * 0, **sc)
+    else:
+        o, lse = attn.forward_decode(q, k, v, table.view(1, -1), lens, **sc)
+    settled(attn)
+    assert np.all(np.abs(f64(o[0, :, 0]) - counts.numpy()) <= (2.0 ** -8 + 2000 * 2.0 ** -24) * counts.numpy())
+    assert np.all(np.abs(f64(lse) - math.log(n)) <= 2000 * 2.0 ** -24 + 2.0 ** -21 * (1 + math.log(n)))
+
+
+@pytest.mark.parametrize("f8", [False, True])
 def test_outputs_beside_others_are_left_alone(attn, f8):
     """Outputs handed in as parts of larger buffers: nothing outside them is written."""
     c = Cache(55, [90, 0, 17], 1, 96, 16, f8, prefix=50)

@@ -123,8 +123,10 @@ __device__ __forceinline__ int dec_len(const DecParams& p, int b) {
   return (int)max(0LL, min(n, p.cap));
 }
 
+// (Lengths go up to 2^31 - 1: sums with one that may pass it are in 64 bits or unsigned.)
+__device__ __forceinline__ int dec_key_blocks(int len) { return (int)(((long long)len + kDecBlock - 1) / kDecBlock); }
 __device__ __forceinline__ int dec_blocks(const DecParams& p, int len) {
-  return p.whole_units ? 1 : max(1, (int)(((long long)len + kDecBlock - 1) / kDecBlock));
+  return p.whole_units ? 1 : max(1, dec_key_blocks(len));
 }
 
 // Weight of a result with running maximum ml.x and sum ml.y against maximum m (none: 0; NaN stays).
@@ -202,8 +204,7 @@ __device__ __forceinline__ DecLine dec_locate(const DecParams& p, unsigned ctas,
   if (lane == 31) sh[warp] = incl;
   __syncthreads();
   DecLine ln;
-  ln.prefix = p.prefix_len > 0 ? (long long)p.Hkv * p.prefix_row_blocks * dec_places((p.prefix_len + kDecBlock - 1) / kDecBlock)
-                               : 0;
+  ln.prefix = p.prefix_len > 0 ? (long long)p.Hkv * p.prefix_row_blocks * dec_places(dec_key_blocks(p.prefix_len)) : 0;
   long long before = ln.prefix, total = ln.prefix;
 #pragma unroll
   for (int w = 0; w < kDecThreads / 32; ++w) {
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
     if constexpr (kWarp) seq = (int)(x / p.Hkv);
     const bool prefix = !kWarp && seq < 0;
     const int len = prefix ? p.prefix_len : dec_len(p, seq);
-    const int nblk = kWarp ? 1 : prefix ? (len + kDecBlock - 1) / kDecBlock : dec_blocks(p, len);
+    const int nblk = kWarp ? 1 : prefix ? dec_key_blocks(len) : dec_blocks(p, len);
     const int row_blocks = prefix ? p.prefix_row_blocks : p.row_blocks;
     const int rows = prefix ? p.B * p.GT : p.GT;
     const int places = dec_places(nblk);
@@ -489,7 +490,8 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
     // this way's steps: keys key_begin + (kg + ways * n) * kStep
     const int stride = kWarp ? Cfg::kStep : ways * Cfg::kStep;
     const int k_first = kWarp ? 0 : key_begin + kg * Cfg::kStep;
-    const int steps = k_first < key_end ? (key_end - k_first + stride - 1) / stride : 0;
+    const int steps = (uint32_t)k_first < (uint32_t)key_end
+                          ? (int)(((uint32_t)(key_end - k_first) + (uint32_t)stride - 1u) / (uint32_t)stride) : 0;
     // page pg of the unit -> its plane in the tensor maps
     auto plane_of = [&](int pg) -> int {
       const int id = table ? __ldg(table + pg) : seq;
@@ -695,7 +697,7 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
               if constexpr (kF8) s[gr][nt][e] *= kf[e >> 1];
             }
         }
-        const bool tail = k + Cfg::kStep > key_end;
+        const bool tail = (uint32_t)k + Cfg::kStep > (uint32_t)key_end;
         if (tail || k + Cfg::kStep > lim_min) {
 #pragma unroll
           for (int gr = 0; gr < G; ++gr)
@@ -1112,7 +1114,7 @@ __global__ void __launch_bounds__(kDecThreads) attn_decode_join_kernel(const Dec
       });
   };
   if (p.prefix_len > 0) {   // few rows: computed by the same kernel
-    const int pre = dec_places((p.prefix_len + kDecBlock - 1) / kDecBlock);
+    const int pre = dec_places(dec_key_blocks(p.prefix_len));
     const int pr = b * p.GT + i;
     const long long a0 = ((long long)h * p.prefix_row_blocks + pr / p.unit_rows) * pre;
     add_unit(a0, a0 + pre, 1, pr % p.unit_rows);
