@@ -187,6 +187,20 @@ def test_cache_calls_check_their_tensors(paged, f8):
 
 
 @pytest.mark.gpu
+def test_a_prefix_past_32_bits_is_refused():
+    """(The C entry point takes an int: 2^32 + 5 would arrive there as 5.)"""
+    import torch
+
+    page = 1 << 20
+    cache = torch.zeros(1, 1, page, 32, dtype=torch.bfloat16, device="cuda")
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    pre, q = torch.zeros(4097, dtype=torch.int32, device="cuda"), torch.zeros(1, 1, 1, 32, dtype=torch.bfloat16, device="cuda")
+    for n in (1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError, match="prefix_len"):
+            attn.forward_shared_prefix(q, cache, cache, pre, n, table, lens)
+
+
+@pytest.mark.gpu
 def test_cross_calls_check_their_tensors():
     import torch
 

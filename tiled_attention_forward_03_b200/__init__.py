@@ -1059,8 +1059,9 @@ def forward_shared_prefix(q, k_cache, v_cache, prefix_table, prefix_len: int, bl
     B, Hkv, D, num_pages, page, max_pages = _cache_sizes(k_cache, v_cache, block_table, lens, k_scale, v_scale, dev)
     Hq, T, out, lse = _decode_outputs(q, B, D, out, lse, stream)
     _expect(prefix_table, "prefix_table", torch.int32, (prefix_table.numel(),), dev)
-    if prefix_len < 0 or prefix_len > prefix_table.numel() * page:
-        raise ValueError(f"prefix_len {prefix_len} does not fit prefix_table's {prefix_table.numel()} pages of {page}")
+    if prefix_len < 0 or prefix_len > min(prefix_table.numel() * page, 0x7fffffff):
+        raise ValueError(f"prefix_len {prefix_len} does not fit prefix_table's {prefix_table.numel()} pages of {page}, "
+                         "or passes 2^31 - 1")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     s = _raw_stream(stream, dev)
