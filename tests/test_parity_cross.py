@@ -139,6 +139,17 @@ def test_forward_keys_that_are_not_finite(attn, bad, nq, nk, d):
             check(np.where(live, go, 0.0), np.where(live[..., 0], gl, -np.inf), w, d, s, nk)
 
 
+@pytest.mark.parametrize("nq", [1, 200])
+@pytest.mark.parametrize("nk", [1, 64, 70, 300, 5000])
+def test_forward_no_key_is_finite(attn, nq, nk):
+    q, k, v, _ = case(9, 2, 2, 1, nq, nk, 64, None)
+    k[0] = math.nan
+    o, lse = attn.forward_cross(q.cuda(), k.cuda(), v.cuda())
+    settled(attn)
+    assert o[0].isnan().all() and lse[0].isnan().all()
+    check(f64(o[1]), f64(lse[1]), attend(f64(q[1]), f64(k[1]), f64(v[1]), [nk] * nq, 1 / 8), 64, 1 / 8, nk)
+
+
 def backward_bounds(q, k, v, do, n, scale, o, lse):
     """Element-wise tolerances of dq, dk, dv for one batch row, from the roundings of the kernel: P and dS to bf16 (half
     a step, 2^-8, of each), the gradients to bf16, and the given o (bf16) in delta; scores, dP and exponentials in fp32

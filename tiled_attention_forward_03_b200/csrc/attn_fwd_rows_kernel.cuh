@@ -65,7 +65,6 @@ struct RowsCfg {
 };
 
 constexpr int kRowsQueue = 4;   // units in the scheduler's ring
-constexpr int kRowsPoly = 2;    // column pairs of every 8 whose exponentials use the polynomial
 
 template <int D, bool kF8>
 struct RowsSmem {
@@ -220,40 +219,6 @@ ATTN_DEV void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int 
       " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
-}
-
-// Maxima that keep a NaN (max.f32 and fmaxf drop it).
-ATTN_DEV float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-ATTN_DEV float max3_nan(float a, float b, float c) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-// 2^x for a pair on the FMA pipe, as exp2_poly2 but with a degree-5 polynomial (csrc/fit_exp2_poly.py
-// 5: largest relative error 2.4e-7 in fp32).  The degree-3 one is 7e-5 low at the row's maximum,
-// which shows in the LSE of rows with few keys.  (The clamp drops a NaN: the row maximum carries it.)
-ATTN_DEV float2 exp2_poly5(float2 x) {
-  constexpr float kRound = 12582912.0f;
-  x.x = fmaxf(x.x, -125.0f);
-  x.y = fmaxf(x.y, -125.0f);
-  const float2 j = add2(x, make_float2(kRound, kRound));
-  const float2 n = add2(j, make_float2(-kRound, -kRound));
-  const float2 f = fma2(n, make_float2(-1.0f, -1.0f), x);
-  float2 q = fma2(make_float2(0.0013276472454890609f, 0.0013276472454890609f), f,
-                  make_float2(0.009675540961325169f, 0.009675540961325169f));
-  q = fma2(q, f, make_float2(0.05550713092088699f, 0.05550713092088699f));
-  q = fma2(q, f, make_float2(0.24022120237350464f, 0.24022120237350464f));
-  q = fma2(q, f, make_float2(0.6931469440460205f, 0.6931469440460205f));
-  q = fma2(q, f, make_float2(1.0000001192092896f, 1.0000001192092896f));
-  float2 r;
-  r.x = __int_as_float(__float_as_int(q.x) + (__float_as_int(j.x) << 23));
-  r.y = __int_as_float(__float_as_int(q.y) + (__float_as_int(j.y) << 23));
-  return r;
 }
 
 template <int D, bool kF8>
@@ -706,27 +671,24 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
           for (int i = 0; i < 64; ++i)
             if (k0 + i > key_lim) s[i] = -INFINITY;
         }
-        // The maximum keeps a NaN score (a key that is NaN): through m the row's sum, O and LSE are NaN
-        // then, also where the polynomial, which takes it for a small probability, has its column.  (An
-        // infinite score makes them NaN at the end of the unit, as infinity - infinity.)
         float mx[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = max3_nan(s[e], s[4 + e], s[8 + e]);
+        for (int e = 0; e < 4; ++e) mx[e] = max3f(s[e], s[4 + e], s[8 + e]);
 #pragma unroll
         for (int i = 12; i < 60; i += 8) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3_nan(mx[e], s[i + e], s[i + 4 + e]);
+          for (int e = 0; e < 4; ++e) mx[e] = max3f(mx[e], s[i + e], s[i + 4 + e]);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = max_nan(mx[e], s[60 + e]);
-        const float m_new = max_nan(m, max_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3]) * c);
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[60 + e]);
+        const float m_new = fmaxf(m, fmaxf(max3f(mx[0], mx[1], mx[2]), mx[3]) * c);
         // Lazy correction, as in the column-split kernel.
         bool any_rescale = false;
         float alpha = 1.f;
         if (j == w.jb) {
           m = m_new;
         } else {
-          const bool need = !(m_new <= m + kRescaleLog2) && m == m;   // (once for a NaN: O and l stay NaN)
+          const bool need = m_new > m + kRescaleLog2;
           any_rescale = __any_sync(0xffffffffu, need);
           if (need) {
             alpha = ex2_approx(m - m_new);  // 0 while m is still -inf (no key of this half seen yet)
@@ -749,6 +711,9 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
             tmem_st32(t_oh + ch * 32, ov);
           }
         }
+        // All exponentials on the special-function unit (the maximum drops a NaN score, its exponential does not).
+        // A quarter of the columns on the FMA pipe's polynomial, as the column-split kernel has it, lost: B4 Hq32 Nq2048
+        // Nk<=4096 D128 372 us against 359, D96 105 / 101, B8 H32 Nq500 Nk<=1500 D32 66 / 63, D64 41.6 / 41.8.
         const float m_use = (m == -INFINITY) ? 0.f : m;
         {
           const float2 c2 = make_float2(c, c);
@@ -759,13 +724,7 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 64; i += 2) {
             const float2 x = fma2(make_float2(s[i], s[i + 1]), c2, nm2);
-            float2 pr;
-            if (((i >> 1) & 7) < kRowsPoly) {
-              pr = exp2_poly5(x);
-            } else {
-              pr.x = ex2_approx(x.x);
-              pr.y = ex2_approx(x.y);
-            }
+            const float2 pr = make_float2(ex2_approx(x.x), ex2_approx(x.y));
             acc[(i >> 1) & 3] = add2(acc[(i >> 1) & 3], pr);
             pk[i >> 1] = pack_bf16x2(pr.x, pr.y);
           }
