@@ -307,6 +307,20 @@ def test_shared_prefix(attn, f8, d, lens, prefix, hq, hkv, T, page):
     check_decode(attn, c, hq, T, which=None if n <= 5 else [0, 1, 2, n // 2, n - 1])
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("d,hq,T", [(32, 8, 1), (64, 8, 1), (96, 8, 1), (128, 8, 1), (64, 8, 2), (128, 4, 3), (128, 20, 1)])
+def test_shared_prefix_as_a_server_has_it(attn, d, hq, T, f8):
+    """Many short sequences behind a long prefix with a page that is none: several sequences in a 128-row tile (E4M3:
+    converted ahead), the prefix's parts over many CTAs, joined by the warp that has the sequence's own keys (up to 16
+    rows; 20: by the joining kernel)."""
+    lens = [(37 * b) % 97 for b in range(128)]
+    lens[5] = lens[64] = 0
+    c = Cache(36, lens, 1, d, 32, f8, prefix=3001)
+    c.prefix_table[40] = -1
+    assert c.table.shape[1] * 32 == 128
+    check_decode(attn, c, hq, T, which=[0, 1, 5, 17, 64, 126, 127])
+
+
 def test_shared_prefix_of_nothing_is_decode(attn):
     c = Cache(32, [50, 0, 300], 2, 64, 16, False)
     q = bf16(gen(2), 3, 4, 2, 64)
