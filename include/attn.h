@@ -440,9 +440,9 @@ int attn_cache_read(const void* k_cache, const void* v_cache, const void* k_scal
  * are exact in f16; each query row is scaled by a power of two and rounded to f16 (nothing is lost
  * down to 2^-27 of its largest element), and probabilities times 2^(their value's exponent) are
  * rounded to f16.  Deterministic; the split of a sequence over the GPU, and with it the fp32 order of
- * its sums, depends on all the batch's lengths.  Positions at and past lens[b] may hold anything.
- * Those that a token of the call does not see but a later one does must hold finite values (their
- * probability is 0, and 0 * infinity is NaN), as with attn_fwd's causal form.
+ * its sums, depends on all the batch's lengths.  Positions at and past lens[b] may hold anything, and
+ * so may those that only a later token of the call sees: infinities and NaN there reach that token
+ * alone (attn_fwd's causal form wants finite values there).
  */
 int attn_fwd_decode(const void* q, const void* k_cache, const void* v_cache, const void* k_scale, const void* v_scale,
                     const int* block_table, const int* lens, void* o, float* lse, int B, int Hq, int Hkv, int T,

@@ -283,6 +283,52 @@ def test_decode_queries_of_any_size(attn, power):
             check(f64(o[b]), f64(lse[b]), decode_want(c, f64(q[b]), b, scale), 64, scale, c.lens[b])
 
 
+@pytest.mark.parametrize("d", [32, 64, 96, 128])
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("what", ["k", "v", "both"])
+@pytest.mark.parametrize("lens,hq,hkv,T,prefix", [
+    ([5], 2, 2, 5, 0),                        # the first tokens see next to nothing
+    ([300, 3, 77, 128, 1], 4, 2, 4, 0),       # 8 rows; some tokens see nothing
+    ([300, 77], 12, 3, 4, 0),                 # 16
+    ([140, 33, 64], 16, 2, 7, 0),             # 56
+    ([9000, 600], 4, 2, 3, 0),                # split and joined
+    ([40, 0, 3] * 30, 8, 2, 2, 260),          # behind a prefix
+])
+def test_decode_what_later_tokens_hold_stays_theirs(attn, lens, hq, hkv, T, prefix, what, f8, d):
+    """The last tokens' keys and values are not finite (E4M3: marked): tokens before them are as if nothing stood there,
+    those that see them are NaN or infinite where the sum is (a key in every column and in lse, a value in its own
+    columns, a marked value in all)."""
+    c = Cache(46, lens, hkv, d, 16, f8, prefix=prefix)
+    for b, n in enumerate(lens):
+        for p in range(max(0, n - T + 1), n):   # seen by some tokens, not by the first
+            i, row = page_row(c.table[b].tolist(), 16, c.k.shape[0], p)
+            for t, sc, name in ((c.k, c.ks, "k"), (c.v, c.vs, "v")):
+                if what not in (name, "both") or (n - 1 - p) % 3 == 2:
+                    continue
+                if f8:
+                    t[i, 0, row] = 0
+                    sc.view(torch.uint8)[i, 0, row] = 255
+                else:
+                    t[i, 0, row, (p * 5) % d] = (math.nan, math.inf, -math.inf)[p % 3]
+    q = bf16(gen(7), len(lens), hq, T, d)
+    o, lse = run_decode(attn, c, q)
+    s = d ** -0.5
+    for b in range(len(lens)) if len(lens) <= 6 else (0, 1, 2, 45, 89):
+        with np.errstate(invalid="ignore"):
+            want = decode_want(c, f64(q[b]), b, s)
+        got, got_l = f64(o[b]), f64(lse[b])
+        # a score of minus infinity leaves the row as it would be without that key: the oracle's |q k| is no bound there
+        fine = np.isfinite(want[0]).all(-1) & ~np.isnan(want[1]) & np.isfinite(want[3])
+        for h in range(hq):
+            rows = np.nonzero(fine[h])[0]
+            check(got[h : h + 1, rows], got_l[h : h + 1, rows], tuple(w[h : h + 1, rows] for w in want), d, s, lens[b] + prefix)
+        nan = np.isnan(want[1])
+        assert np.isnan(got_l[nan]).all() and np.isnan(got[nan]).all() and not np.isnan(got_l[~nan]).any()
+        ok = np.isfinite(want[0]) & ~nan[..., None]
+        assert np.isfinite(got[ok]).all()
+        assert not np.isfinite(got[~np.isfinite(want[0])]).any()
+
+
 def test_decode_is_deterministic(attn):
     c = Cache(28, [2000, 77, 0, 513], 2, 128, 64, True)
     q = bf16(gen(9), 4, 8, 1, 128)

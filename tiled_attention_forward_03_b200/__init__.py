@@ -1024,7 +1024,8 @@ def forward_decode(q, k_cache, v_cache, block_table, lens, k_scale=None, v_scale
     paged cache (see cache_append), which holds their keys and values already: lens[b] counts them, token t stands at
     position lens[b] - T + t and sees the positions up to its own.  Returns (o bf16, lse fp32 [B, Hq, T]); a row that
     sees nothing has o = 0 and lse = -inf.  Table entries that are no page read as zero keys and values.
-    Positions past lens[b] may hold anything; those that only later tokens of the call see must hold finite values.
+    What a token does not see may hold anything, infinities and NaN included: positions past lens[b], and those of the
+    call's later tokens.
 
     Made for few rows: the cache is read once for each 64 rows (T times the query heads of a KV head)."""
     import torch

@@ -82,6 +82,7 @@ struct DecParams {
   const __nv_bfloat16* q;    // [B][Hkv][GT][D]
   const uint8_t* ks;         // E4M3: exponents [num_pages][Hkv][page]
   const uint8_t* vs;
+  const __nv_bfloat16* v;    // bf16: the values once more, for those that are not finite
   const int* table;          // [B][max_pages], or null: sequence b is page b
   const int* lens;           // [B], or null: len_all
   long long cap;             // max_pages * page: no sequence is longer
@@ -406,6 +407,7 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
   __shared__ long long scratch[16];
   __shared__ uint64_t full[kDecStages], empty[kDecStages];
   __shared__ uint32_t abort_word;
+  __shared__ uint32_t odd_words[4];   // this warp's way met values that are not finite (see the step)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   auto so = reinterpret_cast<float(*)[16][Cfg::kRowStride]>(smem);
   volatile uint32_t* abort_flag = &abort_word;
@@ -415,6 +417,7 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
   const int stages = kDecStages / ways;                 // of this way's ring
   const uint32_t ring = smem_u32(smem) + kg * stages * kDecStageBytes;
   uint8_t* const exps = smem + kDecStages * kDecStageBytes + kg * stages * kDecExpBytes;
+  volatile uint32_t* odd = &odd_words[kg];   // (one way: its row tiles' warps share the stages, and this)
   uint64_t* ring_full = full + kg * stages;
   uint64_t* ring_empty = empty + kg * stages;
   if (threadIdx.x == 0) {
@@ -423,6 +426,7 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
       mbar_init(&empty[i], row_tiles);
     }
     *abort_flag = 0u;
+    for (int i = 0; i < 4; ++i) odd_words[i] = 0u;
     fence_mbar_init();
     if (p.cap > 0 || p.prefix_len > 0) {   // (without any key there are no tensor maps)
       tma_prefetch_desc(&tmap_k);
@@ -635,6 +639,47 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
       if (issuer && n + stages - 1 < steps) ok = issue(n + stages - 1);
       ok = wait_phase(&ring_full[stage], phase, abort_flag, kSiteDecodeFull) && ok;
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      // Keys that a later token of the call sees and an earlier one does not: a value there that is not finite
+      // would reach the earlier one as 0 * NaN.  It is taken out of the stage (E4M3: its mark is), and put in for
+      // the rows that see it behind the last step.  (Done here, where few registers are in use: left to the products'
+      // operands it cost 16 rows 5 to 12 %.  In shared memory, B64 T4 N<=8192 E4M3 takes 206 us instead of 248, B20 T4
+      // N<=2000 bf16 35 instead of 40, the 16-row forms spilling less; T1 B20 N<=2000 E4M3 26.5 instead of 25.8.)
+      if (p.T > 1 && lim_min - k < Cfg::kStep) {
+        const int r0 = max(0, lim_min - k), r1 = min(Cfg::kStep, key_end - k);
+        bool found = false;
+        if constexpr (kF8) {
+          uint8_t* e = exps + stage * kDecExpBytes + 32 + lane;
+          if (lane >= r0 && lane < r1 && *e == kE8Nan) {
+            found = true;
+            *e = 0;   // (codes of 0: any exponent does, and this one is no maximum)
+          }
+        } else {
+          // 16 bytes a lane: an exponent of all ones carries into the sign's place
+          const uint32_t tile = ring + stage * kDecStageBytes + Cfg::kVOff;
+          uint32_t carry = 0u;
+          for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
+#pragma unroll
+            for (int c = 0; c < Cfg::kChunks; ++c) {
+              uint32_t w[4];
+              lds16(w, tile + c * Cfg::kChunkBytes + i * 16);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) carry |= (w[e] & 0x7f807f80u) + 0x00800080u;
+            }
+          found = (carry & 0x80008000u) != 0u;
+          if (__any_sync(0xffffffffu, found)) {
+            uint16_t* x = reinterpret_cast<uint16_t*>(smem + (kg * stages + stage) * kDecStageBytes + Cfg::kVOff);
+            for (int c = 0; c < Cfg::kChunks; ++c)
+              for (int i = r0 * 64 + lane; i < r1 * 64; i += 32)
+                if ((x[c * (Cfg::kChunkBytes / 2) + i] & 0x7f80u) == 0x7f80u) x[c * (Cfg::kChunkBytes / 2) + i] = 0;
+            found = true;
+          }
+        }
+        if (found) {
+          *odd = 1u;
+          fence_proxy_async_smem();   // the stage's next load follows
+        }
+        __syncwarp();
+      }
       if (active) {
         const uint32_t tile_k = ring + stage * kDecStageBytes, tile_v = tile_k + Cfg::kVOff;
         // S^T = K Q^T: keys g and g + 8 of each group, rows 2t and 2t + 1 of each tile.  Even and odd K
@@ -891,6 +936,33 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
         phase ^= 1u;
       }
     }
+    if (!kWarp && __syncthreads_or(!ok)) ok = false;   // all rings are empty (or a wait gave up)
+    if (p.T > 1 && *odd != 0u) {   // rare: the values that were taken out, from the cache
+#pragma unroll 1
+      for (int key = max(key_begin, lim_min); key < key_end; ++key) {
+        if (!kWarp && (key - key_begin) / Cfg::kStep % ways != kg) continue;
+        const Walk at = walk_at(key);
+        const int plane = plane_of(at.pg);
+        if (plane == no_plane) continue;
+        const long long row = (long long)plane * p.page + at.row;
+        if (kF8 && p.vs[row] != kE8Nan) continue;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const float x = kF8 ? __uint_as_float(0x7fffffffu) : __bfloat162float(p.v[row * D + dec_col<D, kF8>(c, g)]);
+          if (fabsf(x) < INFINITY) continue;
+#pragma unroll
+          for (int nt = 0; nt < kN; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (key < lim[nt][e]) o[nt][c / 2][2 * (c & 1) + e] += x;
+        }
+      }
+      if (kWarp) {   // (else before the next unit, below)
+        __syncwarp();
+        if (lane == 0) *odd = 0u;
+        __syncwarp();
+      }
+    }
 #pragma unroll
     for (int nt = 0; nt < kN; ++nt)
 #pragma unroll
@@ -975,11 +1047,7 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
       x += (long long)gridDim.x * 4;
       continue;
     }
-    // all rings are empty: the join may take their place, unless a wait gave up
-    if (__syncthreads_or(!ok)) {
-      ok = false;
-      break;
-    }
+    if (!ok) break;
 
     // ---- join the warps' results, and write the unit out or its part to a slot
 #pragma unroll
@@ -995,6 +1063,7 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
         }
       }
     __syncthreads();
+    if (rt == 0 && lane == 0) *odd = 0u;   // (all warps have read it; the next steps follow the barrier below)
     const bool whole = blk0 == 0 && blk1 == nblk;
     const long long slot = 2LL * blockIdx.x + (x == begin ? 0 : 1);
     const int unit_row = rb * row_tiles * kTile;

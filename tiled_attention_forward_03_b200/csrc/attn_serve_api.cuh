@@ -320,6 +320,7 @@ void fill_decode(attn::DecParams& p, const CacheArgs& a, const void* q, void* o,
   p.q = reinterpret_cast<const __nv_bfloat16*>(q);
   p.ks = static_cast<const uint8_t*>(a.ks);
   p.vs = static_cast<const uint8_t*>(a.vs);
+  p.v = static_cast<const __nv_bfloat16*>(a.v);
   p.table = a.table;
   p.lens = a.lens;
   p.cap = cache_cap(a.page, a.max_pages);
