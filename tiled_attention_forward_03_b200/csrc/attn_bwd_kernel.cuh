@@ -115,15 +115,6 @@ enum : unsigned {
   kSiteBwdSoftAcc = 19,
 };
 
-// 1-D bulk copy global -> shared (16-byte aligned addresses, size a multiple of 16),
-// completion counted on `bar` in bytes.
-ATTN_DEV void bulk_load_1d(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 template <int D, bool kKV>
 struct BwdPlan {
   static_assert(D == 32 || D == 64 || D == 96 || D == 128, "head dim must be 32, 64, 96 or 128");

@@ -140,14 +140,6 @@ __device__ __forceinline__ float dec_lse(float m, float l) {
   return l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.69314718055994530942f;
 }
 
-// 1-D bulk copy global -> shared (16-byte aligned addresses, size a multiple of 16).
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
-
 // The many-row kernel's results for row i of sequence b and head h: n of them, rows `at(k)` of
 // p.many.o and p.many.ml.
 struct DecParts {
@@ -551,8 +543,8 @@ __global__ void __launch_bounds__(kDecThreads, kWarp ? 2 : 3)
           if (iplane[i] != no_plane) {
             const long long at = (long long)iplane[i] * p.page + iw[i].row;
             uint8_t* dst = exps + i_stage * kDecExpBytes + i * p.box;
-            bulk_load(dst, p.ks + at, (uint32_t)p.box, &ring_full[i_stage]);
-            bulk_load(dst + 32, p.vs + at, (uint32_t)p.box, &ring_full[i_stage]);
+            bulk_load_1d(dst, p.ks + at, (uint32_t)p.box, &ring_full[i_stage]);
+            bulk_load_1d(dst + 32, p.vs + at, (uint32_t)p.box, &ring_full[i_stage]);
           }
         }
 #pragma unroll

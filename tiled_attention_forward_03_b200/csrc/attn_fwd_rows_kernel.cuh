@@ -461,8 +461,8 @@ __global__ void __launch_bounds__(RowsCfg<kF8>::kThreads, 1)
           if constexpr (kF8) {
             tma_load_3d(sRaw + ring.stage * Plan::kRawBytes + lane * p.box * D, map, bar, 0, row, plane, pol_kv);
             if (is_page)
-              bulk_load(sExp + ring.stage * kBlockN + lane * p.box,
-                             (is_k ? p.ks : p.vs) + ((long long)plane * p.page + row), (uint32_t)p.box, bar);
+              bulk_load_1d(sExp + ring.stage * kBlockN + lane * p.box,
+                           (is_k ? p.ks : p.vs) + ((long long)plane * p.page + row), (uint32_t)p.box, bar);
           } else {
             uint8_t* dst = sKV + ring.stage * Plan::kTileBytes + lane * p.box * 128;
 #pragma unroll

@@ -75,6 +75,15 @@ ATTN_DEV uint64_t global_timer_ns() {
 
 // ---------------------------------------------------------------- TMA
 
+// 1-D bulk copy global -> shared (16-byte aligned addresses, size a multiple of 16),
+// completion counted on `bar` in bytes.
+ATTN_DEV void bulk_load_1d(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // 3-D tiled bulk tensor load global -> shared, completion counted on `bar` in bytes.
 // c0 is the innermost coordinate (elements), then c1, c2.
 ATTN_DEV void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2,
