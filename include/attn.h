@@ -391,8 +391,9 @@ int attn_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* ls
  * Tables and lengths are read on the device when the kernels run, so captured calls see their
  * values at replay.  A table entry outside [0, num_pages) is no page: nothing is written there, and
  * it reads as zeros.  E4M3 caches: what attn_cache_append never writes (NaN codes; exponent bytes below
- * 7 or in 248..254) may count as any value in the results of the rows that see it.  Host checks and errors as in attn_fwd: ATTN_ERR_INVALID_ARG (null pointers,
- * negative sizes, one scale without the other), ATTN_ERR_MISALIGNED, ATTN_ERR_UNSUPPORTED.
+ * 7 or in 248..254) may count as any value in the results of the rows that see it.
+ * Host checks and errors as in attn_fwd: ATTN_ERR_INVALID_ARG (null pointers, negative sizes, one scale
+ * without the other), ATTN_ERR_MISALIGNED, ATTN_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------------------------ */
 
 /*
@@ -407,7 +408,8 @@ int attn_fwd_fp8(const void* q, const void* k, const void* v, void* o, float* ls
  * magnitude for e = 120, so that the value stays finite in bf16).  A row with an infinity or a NaN
  * is stored as codes 0 with the E8M0 NaN (byte 255) and reads as NaN.
  * Two rows of one call must not have the same place (the table's entries of positions being
- * written are distinct); if they do, either may remain.
+ * written are distinct); if they do, what that place holds then is not specified (it may be parts of
+ * both, and an exponent that is not its codes').
  */
 int attn_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, void* k_scale, void* v_scale,
                       const int* block_table, const int* lens, const int* new_lens, int B, int Hkv, int T, int D,

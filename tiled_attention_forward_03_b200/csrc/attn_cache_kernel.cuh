@@ -18,8 +18,8 @@
 //
 // Both kernels move each byte once and are bound by HBM (short calls by launch and the
 // dependent look-ups lens -> table -> row).  Measured: reading 340 MB of a batch back (B16 Hkv8 N<=4096
-// D128 E4M3 to bf16) 54 us, 6.3 TB/s; appending 57 MB (B4 Hkv8 T<=4096) 17 us, with
-// the quantising's integer work as large as the copy's time.
+// D128 E4M3 to bf16) 57 us, 5.9 TB/s; appending 57 MB (B4 Hkv8 T<=4096) 18 us (20.5 with L2 flushed
+// before), with the quantising's integer work as large as the copy's time.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -76,7 +76,7 @@ __device__ __forceinline__ int e8_of_amax(uint32_t bits) {
 // Appends rows t < new_lens[b] of k, v [B][Hkv][T][D] at positions lens[b] + t.  A group of G lanes
 // takes kRows rows of K and of V (16 bytes a lane and row, all loads issued before any use); a row's
 // largest magnitude is a shuffle over the group.  kRows = 4 where the rows fill the GPU several times
-// over: 57 MB of a quantised prompt batch (B4 Hkv8 T<=4096 D128) take 20.5 us, with one row 22.5;
+// over: 57 MB of a quantised prompt batch (B4 Hkv8 T<=4096 D128) take 20.5 us (L2 flushed), with one row 22.5;
 // T512 10.4 and 8.2.
 template <int D, bool kF8, int kRows>
 __global__ void __launch_bounds__(256) attn_cache_append_kernel(const __nv_bfloat16* __restrict__ k,

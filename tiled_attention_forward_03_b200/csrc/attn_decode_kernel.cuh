@@ -49,11 +49,15 @@
 // kernel) is joined in registers as the unit is written.  Sharing such units among a CTA's warps took
 // three times as long (B128 Hkv8 N<=256 behind a prefix: 37 us), most of it between units.
 //
-// Measured (B200; L2 flushed before each call): B64 Hq32 Hkv8 N<=8192 D128 E4M3 (550 MB) 114 us,
-// 4.8 TB/s; B3 T4 N<=100001 bf16 (820 MB) 167 us, 4.9 TB/s: three quarters of a copy's rate.  What is
-// left is the steps' own latency (conversion, products and exponentials in turn, three warps a
-// scheduler) and the ends of the units; short calls are launches, the look-up of the schedule and one
-// step's latency after another (B1 N500: 14 us).
+// Measured (B200; one call after another, and in brackets with L2 flushed before each): B64 Hq32 Hkv8
+// N<=8192 D128 E4M3 (550 MB) 104 us (116), 5.3 TB/s; B3 T4 N<=100001 bf16 (820 MB) 145 us (159), 5.7 TB/s:
+// 0.8 and 0.87 of a copy's rate.  What is left is the steps' own latency (conversion, products and
+// exponentials in turn, three warps a scheduler) and the ends of the units; short calls are launches, the
+// look-up of the schedule and one step's latency after another (B1 N500: 15 us a call, 12 on the GPU).
+//
+// Registers: 168, for three CTAs an SM.  At that, ptxas spills (bytes stored / loaded): 16 rows at D = 128 12 / 12
+// (bf16) and 360 / 248 (E4M3), at D = 96 24 / 36 and 108 / 116, at D = 64 E4M3 40 / 88; 8 rows of E4M3 60 / 124 at
+// D = 128, 20 / 40 at D = 96; the others nothing.
 //
 // A CTA's four warps take `row_tiles` tiles of 16 rows (1, 2 or 4; or one of 8) and share the keys 4 / row_tiles
 // ways; the warps of one way share its ring (a stage is refilled once all of them have left it).

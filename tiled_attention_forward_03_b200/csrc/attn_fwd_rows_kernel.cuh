@@ -25,9 +25,9 @@
 //    instruction cache (each role computing its own schedule took 130 KB of code, and 20 to 30 % of
 //    the time).
 //
-// Bound by the tensor pipe's feeding: a 128-key block takes 1800 clocks at D = 128 (the products alone
-// 1024), the exponentials and the issue of products in turn.  Measured (B200): B4 Hq32 Hkv8 Nq2048
-// Nk<=4096 D128 310 us, 1000 TFLOP/s; B8 H16 Nq500 Nk<=1500 D64 37 us and 8 us for the joining.
+// Bound by the tensor pipe's feeding: a 128-key block takes about 1650 clocks at D = 128 (the products
+// alone 1024), the exponentials and the issue of products in turn.  Measured (B200): B4 Hq32 Hkv8 Nq2048
+// Nk<=4096 D128 284 us, 1090 TFLOP/s; B8 H16 Nq500 Nk<=1500 D64 37 us and 8 us for the joining.
 //
 //   warps 0-3, 4-7  softmax warpgroups     warp 8   TMA producer     warp 9  MMA issuer
 //   warp 10  output store (cross)          warp 11  scheduler        warps 12-19 (kF8) converters

@@ -106,7 +106,6 @@ void launch_cache_read(const attn::CacheView& c, bool f8, void* k, void* v, int 
 
 // ---------------------------------------------------------------- decode schedule
 
-// Few rows over long keys: how attn_decode_kernel is launched, and its workspace.
 // Launches a kernel that may start before the one before it in the stream has ended (it waits for that
 // end itself, where it reads its results).
 template <typename... P, typename... A>
@@ -129,6 +128,7 @@ struct DecodeDeviceInfo {
   cudaError_t err = cudaSuccess;
 };
 
+// Few rows over long keys: how attn_decode_kernel is launched, and its workspace.
 struct DecPlan {
   int tile_rows;             // rows of a warp: 8 or 16
   int row_tiles, unit_rows, row_blocks, prefix_row_blocks = 0;
@@ -151,11 +151,16 @@ constexpr int kDecCtasPerSm = 3, kDecWarpCtasPerSm = 2;   // resident CTAs (the 
 constexpr int kDecShortBlocks = 8, kDecTinyBlocks = 2;
 // Else a CTA takes whole units where no sequence has more than kDecWholeBlocks blocks, or, with a unit (of
 // up to 8 rows) for each SM and no more than there are CTAs, kDecEvenBlocks (kDecEvenNarrow at D <= 64,
-// where a step has more keys): a launch less, and nothing to join.  Whole units against split ones, in us:
-// bf16 Hkv8 D128 B12 N500 16 / 18, B1 N280 12 / 14, B1 N500 16 / 14, B4 N1000 25 / 16; a unit for each SM, D64 Hkv16
-// B10 N<=1000 16 / 21, B16 N<=1500 22.5 / 25.6, all 1500 27 / 32, N<=3000 35 / 34, D32 Hkv8 B30 N2000 33 / 29;
-// D128, E4M3 Hkv8 B48 N<=1000 27 / 34, bf16 Hkv16 B12 N<=1500 33 / 30, Hkv8 B20 N<=2000 39 / 32; 16 rows, E4M3 B20
-// N<=2000 74 / 46; more units than CTAs, B64 N<=1000 42 / 36.
+// where a step has more keys): a launch less, and nothing to join.  Whole units against split ones, in us on the
+// GPU (Hq32, tables that just fit):
+//   8 blocks: Hkv8 D128 bf16 B1 N384 9.8 / 10.9, N500 11.8 / 11.1, B4 N500 11.7 / 12.2, B12 12.8 / 14.8, E4M3 B1 11.4 /
+//   12.7, B12 11.7 / 15.4, D64 bf16 B1 8.5 / 9.3; 16 rows (Hkv2) B1 N256 11.5 / 14.1, N500 16.4 / 14.5, B24 17.3 / 16.4, B40
+//   17.6 / 19.3; behind the border, B4 N1000 25 / 16;
+//   a unit for each SM: D64 Hkv16 B10 N<=1500 18.1 / 18.4, all 1500 18.4 / 21.0, N<=2000 22.6 / 20.0, all 2000 23.0 / 25.0,
+//   N<=2500 26.4 / 22.1; D32 Hkv8 B30 N<=1500 16.5 / 17.8, N<=2000 19.9 / 19.7; D128 Hkv8 B20 N<=1000 E4M3 19.7 / 20.7, bf16
+//   21.8 / 20.7, N<=1300 22.9 / 22.4 and 26.6 / 23.8, E4M3 B48 N<=1000 22.7 / 27.4;
+//   16 rows, E4M3 B20 N<=2000 74 / 46; more units than CTAs, B64 N<=700 38.0 / 31.7.
+// (The table's width stands for the lengths, which the host does not know: a table wider than the border splits.)
 constexpr int kDecWholeBlocks = 8, kDecEvenBlocks = 16, kDecEvenNarrow = 24;
 
 // `cap`: keys a sequence can have at most.  `shared`: a prefix of `prefix_len` keys comes first;
@@ -493,7 +498,7 @@ struct PrefixPlan {
 };
 
 // An E4M3 prefix is converted to bf16 once, ahead, where at least this many 128-row tiles of each head
-// would convert it themselves and the copy is no larger than this.  Prefix of 16384, Hq32 Hkv8 D128, in us,
+// would convert it themselves and the copy is no larger than this (a bound on the workspace).  Prefix of 16384, Hq32 Hkv8 D128, in us,
 // converted ahead against in the kernel: one tile (B32) 80 / 65, two (B64) 81 / 75, three (B96) 89 / 89, four (B128)
 // 101 / 108, eight (B256) 153 / 187.
 constexpr int kWideTiles = 4;
